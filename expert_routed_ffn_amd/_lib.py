@@ -106,6 +106,22 @@ def _load():
     L.moe_layer_decode_slots.restype = st
     L.moe_layer_decode_slots.argtypes = [ctypes.POINTER(QLayer), vp, i32, vp, vp, i32, i32, i32, vp, i32, vp, vp, vp,
                                          vp, vp, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+    L.moe_balance_loss_workspace_bytes.restype = sz
+    L.moe_balance_loss_workspace_bytes.argtypes = [i32, i32]
+    L.moe_balance_loss.restype = st
+    L.moe_balance_loss.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.moe_route_backward.restype = st
+    L.moe_route_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp]
+    L.moe_combine_backward.restype = st
+    L.moe_combine_backward.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp]
+    L.moe_linear_workspace_bytes.restype = sz
+    L.moe_linear_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+    L.moe_linear.restype = st
+    L.moe_linear.argtypes = [vp, i32, vp, vp, i32, vp, i32, i32, i32, i32, vp, i32, vp, vp, sz, vp]
+    L.moe_linear_backward_workspace_bytes.restype = sz
+    L.moe_linear_backward_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32]
+    L.moe_linear_backward.restype = st
+    L.moe_linear_backward.argtypes = [vp, i32, vp, vp, i32, vp, i32, i32, i32, i32, vp, i32, vp, i32, vp, vp, sz, vp]
     L.moe_profile_next_launch.restype = st
     L.moe_profile_next_launch.argtypes = [i32, vp, vp]
     return L
@@ -165,7 +181,9 @@ def _need(t: torch.Tensor, name: str):
 
 
 KERNELS = {"route": 0, "dispatch": 1, "gemv_gateup": 2, "gemv_down": 3, "mfma_gateup": 4, "mfma_down": 5,
-           "combine": 6, "decode_prep": 7, "router": 8}
+           "combine": 6, "decode_prep": 7, "router": 8, "balance": 9, "route_backward": 10, "combine_backward": 11,
+           "linear": 12, "linear_backward": 13}
+ACTS = {"none": 0, "gelu": 1, "silu": 2, "swiglu": 3}
 
 
 def profile_next_launch(kernel: str, start, stop):
@@ -412,6 +430,238 @@ def layer_decode_slots(table, l: int, layer: ExpertLayer, x: torch.Tensor, logit
 
 def decode_workspace_bytes(layer: ExpertLayer, T: int, k: int) -> int:
     return int(lib.moe_layer_decode_workspace_bytes(ctypes.byref(layer.q), T, k))
+
+
+# ---- training the router and the dense parts beside the experts ------------------------
+
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+
+
+def _arg(t: torch.Tensor, name: str, shape: tuple, dtypes: tuple, device=None):
+    """Checks an argument's shape, type, layout and device; returns its address."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors are on {device}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, dims: int):
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    return t.shape
+
+
+def _ws(ws: torch.Tensor | None, need: int, device):
+    """The caller's workspace, or a new one of `need` bytes: (tensor to keep, address, bytes)."""
+    if ws is None:
+        if need == 0:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _arg(ws, "ws", tuple(ws.shape), (torch.uint8,), device)
+    return ws, ws.data_ptr(), ws.numel()
+
+
+def _launch(fn, device, stream, *args):
+    """One library call on `stream` (or `device`'s current stream) with `device` current."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream, device)))
+    else:
+        _check(fn(*args, _stream(stream, device)))
+
+
+def balance_loss(logits: torch.Tensor, ids: torch.Tensor, mask: torch.Tensor | None = None,
+                 loss: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                 lse: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """moe_balance_loss: (loss [2] fp32, counts [E + 1] int32, lse [T] fp32) of logits [T, E] fp32 routed to ids
+    [T, k]; loss[0] is the balance loss, loss[1] the mean squared log-sum-exp, counts[E] the number of tokens that
+    take part.  mask [T] (bool or uint8) leaves padding out."""
+    T, E = _rows(logits, "logits", 2)
+    k = _rows(ids, "ids", 2)[1]
+    a_logits = _arg(logits, "logits", (T, E), (_F32,))
+    dev = logits.device
+    a_ids = _arg(ids, "ids", (T, k), (_I32,), dev)
+    a_mask = None if mask is None else _arg(mask, "mask", (T,), (torch.bool, torch.uint8), dev)
+    with _on(stream, dev):
+        if loss is None:
+            loss = torch.empty(2, dtype=_F32, device=dev)
+        if counts is None:
+            counts = torch.empty(E + 1, dtype=_I32, device=dev)
+        if lse is None:
+            lse = torch.empty(T, dtype=_F32, device=dev)
+        ws, a_ws, n_ws = _ws(ws, int(lib.moe_balance_loss_workspace_bytes(T, E)), dev)
+    _launch(lib.moe_balance_loss, dev, stream, a_logits, a_ids, a_mask, T, E, k,
+            _arg(loss, "loss", (2,), (_F32,), dev), _arg(counts, "counts", (E + 1,), (_I32,), dev),
+            _arg(lse, "lse", (T,), (_F32,), dev), a_ws, n_ws)
+    return loss, counts, lse
+
+
+def route_backward(logits: torch.Tensor, ids: torch.Tensor, w: torch.Tensor | None = None,
+                   dw: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                   counts: torch.Tensor | None = None, dloss: torch.Tensor | None = None,
+                   dlogits: torch.Tensor | None = None, stream=None):
+    """moe_route_backward: dlogits [T, E] fp32.  w and dw [T, k]: route_topk's gate weights and their gradient
+    (combine_backward).  lse, counts: balance_loss's outputs, dloss [2] fp32 the gradients of its two losses.  Either
+    part may be left out."""
+    T, E = _rows(logits, "logits", 2)
+    k = _rows(ids, "ids", 2)[1]
+    if (w is None) != (dw is None):
+        raise ValueError("w and dw go together")
+    if len({lse is None, counts is None, dloss is None}) != 1:
+        raise ValueError("lse, counts and dloss go together")
+    if w is None and lse is None:
+        raise ValueError("neither gate weights (w, dw) nor losses (lse, counts, dloss)")
+    a_logits = _arg(logits, "logits", (T, E), (_F32,))
+    dev = logits.device
+    a_ids = _arg(ids, "ids", (T, k), (_I32,), dev)
+    a_w = a_dw = a_lse = a_counts = a_dloss = None
+    if w is not None:
+        a_w, a_dw = _arg(w, "w", (T, k), (_F32,), dev), _arg(dw, "dw", (T, k), (_F32,), dev)
+    if lse is not None:
+        a_lse, a_counts = _arg(lse, "lse", (T,), (_F32,), dev), _arg(counts, "counts", (E + 1,), (_I32,), dev)
+        a_dloss = _arg(dloss, "dloss", (2,), (_F32,), dev)
+    if dlogits is None:
+        with _on(stream, dev):
+            dlogits = torch.empty((T, E), dtype=_F32, device=dev)
+    _launch(lib.moe_route_backward, dev, stream, a_logits, a_ids, a_w, a_dw, a_lse, a_counts, a_dloss, T, E, k,
+            _arg(dlogits, "dlogits", (T, E), (_F32,), dev))
+    return dlogits
+
+
+def combine_backward(y: torch.Tensor, w: torch.Tensor, dout: torch.Tensor, dw: torch.Tensor | None = None,
+                     dy: torch.Tensor | None = None, need=("dw", "dy"), stream=None):
+    """moe_combine_backward: (dw [T, k] fp32, dy [T, k, H] of y's type) from dout [T, H]; None for what `need` leaves
+    out.  The gradient of combine's residual is dout itself."""
+    T, k, H = _rows(y, "y", 3)
+    if not need or set(need) - {"dw", "dy"}:
+        raise ValueError('need holds "dw", "dy" or both')
+    a_y = _arg(y, "y", (T, k, H), (_F32, _BF16))
+    dev = y.device
+    a_w, a_dout = _arg(w, "w", (T, k), (_F32,), dev), _arg(dout, "dout", (T, H), (_F32, _BF16), dev)
+    with _on(stream, dev):
+        if "dw" not in need:
+            dw = None
+        elif dw is None:
+            dw = torch.empty((T, k), dtype=_F32, device=dev)
+        if "dy" not in need:
+            dy = None
+        elif dy is None:
+            dy = torch.empty((T, k, H), dtype=y.dtype, device=dev)
+    _launch(lib.moe_combine_backward, dev, stream, a_y, _dtype_code(y), a_w, a_dout, _dtype_code(dout), T, k, H,
+            None if dw is None else _arg(dw, "dw", (T, k), (_F32,), dev),
+            None if dy is None else _arg(dy, "dy", (T, k, H), (y.dtype,), dev))
+    return dw, dy
+
+
+def _act_rows(w: torch.Tensor, act: str):
+    """(activation code, output columns) of weight rows w."""
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, got {act!r}")
+    R = w.shape[0]
+    if act == "swiglu" and R % 2:
+        raise ValueError("swiglu needs an even number of weight rows (gate rows, then up rows)")
+    return ACTS[act], R // 2 if act == "swiglu" else R
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
+           residual: torch.Tensor | None = None, y: torch.Tensor | None = None, y_dtype=None,
+           pre: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """moe_linear: y [T, N] = act(x [T, K] . w [R, K]^T + bias [R]) + residual [T, N].
+
+    w is bf16, x and residual fp32 or bf16, bias fp32, y of y_dtype (x's by default).  act is "none", "gelu" (tanh
+    form), "silu" or "swiglu", whose w holds N gate rows, then N up rows (R = 2 N; else R = N).  `pre` [T, R], of y's
+    type, receives the values before the activation, which linear_backward needs."""
+    T, K = _rows(x, "x", 2)
+    R = _rows(w, "w", 2)[0]
+    code, N = _act_rows(w, act)
+    a_x = _arg(x, "x", (T, K), (_F32, _BF16))
+    dev = x.device
+    a_w = _arg(w, "w", (R, K), (_BF16,), dev)
+    a_bias = None if bias is None else _arg(bias, "bias", (R,), (_F32,), dev)
+    a_res = None if residual is None else _arg(residual, "residual", (T, N), (_F32, _BF16), dev)
+    x_t, r_t = _dtype_code(x), MOE_F32 if residual is None else _dtype_code(residual)
+    with _on(stream, dev):
+        if y is None:
+            y = torch.empty((T, N), dtype=x.dtype if y_dtype is None else y_dtype, device=dev)
+        a_y, y_t = _arg(y, "y", (T, N), (_F32, _BF16), dev), _dtype_code(y)
+        a_pre = None if pre is None else _arg(pre, "pre", (T, R), (y.dtype,), dev)
+        ws, a_ws, n_ws = _ws(ws, int(lib.moe_linear_workspace_bytes(T, K, N, code, x_t, y_t)), dev)
+    _launch(lib.moe_linear, dev, stream, a_x, x_t, a_w, a_bias, code, a_res, r_t, T, K, N, a_y, y_t, a_pre, a_ws, n_ws)
+    return y
+
+
+def linear_workspace_bytes(T: int, K: int, N: int, act: str = "none", x_dtype=torch.bfloat16,
+                           y_dtype=torch.bfloat16) -> int:
+    """Bytes of linear's workspace for N output columns."""
+    t = {_F32: MOE_F32, _BF16: MOE_BF16}
+    return int(lib.moe_linear_workspace_bytes(T, K, N, ACTS[act], t[x_dtype], t[y_dtype]))
+
+
+_NEED = {"dx": 1, "dw": 2, "db": 4}
+
+
+def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str = "none",
+                    pre: torch.Tensor | None = None, need=("dx", "dw", "db"), dx: torch.Tensor | None = None,
+                    dw: torch.Tensor | None = None, db: torch.Tensor | None = None, dx_dtype=None,
+                    dw_dtype=torch.float32, ws: torch.Tensor | None = None, stream=None):
+    """moe_linear_backward: (dx [T, K], dw [R, K], db [R] fp32) of linear(x, w, bias, act), None for what `need`
+    leaves out.  dx is of dx_dtype (x's by default), dw of dw_dtype.  `pre` is what linear wrote there, of dy's type
+    (not needed for act "none").  The residual's gradient is dy itself."""
+    T, K = _rows(x, "x", 2)
+    R = _rows(w, "w", 2)[0]
+    code, N = _act_rows(w, act)
+    if not need or set(need) - set(_NEED):
+        raise ValueError('need holds some of "dx", "dw", "db"')
+    if act != "none" and pre is None:
+        raise ValueError(f"act {act!r} needs pre")
+    a_dy = _arg(dy, "dy", (T, N), (_F32, _BF16))
+    dev = dy.device
+    a_x, a_w = _arg(x, "x", (T, K), (_F32, _BF16), dev), _arg(w, "w", (R, K), (_BF16,), dev)
+    a_pre = None if act == "none" else _arg(pre, "pre", (T, R), (dy.dtype,), dev)
+    bits = 0
+    for n in need:
+        bits |= _NEED[n]
+    dx = None if "dx" not in need else dx
+    dw = None if "dw" not in need else dw
+    db = None if "db" not in need else db
+    a_dx = a_dw = a_db = None
+    dx_t = dw_t = MOE_BF16
+    with _on(stream, dev):
+        if "dx" in need:
+            if dx is None:
+                dx = torch.empty((T, K), dtype=x.dtype if dx_dtype is None else dx_dtype, device=dev)
+            a_dx, dx_t = _arg(dx, "dx", (T, K), (_F32, _BF16), dev), _dtype_code(dx)
+        if "dw" in need:
+            if dw is None:
+                dw = torch.empty((R, K), dtype=dw_dtype, device=dev)
+            a_dw, dw_t = _arg(dw, "dw", (R, K), (_F32, _BF16), dev), _dtype_code(dw)
+        if "db" in need:
+            if db is None:
+                db = torch.empty(R, dtype=_F32, device=dev)
+            a_db = _arg(db, "db", (R,), (_F32,), dev)
+        x_t, dy_t = _dtype_code(x), _dtype_code(dy)
+        ws, a_ws, n_ws = _ws(ws, int(lib.moe_linear_backward_workspace_bytes(T, K, N, code, dy_t, x_t, dx_t, dw_t,
+                                                                             bits)), dev)
+    _launch(lib.moe_linear_backward, dev, stream, a_dy, dy_t, a_pre, a_x, x_t, a_w, code, T, K, N, a_dx, dx_t, a_dw,
+            dw_t, a_db, a_ws, n_ws)
+    return dx, dw, db
+
+
+def linear_backward_workspace_bytes(T: int, K: int, N: int, act: str = "none", dy_dtype=torch.bfloat16,
+                                    x_dtype=torch.bfloat16, dx_dtype=torch.bfloat16, dw_dtype=torch.float32,
+                                    need=("dx", "dw", "db")) -> int:
+    """Bytes of linear_backward's workspace for N output columns."""
+    t = {_F32: MOE_F32, _BF16: MOE_BF16}
+    return int(lib.moe_linear_backward_workspace_bytes(T, K, N, ACTS[act], t[dy_dtype], t[x_dtype], t[dx_dtype],
+                                                       t[dw_dtype], sum(_NEED[n] for n in set(need))))
 
 
 # ---- slot table -------------------------------------------------------------------------

@@ -347,8 +347,145 @@ moe_status moe_combine(const void* y, moe_dtype y_t, const float* w, int T, int 
   return launch_combine(y, y_t, w, T, k, H, residual, r_t, out, out_bf16, stream);
 }
 
+// ---- the trainable parts ----
+
+size_t moe_balance_loss_workspace_bytes(int T, int E) {
+  if (T < 0 || E < 1 || E > kMaxE) return 0;
+  return balance_loss_ws_bytes(T, E);
+}
+
+moe_status moe_balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask, int T, int E, int k,
+                            float* loss, int32_t* counts, float* lse, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (T < 0) return fail(MOE_EINVAL, "moe_balance_loss: T < 0");
+  if (moe_status st = check_ek("moe_balance_loss", E, k)) return st;
+  if ((int64_t)T * k > (int64_t)1 << 24) return fail(MOE_EUNSUPPORTED, "moe_balance_loss: T*k above 2^24");
+  if (!loss || !counts) return fail(MOE_EINVAL, "moe_balance_loss: null pointer");
+  if (T > 0 && (!logits || !ids || !lse)) return fail(MOE_EINVAL, "moe_balance_loss: null pointer");
+  if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(lse, 4) ||
+      !aligned(ws, 16))
+    return fail(MOE_EINVAL, "moe_balance_loss: misaligned buffer");
+  const size_t need = balance_loss_ws_bytes(T, E);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(MOE_EWORKSPACE, fmt("moe_balance_loss: workspace %lld bytes, needs %lld", (long long)ws_bytes,
+                                    (long long)need));
+  return launch_balance_loss(logits, ids, mask, T, E, k, loss, counts, lse, ws, stream);
+}
+
+moe_status moe_route_backward(const float* logits, const int32_t* ids, const float* w, const float* dw,
+                              const float* lse, const int32_t* counts, const float* dloss, int T, int E, int k,
+                              float* dlogits, hipStream_t stream) {
+  if (T < 0) return fail(MOE_EINVAL, "moe_route_backward: T < 0");
+  if (moe_status st = check_ek("moe_route_backward", E, k)) return st;
+  if ((int64_t)T * k > (int64_t)1 << 24) return fail(MOE_EUNSUPPORTED, "moe_route_backward: T*k above 2^24");
+  if (T == 0) return MOE_OK;
+  if (!dlogits) return fail(MOE_EINVAL, "moe_route_backward: null pointer");
+  if ((w == nullptr) != (dw == nullptr)) return fail(MOE_EINVAL, "moe_route_backward: w and dw go together");
+  if ((lse == nullptr) != (counts == nullptr) || (lse == nullptr) != (dloss == nullptr))
+    return fail(MOE_EINVAL, "moe_route_backward: lse, counts and dloss go together");
+  if (!w && !lse) return fail(MOE_EINVAL, "moe_route_backward: neither gate weights nor losses");
+  if ((w && !ids) || (lse && !logits)) return fail(MOE_EINVAL, "moe_route_backward: null pointer");
+  if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(w, 4) || !aligned(dw, 4) || !aligned(lse, 4) ||
+      !aligned(counts, 4) || !aligned(dloss, 4) || !aligned(dlogits, 4))
+    return fail(MOE_EINVAL, "moe_route_backward: misaligned buffer");
+  return launch_route_backward(logits, ids, w, dw, lse, counts, dloss, T, E, k, dlogits, stream);
+}
+
+moe_status moe_combine_backward(const void* y, moe_dtype y_t, const float* w, const void* dout, moe_dtype dout_t,
+                                int T, int k, int H, float* dw, void* dy, hipStream_t stream) {
+  if (T < 0 || H < 1) return fail(MOE_EINVAL, "moe_combine_backward: T < 0 or H < 1");
+  if (k < 1 || k > kMaxK) return fail(MOE_EUNSUPPORTED, "moe_combine_backward: k outside [1, 16]");
+  if (H % 4) return fail(MOE_EUNSUPPORTED, "moe_combine_backward: H must be a multiple of 4");
+  if ((int64_t)T * k > (int64_t)1 << 24) return fail(MOE_EUNSUPPORTED, "moe_combine_backward: T*k above 2^24");
+  if (y_t != MOE_F32 && y_t != MOE_BF16) return fail(MOE_EINVAL, "moe_combine_backward: y dtype");
+  if (dout_t != MOE_F32 && dout_t != MOE_BF16) return fail(MOE_EINVAL, "moe_combine_backward: dout dtype");
+  if (T == 0) return MOE_OK;  // (pointers to no elements may be null)
+  if (!dw && !dy) return fail(MOE_EINVAL, "moe_combine_backward: neither dw nor dy");
+  if (!dout || (dw && !y) || (dy && !w)) return fail(MOE_EINVAL, "moe_combine_backward: null pointer");
+  if (!aligned(y, 16) || !aligned(dy, 16) || !aligned(dout, 16) || !aligned(w, 4) || !aligned(dw, 4))
+    return fail(MOE_EINVAL, "moe_combine_backward: misaligned buffer");
+  return launch_combine_backward(y, y_t, w, dout, dout_t, T, k, H, dw, dy, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int kLinearMaxT = 1 << 20, kLinearMaxN = 16384;
+
+moe_status check_linear(const char* fn, int T, int K, int N, moe_act act) {
+  if (T < 0) return fail(MOE_EINVAL, std::string(fn) + ": T < 0");
+  if (act != MOE_ACT_NONE && act != MOE_ACT_GELU && act != MOE_ACT_SILU && act != MOE_ACT_SWIGLU)
+    return fail(MOE_EINVAL, std::string(fn) + ": activation");
+  if (T > kLinearMaxT) return fail(MOE_EUNSUPPORTED, std::string(fn) + fmt(": T=%lld above 2^20", T));
+  if (K < 32 || K > 16384 || K % 32)
+    return fail(MOE_EUNSUPPORTED, std::string(fn) + fmt(": K=%lld (multiple of 32 in [32, 16384])", K));
+  if (N < 1 || N > kLinearMaxN)
+    return fail(MOE_EUNSUPPORTED, std::string(fn) + fmt(": N=%lld outside [1, 16384]", N));
+  return MOE_OK;
+}
+
+bool is_dtype(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16; }
+uintptr_t elem(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_linear_workspace_bytes(int T, int K, int N, moe_act act, moe_dtype x_t, moe_dtype y_t) {
+  if (T < 1 || K < 1 || N < 1) return 0;
+  return linear_ws_bytes(T, K, N, act, x_t, y_t);
+}
+
+moe_status moe_linear(const void* x, moe_dtype x_t, const void* w, const float* bias, moe_act act,
+                      const void* residual, moe_dtype r_t, int T, int K, int N, void* y, moe_dtype y_t, void* pre,
+                      void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (moe_status st = check_linear("moe_linear", T, K, N, act)) return st;
+  if (!is_dtype(x_t)) return fail(MOE_EINVAL, "moe_linear: x dtype");
+  if (!is_dtype(y_t)) return fail(MOE_EINVAL, "moe_linear: y dtype");
+  if (residual && !is_dtype(r_t)) return fail(MOE_EINVAL, "moe_linear: residual dtype");
+  if (T == 0) return MOE_OK;
+  if (!x || !w || !y) return fail(MOE_EINVAL, "moe_linear: null pointer");
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(ws, 256) || !aligned(bias, 4) || !aligned(y, elem(y_t)) ||
+      !aligned(pre, elem(y_t)) || (residual && !aligned(residual, elem(r_t))))
+    return fail(MOE_EINVAL, "moe_linear: misaligned buffer (x and w need 16 bytes, ws 256)");
+  const size_t need = linear_ws_bytes(T, K, N, act, x_t, y_t);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(MOE_EWORKSPACE, fmt("moe_linear: workspace %lld bytes, needs %lld", (long long)ws_bytes,
+                                    (long long)need));
+  return launch_linear(x, x_t, reinterpret_cast<const uint16_t*>(w), bias, act, residual, r_t, T, K, N, y, y_t, pre, ws,
+                       stream);
+}
+
+size_t moe_linear_backward_workspace_bytes(int T, int K, int N, moe_act act, moe_dtype dy_t, moe_dtype x_t,
+                                           moe_dtype dx_t, moe_dtype dw_t, int need) {
+  if (T < 1 || K < 1 || N < 1) return 0;
+  return linear_backward_ws_bytes(T, K, N, act, dy_t, x_t, dx_t, dw_t, need);
+}
+
+moe_status moe_linear_backward(const void* dy, moe_dtype dy_t, const void* pre, const void* x, moe_dtype x_t,
+                               const void* w, moe_act act, int T, int K, int N, void* dx, moe_dtype dx_t, void* dw,
+                               moe_dtype dw_t, float* db, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (moe_status st = check_linear("moe_linear_backward", T, K, N, act)) return st;
+  if (!is_dtype(dy_t)) return fail(MOE_EINVAL, "moe_linear_backward: dy dtype");
+  if (!is_dtype(x_t)) return fail(MOE_EINVAL, "moe_linear_backward: x dtype");
+  if (!is_dtype(dx_t) || !is_dtype(dw_t)) return fail(MOE_EINVAL, "moe_linear_backward: dx or dw dtype");
+  if (T > 0 && !dx && !dw && !db) return fail(MOE_EINVAL, "moe_linear_backward: no output wanted");
+  if (T > 0 && (!dy || (dw && !x) || (dx && !w) || (act != MOE_ACT_NONE && !pre)))
+    return fail(MOE_EINVAL, "moe_linear_backward: null pointer");
+  if ((dw && !aligned(x, 16)) || (dx && !aligned(w, 16)) || !aligned(ws, 256) || !aligned(dx, 16) || !aligned(dw, 16) ||
+      !aligned(db, 4) || !aligned(dy, elem(dy_t)) || (act != MOE_ACT_NONE && !aligned(pre, elem(dy_t))))
+    return fail(MOE_EINVAL, "moe_linear_backward: misaligned buffer (x, w, dx and dw need 16 bytes, ws 256)");
+  const int bits = (dx ? MOE_NEED_DX : 0) | (dw ? MOE_NEED_DW : 0) | (db ? MOE_NEED_DB : 0);
+  const size_t need = T > 0 ? linear_backward_ws_bytes(T, K, N, act, dy_t, x_t, dx_t, dw_t, bits) : 0;
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(MOE_EWORKSPACE, fmt("moe_linear_backward: workspace %lld bytes, needs %lld", (long long)ws_bytes,
+                                    (long long)need));
+  return launch_linear_backward(dy, dy_t, pre, x, x_t, reinterpret_cast<const uint16_t*>(w), act, T, K, N, dx, dx_t, dw,
+                                dw_t, db, ws, stream);
+}
+
 moe_status moe_profile_next_launch(moe_kernel kernel, hipEvent_t start, hipEvent_t stop) {
-  if ((int)kernel < 0 || (int)kernel > (int)MOE_KERNEL_ROUTER) return fail(MOE_EINVAL, "moe_profile_next_launch: kernel");
+  if ((int)kernel < 0 || (int)kernel > (int)MOE_KERNEL_LINEAR_BACKWARD) return fail(MOE_EINVAL, "moe_profile_next_launch: kernel");
   if (!start || !stop) return fail(MOE_EINVAL, "moe_profile_next_launch: null event");
   ProfileReq& p = profile_req();
   p.kernel = (int)kernel;

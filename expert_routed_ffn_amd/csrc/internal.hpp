@@ -152,6 +152,26 @@ moe_status launch_ffn_mfma(const moe_qlayer& q, const void* x, moe_dtype x_t, in
 moe_status launch_combine(const void* y, moe_dtype y_t, const float* w, int T, int k, int H, const void* residual,
                           moe_dtype r_t, float* out, uint16_t* out_bf16, hipStream_t s);
 
+// ---- the trainable parts: balance loss, router gradient, combine gradient, dense product -----
+
+size_t balance_loss_ws_bytes(int T, int E);
+moe_status launch_balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask, int T, int E, int k,
+                               float* loss, int32_t* counts, float* lse, void* ws, hipStream_t s);
+moe_status launch_route_backward(const float* logits, const int32_t* ids, const float* w, const float* dw,
+                                 const float* lse, const int32_t* counts, const float* dloss, int T, int E, int k,
+                                 float* dlogits, hipStream_t s);
+moe_status launch_combine_backward(const void* y, moe_dtype y_t, const float* w, const void* dout, moe_dtype dout_t,
+                                   int T, int k, int H, float* dw, void* dy, hipStream_t s);
+size_t linear_ws_bytes(int T, int K, int N, int act, moe_dtype x_t, moe_dtype y_t);
+moe_status launch_linear(const void* x, moe_dtype x_t, const uint16_t* w, const float* bias, int act,
+                         const void* residual, moe_dtype r_t, int T, int K, int N, void* y, moe_dtype y_t, void* pre,
+                         void* ws, hipStream_t s);
+size_t linear_backward_ws_bytes(int T, int K, int N, int act, moe_dtype dy_t, moe_dtype x_t, moe_dtype dx_t,
+                                moe_dtype dw_t, int need);
+moe_status launch_linear_backward(const void* dy, moe_dtype dy_t, const void* pre, const void* x, moe_dtype x_t,
+                                  const uint16_t* w, int act, int T, int K, int N, void* dx, moe_dtype dx_t, void* dw,
+                                  moe_dtype dw_t, float* db, void* ws, hipStream_t s);
+
 moe_status launch_fill_i32(int32_t* p, int64_t n, int32_t v, hipStream_t s);
 
 // Pending timing request of moe_profile_next_launch (per host thread).

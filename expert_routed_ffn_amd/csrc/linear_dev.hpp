@@ -1,0 +1,176 @@
+// linear_dev.hpp -- device pieces shared by the dense product and its gradient: bf16 conversions, activations, the
+// epilogue, and the description of one product for the tiled kernel.
+#pragma once
+
+#include "internal.hpp"
+
+namespace moe {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+__device__ __forceinline__ uint16_t f32_to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+__device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
+  return (uint32_t)f32_to_bf16(a) | (uint32_t)f32_to_bf16(b) << 16;
+}
+
+// An fp32 value as a sum of up to three bf16 terms, each the nearest bf16 of what is left: 8 + 8 + 8 significant bits,
+// so three terms hold every finite value of normal size exactly and two hold 16 to 17 bits.  A value that rounds
+// past the largest bf16 is cut instead; infinities and NaN stand in the first term alone.
+__device__ __forceinline__ void bf16_terms(float f, uint16_t (&t)[3]) {
+  uint16_t h = f32_to_bf16(f);
+  const bool finite = (__float_as_uint(f) & 0x7F800000u) != 0x7F800000u;
+  if (finite && (h & 0x7F80u) == 0x7F80u) h = (uint16_t)(__float_as_uint(f) >> 16);
+  t[0] = h;
+  const float r = finite ? f - bf16_to_f32(h) : 0.0f;
+  t[1] = f32_to_bf16(r);
+  t[2] = f32_to_bf16(r - bf16_to_f32(t[1]));
+}
+
+// 1 / (1 + e^-z): z -> -inf gives 0, z -> inf gives 1, NaN stays NaN.
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
+}
+// tanh form of GELU: z (1 + tanh(v)) / 2 = z sigmoid(2 v), v = sqrt(2/pi) (z + 0.044715 z^3).
+constexpr float kGeluA2 = 1.59576912f, kGeluB = 0.044715f;  // 2 sqrt(2/pi)
+__device__ __forceinline__ float gelu_gate(float z) {
+  return sigmoid(kGeluA2 * z * __builtin_fmaf(kGeluB * z, z, 1.0f));
+}
+__device__ __forceinline__ float act_value(int act, float z) {
+  if (act == MOE_ACT_GELU) return z * gelu_gate(z);
+  if (act == MOE_ACT_SILU) return z * sigmoid(z);
+  return z;
+}
+__device__ __forceinline__ float act_slope(int act, float z) {
+  if (act == MOE_ACT_GELU) {
+    const float h = gelu_gate(z);
+    return __builtin_fmaf(z * h * (1.0f - h), kGeluA2 * __builtin_fmaf(3.0f * kGeluB * z, z, 1.0f), h);
+  }
+  if (act == MOE_ACT_SILU) {
+    const float h = sigmoid(z);
+    return h * __builtin_fmaf(z, 1.0f - h, 1.0f);
+  }
+  return 1.0f;
+}
+
+// What becomes of an element z of the product: y = act(z + bias) + residual, z + bias kept in `pre`.
+struct Epi {
+  const float* bias;  // [R] or null
+  const void* res;    // [M x N] or null
+  void* y;            // [M x N]
+  void* pre;          // [M x R] of y's type, or null
+  int N, R;           // output columns; product columns (2 N for SwiGLU, else N)
+  int act;
+  int res_bf16, y_bf16;
+  int vec;            // rows start on 16-byte (fp32) / 8-byte (bf16) boundaries and N % 4 == 0
+};
+
+__device__ __forceinline__ float load_any(const void* p, int bf16, size_t i) {
+  return bf16 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[i]) : reinterpret_cast<const float*>(p)[i];
+}
+__device__ __forceinline__ void store_any(void* p, int bf16, size_t i, float v) {
+  if (bf16) reinterpret_cast<uint16_t*>(p)[i] = f32_to_bf16(v);
+  else reinterpret_cast<float*>(p)[i] = v;
+}
+__device__ __forceinline__ void store4(void* p, int bf16, size_t i, const float (&v)[4]) {
+  if (bf16)
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + i) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
+  else
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// One element; zu is the up value of a SwiGLU pair.
+__device__ __forceinline__ void epi_one(const Epi& e, int m, int n, float z, float zu) {
+  const bool pair = e.act == MOE_ACT_SWIGLU;
+  if (e.bias) {
+    z += e.bias[n];
+    if (pair) zu += e.bias[e.N + n];
+  }
+  if (e.pre) {
+    store_any(e.pre, e.y_bf16, (size_t)m * e.R + n, z);
+    if (pair) store_any(e.pre, e.y_bf16, (size_t)m * e.R + e.N + n, zu);
+  }
+  float v = pair ? z * sigmoid(z) * zu : act_value(e.act, z);
+  const size_t i = (size_t)m * e.N + n;
+  if (e.res) v += load_any(e.res, e.res_bf16, i);
+  store_any(e.y, e.y_bf16, i, v);
+}
+// Columns n .. n + 3 of row m (n % 4 == 0); those at N and past it are left out.
+__device__ __forceinline__ void epi_four(const Epi& e, int m, int n, float (&z)[4], float (&zu)[4]) {
+  if (n >= e.N) return;
+  if (!e.vec) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (n + r < e.N) epi_one(e, m, n + r, z[r], zu[r]);
+    return;
+  }
+  const bool pair = e.act == MOE_ACT_SWIGLU;
+  if (e.bias) {
+    const float4 b = *reinterpret_cast<const float4*>(e.bias + n);
+    z[0] += b.x; z[1] += b.y; z[2] += b.z; z[3] += b.w;
+    if (pair) {
+      const float4 c = *reinterpret_cast<const float4*>(e.bias + e.N + n);
+      zu[0] += c.x; zu[1] += c.y; zu[2] += c.z; zu[3] += c.w;
+    }
+  }
+  if (e.pre) {
+    store4(e.pre, e.y_bf16, (size_t)m * e.R + n, z);
+    if (pair) store4(e.pre, e.y_bf16, (size_t)m * e.R + e.N + n, zu);
+  }
+  float v[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v[r] = pair ? z[r] * sigmoid(z[r]) * zu[r] : act_value(e.act, z[r]);
+  const size_t i = (size_t)m * e.N + n;
+  if (e.res) {
+    if (e.res_bf16) {
+      const uint2 q = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(e.res) + i);
+      v[0] += __uint_as_float(q.x << 16); v[1] += __uint_as_float(q.x & 0xFFFF0000u);
+      v[2] += __uint_as_float(q.y << 16); v[3] += __uint_as_float(q.y & 0xFFFF0000u);
+    } else {
+      const float4 q = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(e.res) + i);
+      v[0] += q.x; v[1] += q.y; v[2] += q.z; v[3] += q.w;
+    }
+  }
+  store4(e.y, e.y_bf16, i, v);
+}
+
+// One product C[m][n] = sum over segments and k of A[m][k] B[n][k], both operands with contiguous k.  A segment names
+// one term plane of each operand (see bf16_terms): planes are `a_plane` / `b_plane` elements apart.
+struct Prob {
+  const uint16_t *A, *B;
+  int64_t a_plane, b_plane;
+  int lda, ldb;            // elements per row
+  int M, R, K;             // C is M x R, K the reduction (multiple of 8)
+  int nseg;
+  uint32_t sa, sb;         // two bits per segment: its plane of A and of B
+  int split;               // parts of the reduction, each a workgroup
+  float* partial;          // [split][M][ldp] when split > 1
+  int ldp;                 // R rounded up to 4
+  Epi epi;
+};
+struct Group {  // up to two products in one launch (two only without SwiGLU)
+  Prob p[2];
+  int blocks0;  // workgroups of the first
+};
+struct Join {  // sums of partials: up to two products, and column sums
+  Prob p[2];
+  int n0, n1;            // workgroups of each product (0: not split)
+  const float* db_part;  // [db_rows][db_n]
+  float* db;
+  int db_rows, db_n;
+};
+
+// K-steps of a product over all its segments.
+__host__ __device__ inline int prob_steps(const Prob& p) { return (p.K + 63) / 64 * p.nseg; }
+// How many parts the reduction of products with `tiles` tiles together is cut into.
+int prob_split(int64_t tiles, int64_t steps);
+int64_t prob_tiles(int M, int N, bool swiglu);
+// Launches the products of a group, then what joins their parts.
+moe_status launch_products(int kid, Group& g, int count, const float* db_part, int db_rows, int db_n, float* db,
+                           hipStream_t s, const char* what);
+// Activations to bf16 term planes [T][K], `terms` of them, `plane` elements apart.
+moe_status launch_terms(const float* x, int64_t n, uint16_t* planes, int64_t plane, int terms, hipStream_t s);
+
+}  // namespace moe

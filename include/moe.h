@@ -362,6 +362,128 @@ moe_status moe_slot_table_resolve_device(moe_slot_table* t, int layer, const int
 void moe_slot_table_destroy(moe_slot_table* t);
 
 /*
+ * Training the router, and the dense parts beside the experts.
+ *
+ * The experts stay as they are; what is tuned is the router and the dense
+ * products around it (a shared expert whose output enters moe_combine as its
+ * residual).  A training step runs moe_linear or moe_router_logits,
+ * moe_route_topk, the experts, moe_combine and moe_balance_loss, then
+ * moe_combine_backward (the gate weights' gradient), moe_route_backward (the
+ * logits') and moe_linear_backward (the router's and the dense weights').
+ * Each call gives the same bits for the same inputs every time.
+ */
+
+/*
+ * moe_balance_loss -- per-expert counts, balance loss and logit-size loss of a batch.
+ * Token t takes part when mask[t] != 0 (mask NULL: every token) and its logits
+ * row has a value above -inf; n is the number of such tokens.  With
+ * p[t] = softmax over all E logits and lse[t] = log sum_e exp(logits[t][e]):
+ *   counts[e] = number of (t, j) with ids[t][j] == e, over tokens that take
+ *               part; ids outside [0, E) are not counted.  counts[E] = n.
+ *   loss[0]   = E / (n^2 k) * sum_e counts[e] * sum_t p[t][e]  (1 when even)
+ *   loss[1]   = 1 / n * sum_t lse[t]^2
+ * Both are 0 when n == 0 (T == 0 among that: loss and counts are then written too).
+ *   logits  [T x E] fp32.  Values of -inf are allowed (probability 0); a NaN
+ *           or +inf in a row that takes part makes both losses NaN.  Rows that
+ *           the mask leaves out may hold anything.
+ *   ids     [T x k] int32.     mask  NULL or [T] bytes.
+ *   loss    [2] fp32 out.      counts [E + 1] int32 out.
+ *   lse     [T] fp32 out; -inf for tokens that take no part.
+ *   ws      moe_balance_loss_workspace_bytes(T, E) bytes (0 for small T), 16-byte aligned.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED (E, k out of range, T*k above 2^24), MOE_EWORKSPACE.
+ */
+size_t moe_balance_loss_workspace_bytes(int T, int E);
+moe_status moe_balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask, int T, int E, int k,
+                            float* loss, int32_t* counts, float* lse, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * moe_route_backward -- gradient of the logits, from the gate weights and from the losses.
+ * dlogits[t] = gate part + loss part, either of which may be left out:
+ *   gate  (w and dw not NULL): w[t][j] * (dw[t][j] - sum_i w[t][i] dw[t][i]) at
+ *         e = ids[t][j] (the gradient of moe_route_topk's w; entries of an
+ *         expert named twice add up, ids outside [0, E) are left out);
+ *   loss  (lse, counts and dloss not NULL; lse and counts as moe_balance_loss
+ *         wrote them, and the same logits): with A = dloss[0] E / (n^2 k),
+ *         p[t][e] * (A (counts[e] - sum_f p[t][f] counts[f]) + 2 dloss[1] / n * lse[t]).
+ * The counts are constants of the gradient.  With the loss part, rows that
+ * took no part (lse == -inf) are zero, their gate part too.
+ *   logits  [T x E] fp32 (may be NULL without the loss part); ids [T x k] int32
+ *           (may be NULL without the gate part).
+ *   w, dw   [T x k] fp32.      dloss [2] fp32: the gradients of loss[0] and loss[1].
+ *   dlogits [T x E] fp32 out; may not overlap the inputs.
+ * Errors: MOE_EINVAL (neither part, half a part, null pointers), MOE_EUNSUPPORTED.
+ */
+moe_status moe_route_backward(const float* logits, const int32_t* ids, const float* w, const float* dw,
+                              const float* lse, const int32_t* counts, const float* dloss, int T, int E, int k,
+                              float* dlogits, hipStream_t stream);
+
+/*
+ * moe_combine_backward -- gradient of moe_combine.
+ *   dw[t][j]    = sum_c dout[t][c] * y[t][j][c], fp32 (NULL: not wanted)
+ *   dy[t][j][c] = w[t][j] * dout[t][c], dtype y_t (NULL: not wanted)
+ * The residual's gradient is dout itself.
+ *   y     [T x k x H], dtype y_t (may be NULL without dw).
+ *   w     [T x k] fp32 (may be NULL without dy).
+ *   dout  [T x H], dtype dout_t.
+ * y, dy and dout must be 16-byte aligned, H a multiple of 4, k in [1, 16].
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED.
+ */
+moe_status moe_combine_backward(const void* y, moe_dtype y_t, const float* w, const void* dout, moe_dtype dout_t,
+                                int T, int k, int H, float* dw, void* dy, hipStream_t stream);
+
+typedef enum moe_act {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_GELU = 1,  /* tanh form: z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  MOE_ACT_SILU = 2,  /* z / (1 + exp(-z)) */
+  MOE_ACT_SWIGLU = 3 /* silu(z[n]) * z[N + n]: w has 2 N rows, the first N of them the gate */
+} moe_act;
+
+/*
+ * moe_linear -- dense product with bias, activation and residual.
+ * z[t][r] = sum_c x[t][c] * w[r][c] + bias[r];  y[t][n] = act(z[t])[n] + residual[t][n].
+ *   x         [T x K], dtype x_t, 16-byte aligned; K % 32 == 0, 32 <= K <= 16384.
+ *   w         [R x K] bf16 bits, 16-byte aligned, finite; R = 2 N for SwiGLU, else N; 1 <= N <= 16384.
+ *   bias      NULL or [R] fp32.
+ *   residual  NULL or [T x N], dtype r_t.
+ *   y         [T x N] out, dtype y_t; may not overlap the inputs, except that y
+ *             may be the residual itself when r_t == y_t.
+ *   pre       NULL or [T x R] out, dtype y_t: z, which moe_linear_backward needs
+ *             for every activation but MOE_ACT_NONE.
+ *   ws        moe_linear_workspace_bytes(T, K, N, act, x_t, y_t) bytes, 256-byte aligned.
+ * Sums in fp32.  fp32 x is used to full precision when y is fp32 or T <= 64; a
+ * bf16 y of more tokens takes x rounded to bf16.  T <= 2^20.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE.
+ */
+size_t moe_linear_workspace_bytes(int T, int K, int N, moe_act act, moe_dtype x_t, moe_dtype y_t);
+moe_status moe_linear(const void* x, moe_dtype x_t, const void* w, const float* bias, moe_act act,
+                      const void* residual, moe_dtype r_t, int T, int K, int N, void* y, moe_dtype y_t, void* pre,
+                      void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* What moe_linear_backward is asked for (the workspace query's `need`). */
+enum { MOE_NEED_DX = 1, MOE_NEED_DW = 2, MOE_NEED_DB = 4 };
+
+/*
+ * moe_linear_backward -- gradient of moe_linear; with dz[t][r] = gradient of z:
+ *   dx[t][c] = sum_r dz[t][r] w[r][c]     dw[r][c] = sum_t dz[t][r] x[t][c]     db[r] = sum_t dz[t][r]
+ * The residual's gradient is dy itself.
+ *   dy   [T x N], dtype dy_t.
+ *   pre  [T x R], dtype dy_t, as moe_linear wrote it (NULL for MOE_ACT_NONE, where it is not read).
+ *   x, w as given to moe_linear (x may be NULL without dw, w without dx).
+ *   dx   NULL or [T x K] out, dtype dx_t.   dw NULL or [R x K] out, dtype dw_t.
+ *   db   NULL or [R] fp32 out.  With T == 0, dw and db are set to zero.
+ *   ws   moe_linear_backward_workspace_bytes(...) bytes, 256-byte aligned, `need`
+ *        the MOE_NEED_* bits of the outputs that are not NULL.
+ * dx and dw must be 16-byte aligned.  Sums in fp32.  An fp32 dx or dw comes from dz (and x) at
+ * full precision; a bf16 one from dz rounded to bf16.
+ * Errors: MOE_EINVAL (no output wanted among that), MOE_EUNSUPPORTED, MOE_EWORKSPACE.
+ */
+size_t moe_linear_backward_workspace_bytes(int T, int K, int N, moe_act act, moe_dtype dy_t, moe_dtype x_t,
+                                           moe_dtype dx_t, moe_dtype dw_t, int need);
+moe_status moe_linear_backward(const void* dy, moe_dtype dy_t, const void* pre, const void* x, moe_dtype x_t,
+                               const void* w, moe_act act, int T, int K, int N, void* dx, moe_dtype dx_t, void* dw,
+                               moe_dtype dw_t, float* db, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
  * Kernel timing hook (for measurement tools; not part of the layer).  The
  * next launch of `kernel` issued by this host thread is made with
  * hipExtLaunchKernel so that `start` and `stop` (created by the caller with
@@ -377,7 +499,12 @@ typedef enum moe_kernel {
   MOE_KERNEL_MFMA_GATEUP = 4,
   MOE_KERNEL_MFMA_DOWN = 5,
   MOE_KERNEL_COMBINE = 6,
-  MOE_KERNEL_ROUTER = 8 /* router projection (GEMV or MFMA) */
+  MOE_KERNEL_ROUTER = 8, /* router projection (GEMV or MFMA) */
+  MOE_KERNEL_BALANCE = 9,           /* balance loss: the pass over the logits */
+  MOE_KERNEL_ROUTE_BACKWARD = 10,   /* gradient of the logits */
+  MOE_KERNEL_COMBINE_BACKWARD = 11,
+  MOE_KERNEL_LINEAR = 12,           /* dense product (few tokens, or tiled) */
+  MOE_KERNEL_LINEAR_BACKWARD = 13   /* the two products of its gradient */
 } moe_kernel;
 moe_status moe_profile_next_launch(moe_kernel kernel, hipEvent_t start, hipEvent_t stop);
 

@@ -1,0 +1,153 @@
+"""Training entry points, without a GPU: bad arguments are refused on the host before anything is enqueued, sizes of
+workspaces follow the sizes of the work, and the binding names what is wrong."""
+import ctypes
+
+import pytest
+import torch
+
+import expert_routed_ffn_amd as m
+from expert_routed_ffn_amd import _lib
+
+L = _lib.lib
+P = ctypes.c_void_p(0x100000)    # never read: every call below is refused, or has no rows
+ODD = ctypes.c_void_p(0x100002)
+F32, BF16 = _lib.MOE_F32, _lib.MOE_BF16
+OK, EINVAL, EUNSUP, EWS = _lib.MOE_OK, _lib.MOE_EINVAL, _lib.MOE_EUNSUPPORTED, _lib.MOE_EWORKSPACE
+
+
+def _loss(logits=P, ids=P, mask=None, T=100, E=8, k=2, loss=P, counts=P, lse=P, ws=P, nb=1 << 24):
+    return int(L.moe_balance_loss(logits, ids, mask, T, E, k, loss, counts, lse, ws, nb, None))
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), EINVAL), (dict(E=0), EUNSUP), (dict(E=1025), EUNSUP), (dict(k=0), EUNSUP), (dict(k=9), EUNSUP),
+    (dict(k=17, E=64), EUNSUP), (dict(T=(1 << 23) + 1), EUNSUP), (dict(loss=None), EINVAL), (dict(counts=None), EINVAL),
+    (dict(logits=None), EINVAL), (dict(ids=None), EINVAL), (dict(lse=None), EINVAL), (dict(logits=ODD), EINVAL),
+    (dict(ws=None), EWS), (dict(nb=0), EWS), (dict(T=0, counts=None), EINVAL)])
+def test_balance_loss_refusals(kw, want):
+    assert _loss(**kw) == want
+    assert b"moe_balance_loss" in L.moe_last_error()
+
+
+def _route(logits=P, ids=P, w=P, dw=P, lse=P, counts=P, dloss=P, T=4, E=8, k=2, out=P):
+    return int(L.moe_route_backward(logits, ids, w, dw, lse, counts, dloss, T, E, k, out, None))
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), EINVAL), (dict(E=2000), EUNSUP), (dict(k=9), EUNSUP), (dict(out=None), EINVAL), (dict(w=None), EINVAL),
+    (dict(dw=None), EINVAL), (dict(lse=None), EINVAL), (dict(counts=None), EINVAL), (dict(dloss=None), EINVAL),
+    (dict(w=None, dw=None, lse=None, counts=None, dloss=None), EINVAL), (dict(ids=None), EINVAL),
+    (dict(logits=None), EINVAL), (dict(out=ODD), EINVAL), (dict(T=(1 << 23) + 1), EUNSUP)])
+def test_route_backward_refusals(kw, want):
+    assert _route(**kw) == want
+    assert b"moe_route_backward" in L.moe_last_error()
+
+
+def test_route_backward_no_rows():
+    assert _route(T=0) == OK
+
+
+def _combine(y=P, y_t=BF16, w=P, dout=P, d_t=F32, T=4, k=2, H=64, dw=P, dy=P):
+    return int(L.moe_combine_backward(y, y_t, w, dout, d_t, T, k, H, dw, dy, None))
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), EINVAL), (dict(H=0), EINVAL), (dict(H=66), EUNSUP), (dict(k=0), EUNSUP), (dict(k=17), EUNSUP),
+    (dict(y_t=5), EINVAL), (dict(d_t=-1), EINVAL), (dict(dw=None, dy=None), EINVAL), (dict(dout=None), EINVAL),
+    (dict(y=None), EINVAL), (dict(w=None), EINVAL), (dict(y=ODD), EINVAL), (dict(dout=ODD), EINVAL),
+    (dict(dy=ODD), EINVAL), (dict(T=(1 << 23) + 1), EUNSUP)])
+def test_combine_backward_refusals(kw, want):
+    assert _combine(**kw) == want
+    assert b"moe_combine_backward" in L.moe_last_error()
+
+
+def test_combine_backward_no_rows():
+    assert _combine(T=0) == OK
+
+
+def _linear(x=P, x_t=BF16, w=P, bias=None, act=0, res=None, r_t=0, T=100, K=64, N=8, y=P, y_t=BF16, pre=None, ws=P,
+            nb=1 << 30):
+    return int(L.moe_linear(x, x_t, w, bias, act, res, r_t, T, K, N, y, y_t, pre, ws, nb, None))
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), EINVAL), (dict(T=(1 << 20) + 1), EUNSUP), (dict(K=48), EUNSUP), (dict(K=0), EUNSUP),
+    (dict(K=16416), EUNSUP), (dict(N=0), EUNSUP), (dict(N=16385), EUNSUP), (dict(act=4), EINVAL), (dict(act=-1), EINVAL),
+    (dict(x_t=2), EINVAL), (dict(y_t=2), EINVAL), (dict(res=P, r_t=3), EINVAL), (dict(x=None), EINVAL),
+    (dict(w=None), EINVAL), (dict(y=None), EINVAL), (dict(x=ODD), EINVAL), (dict(w=ODD), EINVAL),
+    (dict(ws=ODD), EINVAL), (dict(y=ODD, y_t=F32), EINVAL), (dict(bias=ODD), EINVAL),
+    (dict(x_t=F32, y_t=F32, ws=None), EWS), (dict(x_t=F32, y_t=F32, nb=16), EWS)])
+def test_linear_refusals(kw, want):
+    assert _linear(**kw) == want
+    assert b"moe_linear" in L.moe_last_error()
+
+
+def test_linear_no_rows():
+    assert _linear(T=0) == OK
+
+
+def _back(dy=P, dy_t=BF16, pre=P, x=P, x_t=BF16, w=P, act=2, T=100, K=64, N=8, dx=P, dx_t=BF16, dw=P, dw_t=F32, db=P,
+          ws=P, nb=1 << 30):
+    return int(L.moe_linear_backward(dy, dy_t, pre, x, x_t, w, act, T, K, N, dx, dx_t, dw, dw_t, db, ws, nb, None))
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), EINVAL), (dict(T=(1 << 20) + 1), EUNSUP), (dict(K=40), EUNSUP), (dict(N=0), EUNSUP), (dict(act=9), EINVAL),
+    (dict(dy_t=2), EINVAL), (dict(x_t=2), EINVAL), (dict(dx_t=2), EINVAL), (dict(dw_t=2), EINVAL),
+    (dict(dx=None, dw=None, db=None), EINVAL), (dict(dy=None), EINVAL), (dict(pre=None), EINVAL), (dict(x=None), EINVAL),
+    (dict(w=None), EINVAL), (dict(dx=ODD), EINVAL), (dict(dw=ODD), EINVAL), (dict(x=ODD), EINVAL), (dict(w=ODD), EINVAL),
+    (dict(ws=None), EWS), (dict(nb=0), EWS)])
+def test_linear_backward_refusals(kw, want):
+    assert _back(**kw) == want
+    assert b"moe_linear_backward" in L.moe_last_error()
+
+
+def test_linear_backward_no_rows_without_sums():
+    assert _back(T=0, dw=None, db=None) == OK
+
+
+def test_workspaces():
+    assert int(L.moe_balance_loss_workspace_bytes(0, 512)) == 0
+    assert int(L.moe_balance_loss_workspace_bytes(12, 512)) == 0
+    assert int(L.moe_balance_loss_workspace_bytes(8192, 512)) > 0
+    assert int(L.moe_balance_loss_workspace_bytes(8192, 5000)) == 0
+    assert m.linear_workspace_bytes(3, 2048, 512, "swiglu") == 0
+    # fp32 activations of a tiled product become bf16 terms: three for an fp32 result, one for a bf16 one
+    one = m.linear_workspace_bytes(8192, 4096, 4096, "none", torch.float32, torch.bfloat16)
+    three = m.linear_workspace_bytes(8192, 4096, 4096, "none", torch.float32, torch.float32)
+    assert one == 8192 * 4096 * 2 and three == 3 * one
+    every = m.linear_backward_workspace_bytes(333, 544, 201, "gelu")
+    assert every > m.linear_backward_workspace_bytes(333, 544, 201, "gelu", need=("dw",)) > 0
+    assert 0 < m.linear_backward_workspace_bytes(333, 544, 201, "gelu", need=("db",)) < every
+
+
+def _t(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype)
+
+
+BF = torch.bfloat16
+
+
+@pytest.mark.parametrize("call,error,word", [
+    (lambda: m.balance_loss(_t(4), _t(4, 2, dtype=torch.int32)), ValueError, "logits"),
+    (lambda: m.balance_loss(_t(4, 8, dtype=BF), _t(4, 2, dtype=torch.int32)), TypeError, "logits"),
+    (lambda: m.balance_loss(_t(8, 4).t(), _t(4, 2, dtype=torch.int32)), ValueError, "contiguous"),
+    (lambda: m.balance_loss(_t(4, 8), _t(4, 2, dtype=torch.int32)), ValueError, "CUDA"),
+    (lambda: m.route_backward(_t(4, 8), _t(4, 2, dtype=torch.int32)), ValueError, "neither"),
+    (lambda: m.route_backward(_t(4, 8), _t(4, 2, dtype=torch.int32), w=_t(4, 2)), ValueError, "together"),
+    (lambda: m.route_backward(_t(4, 8), _t(4, 2, dtype=torch.int32), lse=_t(4)), ValueError, "together"),
+    (lambda: m.combine_backward(_t(4, 2), _t(4, 2), _t(4, 8)), ValueError, "dimensions"),
+    (lambda: m.combine_backward(_t(4, 2, 8), _t(4, 2), _t(4, 8), need=()), ValueError, "need"),
+    (lambda: m.combine_backward(_t(4, 2, 8), _t(4, 2), _t(4, 8), need=("dz",)), ValueError, "need"),
+    (lambda: m.combine_backward(_t(4, 2, 8, dtype=torch.float16), _t(4, 2), _t(4, 8)), TypeError, "y must be"),
+    (lambda: m.linear(_t(4, 64), _t(8, 64, dtype=BF), act="relu"), ValueError, "act"),
+    (lambda: m.linear(_t(4, 64), _t(7, 64, dtype=BF), act="swiglu"), ValueError, "even"),
+    (lambda: m.linear(_t(4, 64, dtype=torch.float16), _t(8, 64, dtype=BF)), TypeError, "x must be"),
+    (lambda: m.linear(_t(4, 64), _t(8, 64, dtype=BF)), ValueError, "CUDA"),
+    (lambda: m.linear_backward(_t(4, 8), _t(4, 64), _t(8, 64, dtype=BF), act="silu"), ValueError, "pre"),
+    (lambda: m.linear_backward(_t(4, 8), _t(4, 64), _t(8, 64, dtype=BF), need=("dx", "dy")), ValueError, "need"),
+    (lambda: m.linear_backward(_t(4, 9), _t(4, 64), _t(8, 64, dtype=BF)), ValueError, "dy"),
+])
+def test_binding_refusals(call, error, word):
+    with pytest.raises(error, match=word):
+        call()
