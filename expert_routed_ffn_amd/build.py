@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libmoe.so")
 
 SOURCES = ["api.hip", "route_topk.hip", "dispatch.hip", "ffn_gemv.hip", "ffn_mfma.hip", "combine.hip",
            "slot_table.hip", "router.hip", "noalloc.hip", "balance.hip", "combine_grad.hip", "linear.hip",
-           "linear_grad.hip"]
+           "linear_grad.hip", "product.hip"]
 
 ARCH = "gfx950"
 # Packed fp32 VALU ops are disabled for all device code.  Floating-point

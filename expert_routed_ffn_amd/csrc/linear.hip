@@ -2,7 +2,7 @@
 //   z = x W^T + b,  y = act(z) + residual,  SwiGLU: y = silu(z_gate) z_up + residual with W's first N rows the gate.
 //
 // Up to 64 tokens: linear_few_kernel, weights straight from memory into matrix operands, the reduction split over the
-// waves of a workgroup.  More: product_kernel, a tiled product through LDS.  Sums in fp32.  fp32 activations enter
+// waves of a workgroup.  More: the tiled product of product.hip.  Sums in fp32.  fp32 activations enter
 // as bf16 terms (bf16_terms in linear_dev.hpp): three, which hold them exactly, when y is fp32; one, a rounding by at
 // most 2^-9 relative that y's own rounding to bf16 matches, when y is bf16 and the product is tiled.
 #include <algorithm>
@@ -132,230 +132,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(const void* 
   }
 }
 
-// ---- tiled product ------------------------------------------------------------------------
+// ---- more tokens ---------------------------------------------------------------------------
 
-constexpr int kTM = 128, kTN = 128, kBK = 64;  // rows of A, rows of B, K-step
-constexpr int kWM = 2, kWN = 2;                // waves
-constexpr int kThreads = 64 * kWM * kWN;
-constexpr int kFM = kTM / kWM / 32, kFN = kTN / kWN / 32;  // 32 x 32 fragments per wave
-constexpr int kRows = kThreads / 8;                        // tile rows per pass of 16-byte loads
-constexpr int kLA = kTM / kRows, kLB = kTN / kRows;
-constexpr int kLds = std::max(2 * (kTM + kTN) * kBK * 2, kTM * kTN * 4);  // two buffers; then the fp32 tile
-
-// 128-byte LDS rows of 64 bf16; 16-byte chunk c of row r sits at c ^ (r & 7), so that the 8 rows a fragment read
-// takes at one chunk lie in 8 different places.
-__device__ __forceinline__ int lds_at(int row, int chunk) { return row * kBK + ((chunk ^ (row & 7)) * 8); }
-
-// Workgroup number to work item: each of the 8 dies (workgroup b runs on die b % 8) gets one contiguous range of
-// items, so that neighbouring tiles share its L2.
-__device__ __forceinline__ int die_item(int b, int total) {
-  const int per = total >> 3, rem = total & 7, x = b & 7;
-  return x * per + min(x, rem) + (b >> 3);
-}
-
-// Four columns n ... of a part's row, those below N.
-__device__ __forceinline__ void put_part(float* out, int n, int N, int vec, const float (&z)[4]) {
-  if (vec) {
-    if (n < N) *reinterpret_cast<float4*>(out) = make_float4(z[0], z[1], z[2], z[3]);
-  } else {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (n + r < N) out[r] = z[r];
-  }
-}
-
-// PAIR: SwiGLU, whose tiles hold kTN / 2 gate rows of W and the same up rows.
-template <bool PAIR>
-__global__ __launch_bounds__(kThreads, 2) void product_kernel(Group g) {
-  constexpr int kStage = (kTM + kTN) * kBK;  // bf16 values of one buffer
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
-  auto lds_a = [&](int buf) { return reinterpret_cast<uint16_t*>(lds) + buf * kStage; };
-  auto lds_b = [&](int buf) { return reinterpret_cast<uint16_t*>(lds) + buf * kStage + kTM * kBK; };
-  const int which = (int)blockIdx.x >= g.blocks0;
-  const Prob& p = g.p[which];
-  const int b = which ? blockIdx.x - g.blocks0 : blockIdx.x;
-  const int total = which ? gridDim.x - g.blocks0 : g.blocks0;
-  constexpr int cols = PAIR ? kTN / 2 : kTN;  // output columns per tile
-  const int tm = (p.M + kTM - 1) / kTM, tn = (p.epi.N + cols - 1) / cols;
-  const int item = die_item(b, total);
-  const int part = item / (tm * tn);
-  // tiles in bands of 8 row tiles, walked column by column
-  const int tile = item - part * tm * tn;
-  const int band = tile / (8 * tn), in_band = tile - band * 8 * tn;
-  const int band_rows = min(8, tm - band * 8);
-  const int mt = band * 8 + in_band % band_rows, nt = in_band / band_rows;
-  const int m0 = mt * kTM, n0 = nt * cols;
-
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave / kWN, wn = wave % kWN;
-  const int r0 = tid >> 3, ch = tid & 7;
-  // offsets from the tile's first row; rows past the end read the last one and are not stored
-  uint32_t oa[kLA], ob[kLB];
-#pragma unroll
-  for (int i = 0; i < kLA; ++i) oa[i] = (uint32_t)(min(m0 + r0 + kRows * i, p.M - 1) - m0) * p.lda + ch * 8;
-#pragma unroll
-  for (int i = 0; i < kLB; ++i) {
-    const int r = r0 + kRows * i;
-    constexpr int kW = kTN / kWN, kH = kW / 2;  // PAIR: each wave's rows are kH gate rows, then the kH up rows
-    const int n = PAIR ? (r / kW) * kH + r % kH : r;
-    const uint32_t up = PAIR && (r % kW) >= kH ? p.epi.N : 0;
-    ob[i] = (min(n0 + n, p.epi.N - 1) - n0 + up) * (uint32_t)p.ldb + ch * 8;
-  }
-  const int seg_steps = (p.K + kBK - 1) / kBK;
-  const int steps = seg_steps * p.nseg;
-  const int lo = (int)((int64_t)steps * part / p.split), hi = (int)((int64_t)steps * (part + 1) / p.split);
-
-  struct Stage {
-    uint4 a[kLA], b[kLB];
-  };
-  auto load = [&](Stage& st, int step) {
-    const int seg = step / seg_steps, k0 = (step - seg * seg_steps) * kBK;
-    const uint16_t* A = p.A + ((p.sa >> (2 * seg)) & 3) * p.a_plane + (size_t)m0 * p.lda + k0;
-    const uint16_t* B = p.B + ((p.sb >> (2 * seg)) & 3) * p.b_plane + (size_t)n0 * p.ldb + k0;
-    if (k0 + kBK <= p.K) {
-#pragma unroll
-      for (int i = 0; i < kLA; ++i) st.a[i] = *reinterpret_cast<const uint4*>(A + oa[i]);
-#pragma unroll
-      for (int i = 0; i < kLB; ++i) st.b[i] = *reinterpret_cast<const uint4*>(B + ob[i]);
-    } else {
-      const bool in = k0 + ch * 8 < p.K;
-#pragma unroll
-      for (int i = 0; i < kLA; ++i) st.a[i] = in ? *reinterpret_cast<const uint4*>(A + oa[i]) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < kLB; ++i) st.b[i] = in ? *reinterpret_cast<const uint4*>(B + ob[i]) : make_uint4(0, 0, 0, 0);
-    }
-  };
-  auto store = [&](const Stage& st, int buf) {
-#pragma unroll
-    for (int i = 0; i < kLA; ++i) *reinterpret_cast<uint4*>(&lds_a(buf)[lds_at(r0 + kRows * i, ch)]) = st.a[i];
-#pragma unroll
-    for (int i = 0; i < kLB; ++i) *reinterpret_cast<uint4*>(&lds_b(buf)[lds_at(r0 + kRows * i, ch)]) = st.b[i];
-  };
-  f32x16_t acc[kFM][kFN];
-#pragma unroll
-  for (int i = 0; i < kFM; ++i)
-#pragma unroll
-    for (int j = 0; j < kFN; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-  const int fr = lane & 31, fh = lane >> 5;
-  auto mma = [&](int buf) {
-#pragma unroll
-    for (int kk = 0; kk < kBK / 16; ++kk) {
-      bf16x8_t af[kFM], bf[kFN];
-#pragma unroll
-      for (int i = 0; i < kFM; ++i)
-        af[i] = *reinterpret_cast<const bf16x8_t*>(&lds_a(buf)[lds_at((kTM / kWM) * wm + 32 * i + fr, 2 * kk + fh)]);
-#pragma unroll
-      for (int j = 0; j < kFN; ++j)
-        bf[j] = *reinterpret_cast<const bf16x8_t*>(&lds_b(buf)[lds_at((kTN / kWN) * wn + 32 * j + fr, 2 * kk + fh)]);
-#pragma unroll
-      for (int i = 0; i < kFM; ++i)
-#pragma unroll
-        for (int j = 0; j < kFN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
-    }
-  };
-
-  // step s in LDS while step s + 1 waits in registers for the other buffer; loads past the part's end repeat its last
-  if (lo < hi) {
-    Stage st;
-    load(st, lo);
-    store(st, 0);
-    load(st, min(lo + 1, hi - 1));
-    __syncthreads();
-    int buf = 0;
-    for (int s = lo; s < hi; ++s, buf ^= 1) {
-      store(st, buf ^ 1);
-      load(st, min(s + 2, hi - 1));
-      mma(buf);
-      __syncthreads();
-    }
-  }
-
-  // The fp32 tile goes through LDS so that a wave's loads and stores of the epilogue run along rows.  A lane holds
-  // row lane & 31 of A and rows 8 (v / 4) + 4 (lane / 32) + v % 4 of B: 16-byte pieces, piece c of row m at
-  // c ^ (m & 31), so that the 32 rows written at one piece lie in 32 different places.
-  float* tile_c = reinterpret_cast<float*>(lds);
-  constexpr int kPieces = kTN / 4;
-#pragma unroll
-  for (int i = 0; i < kFM; ++i)
-#pragma unroll
-    for (int j = 0; j < kFN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int m = (kTM / kWM) * wm + 32 * i + fr, c = (kTN / kWN / 4) * wn + 8 * j + 2 * q + fh;
-        *reinterpret_cast<float4*>(tile_c + (m * kPieces + (c ^ (m & 31))) * 4) =
-            make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
-      }
-  __syncthreads();
-  constexpr int kOutPieces = cols / 4;
-  const bool split = p.split > 1;
-#pragma unroll 2
-  for (int i = tid; i < kTM * kOutPieces; i += kThreads) {
-    const int r = i / kOutPieces, o = i % kOutPieces;
-    const int m = m0 + r, n = n0 + 4 * o;
-    if (m >= p.M || n >= p.epi.N) continue;
-    constexpr int kH = kTN / kWN / 8;  // pieces of a wave's gate rows
-    const int c = PAIR ? (o / kH) * 2 * kH + o % kH : o;
-    float z[4], zu[4];
-    const float4 q = *reinterpret_cast<const float4*>(tile_c + (r * kPieces + (c ^ (r & 31))) * 4);
-    z[0] = q.x; z[1] = q.y; z[2] = q.z; z[3] = q.w;
-    if constexpr (PAIR) {
-      const float4 u = *reinterpret_cast<const float4*>(tile_c + (r * kPieces + ((c + kH) ^ (r & 31))) * 4);
-      zu[0] = u.x; zu[1] = u.y; zu[2] = u.z; zu[3] = u.w;
-    }
-    if (split) {
-      float* out = p.partial + ((size_t)part * p.M + m) * p.ldp + n;
-      put_part(out, n, p.epi.N, p.epi.vec, z);
-      if constexpr (PAIR) put_part(out + p.epi.N, n, p.epi.N, p.epi.vec, zu);
-    } else {
-      epi_four(p.epi, m, n, z, zu);
-    }
-  }
-}
-
-// Adds the parts of split products in part order and applies their epilogue; the workgroups after those add the
-// column sums' parts.  Four columns per thread.
-__global__ __launch_bounds__(256) void join_kernel(Join jn) {
-  int b = blockIdx.x;
-  if (b < jn.n0 + jn.n1) {
-    const Prob& p = jn.p[b >= jn.n0];
-    if (b >= jn.n0) b -= jn.n0;
-    const int quads = (p.epi.N + 3) >> 2;
-    const int64_t i = (int64_t)b * 256 + threadIdx.x;
-    if (i >= (int64_t)p.M * quads) return;
-    const int m = (int)(i / quads), n = (int)(i - (int64_t)m * quads) * 4;
-    const bool pair = p.epi.act == MOE_ACT_SWIGLU;
-    float z[4] = {0.f, 0.f, 0.f, 0.f}, zu[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < p.split; ++s) {
-      const float* in = p.partial + ((size_t)s * p.M + m) * p.ldp + n;
-      if (p.epi.vec) {
-        const float4 q = *reinterpret_cast<const float4*>(in);
-        z[0] += q.x; z[1] += q.y; z[2] += q.z; z[3] += q.w;
-        if (pair) {
-          const float4 u = *reinterpret_cast<const float4*>(in + p.epi.N);
-          zu[0] += u.x; zu[1] += u.y; zu[2] += u.z; zu[3] += u.w;
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (n + r < p.epi.N) {
-            z[r] += in[r];
-            if (pair) zu[r] += in[p.epi.N + r];
-          }
-      }
-    }
-    epi_four(p.epi, m, n, z, zu);
-    return;
-  }
-  const int c = (b - jn.n0 - jn.n1) * 256 + threadIdx.x;
-  if (c >= jn.db_n) return;
-  float v = 0.0f;
-  for (int r = 0; r < jn.db_rows; ++r) v += jn.db_part[(size_t)r * jn.db_n + c];
-  jn.db[c] = v;
-}
-
+// fp32 activations to bf16 term planes, `plane` elements apart.
 __global__ __launch_bounds__(256) void terms_kernel(const float* __restrict__ x, int64_t n4, uint16_t* __restrict__ planes,
                                                     int64_t plane, int terms) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
@@ -376,7 +155,8 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct LinearPlan {
   bool few;
-  int terms, split;
+  int terms;
+  Plan plan;
   size_t planes, partial, bytes;  // offsets and size of the workspace
   int R, ldp;
 };
@@ -387,60 +167,18 @@ LinearPlan linear_plan(int T, int K, int N, int act, moe_dtype x_t, moe_dtype y_
   p.few = T <= kFewT;
   if (p.few) return p;
   p.terms = x_t == MOE_BF16 ? 1 : y_t == MOE_F32 ? 3 : 1;
-  p.split = prob_split(prob_tiles(T, N, act == MOE_ACT_SWIGLU), ceil_div(K, kBK) * p.terms);
+  const Shape shape{T, p.R, K, p.terms};
+  p.plan = plan_products(&shape, 1);
   size_t o = 0;
   p.planes = o;
   if (x_t == MOE_F32) o = up256(o + (size_t)p.terms * T * K * 2);
   p.partial = o;
-  if (p.split > 1) o = up256(o + (size_t)p.split * T * p.ldp * 4);
+  if (p.plan.split[0] > 1) o = up256(o + (size_t)p.plan.split[0] * T * p.ldp * 4);
   p.bytes = o;
   return p;
 }
 
-bool epi_vec(const Epi& e) {
-  auto ok = [](const void* q, int bf16) { return reinterpret_cast<uintptr_t>(q) % (bf16 ? 8 : 16) == 0; };
-  return e.N % 4 == 0 && ok(e.y, e.y_bf16) && ok(e.pre, e.y_bf16) && ok(e.res, e.res_bf16) && ok(e.bias, 0);
-}
-
 }  // namespace
-
-int64_t prob_tiles(int M, int N, bool swiglu) { return ceil_div(M, kTM) * ceil_div(N, swiglu ? kTN / 2 : kTN); }
-
-int prob_split(int64_t tiles, int64_t steps) {
-  const int64_t want = 512 / std::max<int64_t>(tiles, 1);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, steps / 4, 16}));
-}
-
-moe_status launch_products(int kid, Group& g, int count, const float* db_part, int db_rows, int db_n, float* db,
-                           hipStream_t s, const char* what) {
-  int64_t blocks[2] = {0, 0};
-  Join j{};
-  for (int i = 0; i < count; ++i) {
-    Prob& p = g.p[i];
-    p.epi.vec = epi_vec(p.epi);
-    blocks[i] = prob_tiles(p.M, p.epi.N, p.epi.act == MOE_ACT_SWIGLU) * p.split;
-    j.p[i] = p;
-    if (p.split > 1) (i ? j.n1 : j.n0) = (int)ceil_div((int64_t)p.M * ((p.epi.N + 3) / 4), 256);
-  }
-  if (blocks[0] + blocks[1] > 0x7FFFFFFF) return fail(MOE_EUNSUPPORTED, std::string(what) + ": too many tiles");
-  g.blocks0 = (int)blocks[0];
-  if (count > 0) {
-    const dim3 grid((unsigned)(blocks[0] + blocks[1]));
-    if (g.p[0].epi.act == MOE_ACT_SWIGLU) launch_k(kid, product_kernel<true>, grid, dim3(kThreads), 0, s, g);
-    else launch_k(kid, product_kernel<false>, grid, dim3(kThreads), 0, s, g);
-    if (moe_status st = check_launch(what)) return st;
-  }
-  j.db_part = db_part;
-  j.db = db;
-  j.db_rows = db_rows;
-  j.db_n = db ? db_n : 0;
-  const int64_t jb = (int64_t)j.n0 + j.n1 + ceil_div(j.db_n, 256);
-  if (jb > 0) {
-    join_kernel<<<dim3((unsigned)jb), 256, 0, s>>>(j);
-    return check_launch(what);
-  }
-  return MOE_OK;
-}
 
 moe_status launch_terms(const float* x, int64_t n, uint16_t* planes, int64_t plane, int terms, hipStream_t s) {
   const int64_t n4 = n / 4;
@@ -467,8 +205,7 @@ moe_status launch_linear(const void* x, moe_dtype x_t, const uint16_t* w, const 
     return check_launch("linear");
   }
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
-  Group g{};
-  Prob& p = g.p[0];
+  Prob p{};
   p.A = reinterpret_cast<const uint16_t*>(x);
   if (x_t == MOE_F32) {
     uint16_t* planes = reinterpret_cast<uint16_t*>(base + pl.planes);
@@ -485,11 +222,11 @@ moe_status launch_linear(const void* x, moe_dtype x_t, const uint16_t* w, const 
   p.nseg = pl.terms;
   p.sa = 0 | 1u << 2 | 2u << 4;
   p.sb = 0;
-  p.split = pl.split;
+  p.split = pl.plan.split[0];
   p.partial = reinterpret_cast<float*>(base + pl.partial);
   p.ldp = pl.ldp;
   p.epi = e;
-  return launch_products(MOE_KERNEL_LINEAR, g, 1, nullptr, 0, 0, nullptr, s, "linear");
+  return launch_products(MOE_KERNEL_LINEAR, pl.plan, &p, 1, false, false, nullptr, 0, 0, nullptr, s, "linear");
 }
 
 }  // namespace moe

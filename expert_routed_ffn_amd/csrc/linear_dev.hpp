@@ -136,23 +136,20 @@ __device__ __forceinline__ void epi_four(const Epi& e, int m, int n, float (&z)[
   store4(e.y, e.y_bf16, i, v);
 }
 
-// One product C[m][n] = sum over segments and k of A[m][k] B[n][k], both operands with contiguous k.  A segment names
-// one term plane of each operand (see bf16_terms): planes are `a_plane` / `b_plane` elements apart.
+// One product C[m][n] = sum over segments and k of A(m, k) B(n, k); which operand lies [index][k] and which [k][index]
+// is the kernel's.  A segment names one term plane of each operand (see bf16_terms): planes are `a_plane` / `b_plane`
+// elements apart.
 struct Prob {
   const uint16_t *A, *B;
   int64_t a_plane, b_plane;
-  int lda, ldb;            // elements per row
-  int M, R, K;             // C is M x R, K the reduction (multiple of 8)
+  int lda, ldb;            // elements per stored row, multiples of 8
+  int M, R, K;             // C is M x R, K the reduction (a multiple of 8 where an operand is [index][k])
   int nseg;
   uint32_t sa, sb;         // two bits per segment: its plane of A and of B
   int split;               // parts of the reduction, each a workgroup
   float* partial;          // [split][M][ldp] when split > 1
   int ldp;                 // R rounded up to 4
   Epi epi;
-};
-struct Group {  // up to two products in one launch (two only without SwiGLU)
-  Prob p[2];
-  int blocks0;  // workgroups of the first
 };
 struct Join {  // sums of partials: up to two products, and column sums
   Prob p[2];
@@ -162,15 +159,18 @@ struct Join {  // sums of partials: up to two products, and column sums
   int db_rows, db_n;
 };
 
-// K-steps of a product over all its segments.
-__host__ __device__ inline int prob_steps(const Prob& p) { return (p.K + 63) / 64 * p.nseg; }
-// How many parts the reduction of products with `tiles` tiles together is cut into.
-int prob_split(int64_t tiles, int64_t steps);
-int64_t prob_tiles(int M, int N, bool swiglu);
-// Launches the products of a group, then what joins their parts.
-moe_status launch_products(int kid, Group& g, int count, const float* db_part, int db_rows, int db_n, float* db,
-                           hipStream_t s, const char* what);
-// Activations to bf16 term planes [T][K], `terms` of them, `plane` elements apart.
-moe_status launch_terms(const float* x, int64_t n, uint16_t* planes, int64_t plane, int terms, hipStream_t s);
+// Sizes of a product, and how a launch of up to two cuts them.
+struct Shape {
+  int M, R, K, nseg;
+};
+struct Plan {
+  int large;     // 256 x 256 tiles
+  int split[2];
+};
+Plan plan_products(const Shape* s, int count);
+// Launches a forward product (`grad` false, count = 1) or the gradient's (dW first where both are there), then what
+// joins their parts and adds db's.
+moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool grad, bool first_is_dw,
+                           const float* db_part, int db_rows, int db_n, float* db, hipStream_t s, const char* what);
 
 }  // namespace moe

@@ -1,0 +1,466 @@
+// product.hip -- the tiled bf16 product behind the dense product and its gradient:
+//   C[m][n] = sum_k A(m, k) B(n, k),  fp32 sums,  then the epilogue of linear_dev.hpp
+// Either operand lies with k contiguous ([m][k]) or with its own index contiguous ([k][m]): the forward product reads
+// x and W as they are, dx = dz W and dW = dz^T x read W, dz and x in the second form, so no operand is transposed in
+// memory.
+//
+// v_mfma_f32_16x16x32_bf16 with B's rows first, so a lane holds four consecutive columns of C.  16 x 16 fragments
+// measured 10% faster than 32 x 32 ones in the same kernel (36.5 against 40.5 us on 8192 x 2048 x 1024, 224 against
+// 241 us on 8192 x 4096 x 4096).  Tiles go from memory straight to LDS (16 bytes a lane, two buffers of 64 k), and
+// the step's loop is turned so that neither the loads nor the LDS reads are waited for with the matrix units idle:
+// fragments of one 32-k half are read while the other half is multiplied, and the barrier that hands over the buffers
+// stands before the last half's products.  Memory latency behind deeper rings (3 or 4 buffers of 32 k) measured no
+// better.
+//
+// LDS places: 64 banks of 4 bytes serve 16 lanes of a 16-byte read at once.  [m][k] tiles are rows of 128 bytes whose
+// 16-byte piece c lies at c ^ (row / 2 % 8): the 16 rows that such a group reads at one piece fall on 16 different
+// places (with row % 8 they fell on 8, and half of all LDS cycles were conflicts).  [k][m] tiles are read with
+// ds_read_b64_tr_b16, where 16 lanes take 4 k of 16 columns and each receives its column's 4 values; the 32-byte
+// stretch s of row k lies at s ^ (k % 4 + 4 (k / 8 % 2)), which spreads the 8 rows that 32 lanes touch over 256 bytes.
+//
+// Two tile shapes.  256 x 256 (8 waves, 128 KB of LDS, one workgroup per CU) reads half as much per product as
+// 128 x 128 (4 waves, two workgroups per CU), but needs enough tiles to fill 256 CUs evenly: see pick_tile.
+#include <algorithm>
+
+#include "linear_dev.hpp"
+
+namespace moe {
+namespace {
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+constexpr int kBK = 64;
+
+template <int TM_, int TN_, int WM_, int WN_>
+struct Tile {
+  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_;
+  static constexpr int kThreads = 64 * WM * WN;
+  static constexpr int kFM = TM / WM / 16, kFN = TN / WN / 16;  // 16 x 16 fragments per wave
+  static constexpr int kStage = (TM + TN) * kBK;                // bf16 values of one buffer
+  static constexpr int kBuffers = 2 * kStage * 2;               // bytes
+  // the fp32 tile passes through the same LDS, in one piece or by rows of waves
+  static constexpr int kPasses = TM * TN * 4 <= 64 * 1024 ? 1 : WM;
+  static constexpr int kLds = std::max(kBuffers, TM * TN * 4 / kPasses);
+};
+using Small = Tile<128, 128, 2, 2>;
+using Large = Tile<256, 256, 2, 4>;
+static_assert(Small::kLds <= 80 * 1024 && Large::kLds <= 160 * 1024, "LDS of a CU");
+
+// Workgroup number to work item: each of the 8 dies (workgroup b runs on die b % 8) gets one contiguous range of
+// items, so that neighbouring tiles share its L2.
+__device__ __forceinline__ int die_item(int b, int total) {
+  const int per = total >> 3, rem = total & 7, x = b & 7;
+  return x * per + min(x, rem) + (b >> 3);
+}
+
+__device__ __forceinline__ void to_lds16(const uint16_t* g, uint16_t* l) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)g,
+                                   (__attribute__((address_space(3))) uint32_t*)l, 16, 0, 0);
+}
+
+// Loader and reader of one operand's tile: ROWS indices (m or n) by 64 k.
+template <int ROWS, int THREADS, bool KROWS>
+struct Operand;
+
+template <int ROWS, int THREADS>
+struct Operand<ROWS, THREADS, false> {  // [m][k]
+  static constexpr int kPer = THREADS / 8, kLoads = ROWS / kPer;
+  uint32_t off[kLoads];  // from the tile's first row
+  int chunk;             // which 16 bytes of a row this thread brings
+  // `row(i)` is the source row, relative to the tile's first, of tile row i
+  template <typename Row>
+  __device__ __forceinline__ void init(int ld, int, Row row) {
+    const int r = threadIdx.x >> 3;
+    chunk = (threadIdx.x & 7) ^ ((r >> 1) & 7);  // kPer is a multiple of 16: the same for each load
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) off[i] = (uint32_t)row(r + kPer * i) * ld + chunk * 8;
+  }
+  __device__ __forceinline__ const uint16_t* at(const uint16_t* p, size_t first, int k0, int ld) const {
+    return p + first * ld + k0;
+  }
+  __device__ __forceinline__ void load(const uint16_t* p, int, uint16_t* lds) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) to_lds16(p + off[i], lds + (i * THREADS + (threadIdx.x & ~63)) * 8);
+  }
+  // the last step of a reduction that is no multiple of 64: `left` k are there, the others become zeros
+  __device__ __forceinline__ void load_tail(const uint16_t* p, int, int left, uint16_t* lds) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint4 v = chunk * 8 < left ? *reinterpret_cast<const uint4*>(p + off[i]) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(lds + (i * THREADS + threadIdx.x) * 8) = v;
+    }
+  }
+  template <int F>
+  __device__ __forceinline__ void read(const uint16_t* lds, int base, int kk, bf16x8_t (&f)[F]) const {
+    const int r16 = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+      const int row = base + 16 * i + r16;
+      f[i] = *reinterpret_cast<const bf16x8_t*>(lds + row * kBK + (((4 * kk + q) ^ ((row >> 1) & 7)) * 8));
+    }
+  }
+};
+
+template <int ROWS, int THREADS>
+struct Operand<ROWS, THREADS, true> {  // [k][m]
+  static constexpr int kSlots = ROWS / 8, kPer = THREADS / kSlots, kLoads = kBK / kPer;  // 16-byte pieces of a row; k per load
+  uint32_t off;
+  template <typename Row>
+  __device__ __forceinline__ void init(int ld, int cols, Row) {
+    const int k = threadIdx.x / kSlots, s = threadIdx.x % kSlots;
+    const int c = s ^ (((k & 3) | ((k >> 1) & 4)) << 1);  // kPer is a multiple of 16: the same for each load
+    // `cols` columns are there from the tile's first on (a multiple of 8); further ones repeat the last and are not stored
+    off = (uint32_t)k * ld + min(c * 8, cols - 8);
+  }
+  __device__ __forceinline__ const uint16_t* at(const uint16_t* p, size_t first, int k0, int ld) const {
+    return p + (size_t)k0 * ld + first;
+  }
+  __device__ __forceinline__ void load(const uint16_t* p, int ld, uint16_t* lds) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) to_lds16(p + off + (uint32_t)i * kPer * ld, lds + (i * THREADS + (threadIdx.x & ~63)) * 8);
+  }
+  __device__ __forceinline__ void load_tail(const uint16_t* p, int ld, int left, uint16_t* lds) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const bool in = i * kPer + (int)threadIdx.x / kSlots < left;
+      const uint4 v = in ? *reinterpret_cast<const uint4*>(p + off + (uint32_t)i * kPer * ld) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(lds + (i * THREADS + threadIdx.x) * 8) = v;
+    }
+  }
+  template <int F>
+  __device__ __forceinline__ void read(const uint16_t* lds, int base, int kk, bf16x8_t (&f)[F]) const {
+    const int l16 = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
+    const int g = (l16 >> 2) | (q & 1) << 2;
+    // lane l16 of a group of 16 reads 4 columns (l16 % 4) of k = 8 q + l16 / 4 (then 4 further) and gets column l16
+    const uint16_t* p = lds + (32 * kk + 8 * q + (l16 >> 2)) * ROWS + (l16 & 3) * 4;
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+      const uint16_t* s = p + (((base >> 4) + i) ^ g) * 16;
+      const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)s);
+      const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(s + 4 * ROWS));
+      f[i] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
+
+// Four columns n ... of a part's row, those below N.
+__device__ __forceinline__ void put_part(float* out, int n, int N, int vec, const float (&z)[4]) {
+  if (vec) {
+    if (n < N) *reinterpret_cast<float4*>(out) = make_float4(z[0], z[1], z[2], z[3]);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (n + r < N) out[r] = z[r];
+  }
+}
+
+// One tile of one part of a product's reduction.  AK, BK: the operand is [k][index].  PAIR: SwiGLU, whose tiles hold
+// TN / 2 gate rows of W and the same up rows, each wave's gate rows before its up rows.
+template <typename T, bool AK, bool BK, bool PAIR>
+__device__ __forceinline__ void product_tile(const Prob& p, int b, int total, uint8_t* lds) {
+  constexpr int TM = T::TM, TN = T::TN, WM = T::WM, WN = T::WN, kFM = T::kFM, kFN = T::kFN, kThreads = T::kThreads;
+  constexpr int cols = PAIR ? TN / 2 : TN;  // output columns per tile
+  const int tm = (p.M + TM - 1) / TM, tn = (p.epi.N + cols - 1) / cols;
+  const int item = die_item(b, total);
+  const int part = item / (tm * tn);
+  // tiles in bands of 8 row tiles, walked column by column
+  const int tile = item - part * tm * tn;
+  const int band = tile / (8 * tn), in_band = tile - band * 8 * tn;
+  const int band_rows = min(8, tm - band * 8);
+  const int m0 = (band * 8 + in_band % band_rows) * TM, n0 = in_band / band_rows * cols;
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  Operand<TM, kThreads, AK> A;
+  Operand<TN, kThreads, BK> B;
+  // rows past the end read the last one and are not stored
+  A.init(p.lda, p.lda - m0, [&](int r) { return min(m0 + r, p.M - 1) - m0; });
+  B.init(p.ldb, p.ldb - n0, [&](int r) {
+    constexpr int kW = TN / WN, kH = kW / 2;
+    const int n = PAIR ? (r / kW) * kH + r % kH : r;
+    return min(n0 + n, p.epi.N - 1) - n0 + (PAIR && r % kW >= kH ? p.epi.N : 0);
+  });
+  const int seg_steps = (p.K + kBK - 1) / kBK;
+  const int steps = seg_steps * p.nseg;
+  const int lo = (int)((int64_t)steps * part / p.split), hi = (int)((int64_t)steps * (part + 1) / p.split);
+
+  uint16_t* const base = reinterpret_cast<uint16_t*>(lds);
+  int seg = lo / seg_steps, kstep = lo - seg * seg_steps, next = lo;  // the step that is loaded next
+  auto load = [&](int buf) {
+    uint16_t* la = base + buf * T::kStage;
+    uint16_t* lb = la + TM * kBK;
+    const int k0 = kstep * kBK;
+    const uint16_t* a = A.at(p.A + ((p.sa >> (2 * seg)) & 3) * p.a_plane, m0, k0, p.lda);
+    const uint16_t* c = B.at(p.B + ((p.sb >> (2 * seg)) & 3) * p.b_plane, n0, k0, p.ldb);
+    if (k0 + kBK <= p.K) {
+      A.load(a, p.lda, la);
+      B.load(c, p.ldb, lb);
+    } else {
+      A.load_tail(a, p.lda, p.K - k0, la);
+      B.load_tail(c, p.ldb, p.K - k0, lb);
+    }
+    if (++next < hi) {  // (past the part's end the last step is loaded again, into a buffer that nobody reads)
+      if (++kstep == seg_steps) {
+        kstep = 0;
+        ++seg;
+      }
+    }
+  };
+
+  f32x4_t acc[kFM][kFN];
+#pragma unroll
+  for (int i = 0; i < kFM; ++i)
+#pragma unroll
+    for (int j = 0; j < kFN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  bf16x8_t af[2][kFM], bf[2][kFN];
+  auto read = [&](int buf, int kk, int w) {
+    const uint16_t* la = base + buf * T::kStage;
+    B.template read<kFN>(la + TM * kBK, (TN / WN) * wn, kk, bf[w]);
+    A.template read<kFM>(la, (TM / WM) * wm, kk, af[w]);
+  };
+  auto mma = [&](int w) {
+#pragma unroll
+    for (int i = 0; i < kFM; ++i)
+#pragma unroll
+      for (int j = 0; j < kFN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[w][j], af[w][i], acc[i][j], 0, 0, 0);
+  };
+  constexpr int kReads = kFM * (AK ? 2 : 1) + kFN * (BK ? 2 : 1);
+  auto mix = [&] {  // the reads of the next half spread between the products of this one
+    constexpr int kPerRead = std::max(1, std::min(2, kFM * kFN / kReads));
+#pragma unroll
+    for (int x = 0; x < kReads; ++x) {
+      __builtin_amdgcn_sched_group_barrier(0x008, kPerRead, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    if constexpr (kFM * kFN > kPerRead * kReads) __builtin_amdgcn_sched_group_barrier(0x008, kFM * kFN - kPerRead * kReads, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Hands the buffers over: this wave's loads into one have landed and its reads of the other are done, then everyone's.
+  auto hand_over = [&] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  if (lo < hi) {
+    load(0);
+    hand_over();
+    load(1);
+    read(0, 0, 0);
+    int buf = 0;
+    for (int s = lo; s < hi; ++s, buf ^= 1) {
+      read(buf, 1, 1);
+      mma(0);
+      mix();
+      hand_over();  // the other buffer holds step s + 1; nobody reads this one any more
+      load(buf);
+      __builtin_amdgcn_sched_barrier(0);
+      read(buf ^ 1, 0, 0);
+      mma(1);
+      mix();
+    }
+  }
+
+  // The fp32 tile goes through LDS so that a wave's loads and stores of the epilogue run along rows.  A lane holds
+  // row lane % 16 of A and four rows 4 (lane / 16) of B: 16-byte pieces, piece c of row m at c ^ (m % 16), so that the
+  // lanes that write together lie in 16 different places.
+  float* tile_c = reinterpret_cast<float*>(lds);
+  constexpr int kPieces = TN / 4, kPassRows = TM / T::kPasses, kOutPieces = cols / 4;
+  const int r16 = lane & 15, q = lane >> 4;
+  const bool split = p.split > 1;
+#pragma unroll
+  for (int pass = 0; pass < T::kPasses; ++pass) {
+    hand_over();  // the loads and reads of the loop, or the reads of the pass before, are done
+    if (T::kPasses == 1 || wm == pass) {
+#pragma unroll
+      for (int i = 0; i < kFM; ++i)
+#pragma unroll
+        for (int j = 0; j < kFN; ++j) {
+          const int m = (T::kPasses == 1 ? (TM / WM) * wm : 0) + 16 * i + r16, c = (TN / WN / 4) * wn + 4 * j + q;
+          *reinterpret_cast<f32x4_t*>(tile_c + (m * kPieces + (c ^ (m & 15))) * 4) = acc[i][j];
+        }
+    }
+    hand_over();
+#pragma unroll 2
+    for (int i = tid; i < kPassRows * kOutPieces; i += kThreads) {
+      const int r = i / kOutPieces, o = i % kOutPieces;
+      const int m = m0 + pass * kPassRows + r, n = n0 + 4 * o;
+      if (m >= p.M || n >= p.epi.N) continue;
+      constexpr int kH = TN / WN / 8;  // pieces of a wave's gate rows
+      const int c = PAIR ? (o / kH) * 2 * kH + o % kH : o;
+      float z[4], zu[4] = {0.f, 0.f, 0.f, 0.f};
+      const float4 v = *reinterpret_cast<const float4*>(tile_c + (r * kPieces + (c ^ (r & 15))) * 4);
+      z[0] = v.x; z[1] = v.y; z[2] = v.z; z[3] = v.w;
+      if constexpr (PAIR) {
+        const float4 u = *reinterpret_cast<const float4*>(tile_c + (r * kPieces + ((c + kH) ^ (r & 15))) * 4);
+        zu[0] = u.x; zu[1] = u.y; zu[2] = u.z; zu[3] = u.w;
+      }
+      if (split) {
+        float* out = p.partial + ((size_t)part * p.M + m) * p.ldp + n;
+        put_part(out, n, p.epi.N, p.epi.vec, z);
+        if constexpr (PAIR) put_part(out + p.epi.N, n, p.epi.N, p.epi.vec, zu);
+      } else {
+        epi_four(p.epi, m, n, z, zu);
+      }
+    }
+  }
+}
+
+// The forward product.
+template <typename T, bool PAIR>
+__global__ __launch_bounds__(T::kThreads, 2) void linear_product_kernel(Prob p) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[T::kLds];
+  product_tile<T, false, false, PAIR>(p, blockIdx.x, gridDim.x, lds);
+}
+
+// The gradient's two products in one grid, so that the tiles of one fill what the other leaves idle: first dW (the
+// longer reduction as a rule), then dx.
+template <typename T>
+__global__ __launch_bounds__(T::kThreads, 2) void grad_products_kernel(Prob dw, Prob dx, int dw_blocks) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[T::kLds];
+  const int b = blockIdx.x;
+  if (b < dw_blocks) product_tile<T, true, true, false>(dw, b, dw_blocks, lds);
+  else product_tile<T, false, true, false>(dx, b - dw_blocks, gridDim.x - dw_blocks, lds);
+}
+
+// Adds the parts of split products in part order and applies their epilogue; the workgroups after those add the
+// column sums' parts.  Four columns per thread.
+__global__ __launch_bounds__(256) void join_kernel(Join jn) {
+  int b = blockIdx.x;
+  if (b < jn.n0 + jn.n1) {
+    const Prob& p = jn.p[b >= jn.n0];
+    if (b >= jn.n0) b -= jn.n0;
+    const int quads = (p.epi.N + 3) >> 2;
+    const int64_t i = (int64_t)b * 256 + threadIdx.x;
+    if (i >= (int64_t)p.M * quads) return;
+    const int m = (int)(i / quads), n = (int)(i - (int64_t)m * quads) * 4;
+    const bool pair = p.epi.act == MOE_ACT_SWIGLU;
+    float z[4] = {0.f, 0.f, 0.f, 0.f}, zu[4] = {0.f, 0.f, 0.f, 0.f};
+    const size_t step = (size_t)p.M * p.ldp;
+    const float* in = p.partial + (size_t)m * p.ldp + n;
+    if (p.epi.vec) {
+#pragma unroll 4
+      for (int s = 0; s < p.split; ++s) {
+        const float4 q = *reinterpret_cast<const float4*>(in + s * step);
+        z[0] += q.x; z[1] += q.y; z[2] += q.z; z[3] += q.w;
+        if (pair) {
+          const float4 u = *reinterpret_cast<const float4*>(in + s * step + p.epi.N);
+          zu[0] += u.x; zu[1] += u.y; zu[2] += u.z; zu[3] += u.w;
+        }
+      }
+    } else {
+      for (int s = 0; s < p.split; ++s) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (n + r < p.epi.N) {
+            z[r] += in[s * step + r];
+            if (pair) zu[r] += in[s * step + p.epi.N + r];
+          }
+      }
+    }
+    epi_four(p.epi, m, n, z, zu);
+    return;
+  }
+  // 64 columns a workgroup; its four waves take every fourth row, and their sums are added in wave order
+  __shared__ float part[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = (b - jn.n0 - jn.n1) * 64 + lane;
+  float v = 0.0f;
+  if (c < jn.db_n) {
+#pragma unroll 8
+    for (int r = wave; r < jn.db_rows; r += 4) v += jn.db_part[(size_t)r * jn.db_n + c];
+  }
+  part[wave][lane] = v;
+  __syncthreads();
+  if (wave == 0 && c < jn.db_n) jn.db[c] = part[0][lane] + part[1][lane] + part[2][lane] + part[3][lane];
+}
+
+bool epi_vec(const Epi& e) {
+  auto ok = [](const void* q, int bf16) { return reinterpret_cast<uintptr_t>(q) % (bf16 ? 8 : 16) == 0; };
+  return e.N % 4 == 0 && ok(e.y, e.y_bf16) && ok(e.pre, e.y_bf16) && ok(e.res, e.res_bf16) && ok(e.bias, 0);
+}
+
+int64_t tiles_of(const Shape& s, int side) { return ceil_div(s.M, side) * ceil_div(s.R, side); }
+int64_t steps_of(const Shape& s) { return ceil_div(s.K, kBK) * s.nseg; }
+
+// How many parts a reduction of `steps` K-steps is cut into, where the launch's tiles make `work` K-steps in all and
+// `slots` workgroups run at once: as many as it takes for a part to be no longer than an even share of the work, but
+// no part below 8 K-steps (each costs about as much again to start, and its fp32 sums go through memory).
+int split_of(int64_t steps, int64_t work, int64_t slots) {
+  const int64_t share = std::max<int64_t>(8, ceil_div(work, slots));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(16, steps / share));
+}
+
+}  // namespace
+
+// The tile shape and the parts of one or two products launched together.  A round of 256 x 256 tiles (256 at once)
+// measured 1.72 times as long as one of 128 x 128 tiles (512 at once) at the same K, for twice the work: 8192 x 4096 x
+// 4096 takes 224 us with the large tile (2 rounds) against 261 us (4 rounds), 8192 x 2048 x 1024 takes 52 us (half the
+// CUs idle) against 36.5.  So the shape with the lower estimate is taken.
+Plan plan_products(const Shape* s, int count) {
+  int64_t work[2] = {0, 0};
+  for (int i = 0; i < count; ++i) {
+    work[0] += tiles_of(s[i], 128) * steps_of(s[i]);
+    work[1] += tiles_of(s[i], 256) * steps_of(s[i]);
+  }
+  double cost[2] = {0, 0};
+  Plan best{};
+  for (int large = 0; large < 2; ++large) {
+    const int slots = large ? 256 : 512, side = large ? 256 : 128;
+    Plan p{};
+    p.large = large;
+    int64_t blocks = 0, longest = 0;
+    for (int i = 0; i < count; ++i) {
+      p.split[i] = split_of(steps_of(s[i]), work[large], slots);
+      blocks += tiles_of(s[i], side) * p.split[i];
+      longest = std::max(longest, ceil_div(steps_of(s[i]), p.split[i]));
+    }
+    const double even = (double)work[large] / slots;
+    const double rounds = (double)ceil_div(blocks, slots) * work[large] / std::max<int64_t>(blocks, 1);
+    cost[large] = std::max({even, rounds, (double)longest}) * (large ? 1.72 : 1.0);
+    if (large == 0 || cost[1] < cost[0]) best = p;
+  }
+  return best;
+}
+
+moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool grad, bool first_is_dw,
+                           const float* db_part, int db_rows, int db_n, float* db, hipStream_t s, const char* what) {
+  const int side = plan.large ? 256 : 128;
+  int64_t blocks[2] = {0, 0};
+  Join j{};
+  for (int i = 0; i < count; ++i) {
+    p[i].epi.vec = epi_vec(p[i].epi);
+    blocks[i] = tiles_of(Shape{p[i].M, p[i].R, p[i].K, p[i].nseg}, side) * p[i].split;
+    // (SwiGLU tiles hold half as many output columns, of which there are half as many as rows of W)
+    if (p[i].epi.act == MOE_ACT_SWIGLU) blocks[i] = ceil_div(p[i].M, side) * ceil_div(p[i].epi.N, side / 2) * p[i].split;
+    j.p[i] = p[i];
+    if (p[i].split > 1) (i ? j.n1 : j.n0) = (int)ceil_div((int64_t)p[i].M * ((p[i].epi.N + 3) / 4), 256);
+  }
+  if (blocks[0] + blocks[1] > 0x7FFFFFFF) return fail(MOE_EUNSUPPORTED, std::string(what) + ": too many tiles");
+  if (count > 0) {
+    const dim3 grid((unsigned)(blocks[0] + blocks[1]));
+    auto fwd = [&](auto kernel, int threads) { launch_k(kid, kernel, grid, dim3((unsigned)threads), 0, s, p[0]); };
+    auto bwd = [&](auto kernel, int threads) {
+      const int n = first_is_dw ? (int)blocks[0] : 0;
+      launch_k(kid, kernel, grid, dim3((unsigned)threads), 0, s, p[0], p[count - 1], n);
+    };
+    const bool pair = p[0].epi.act == MOE_ACT_SWIGLU;
+    if (grad) plan.large ? bwd(grad_products_kernel<Large>, Large::kThreads) : bwd(grad_products_kernel<Small>, Small::kThreads);
+    else if (plan.large && pair) fwd(linear_product_kernel<Large, true>, Large::kThreads);
+    else if (plan.large) fwd(linear_product_kernel<Large, false>, Large::kThreads);
+    else if (pair) fwd(linear_product_kernel<Small, true>, Small::kThreads);
+    else fwd(linear_product_kernel<Small, false>, Small::kThreads);
+    if (moe_status st = check_launch(what)) return st;
+  }
+  j.db_part = db_part;
+  j.db = db;
+  j.db_rows = db_rows;
+  j.db_n = db ? db_n : 0;
+  const int64_t jb = (int64_t)j.n0 + j.n1 + ceil_div(j.db_n, 64);
+  if (jb > 0) {
+    join_kernel<<<dim3((unsigned)jb), 256, 0, s>>>(j);
+    return check_launch(what);
+  }
+  return MOE_OK;
+}
+
+}  // namespace moe
