@@ -57,7 +57,10 @@ __device__ __forceinline__ void to_lds16(const uint16_t* g, uint16_t* l) {
                                    (__attribute__((address_space(3))) uint32_t*)l, 16, 0, 0);
 }
 
-// Loader and reader of one operand's tile: ROWS indices (m or n) by 64 k.
+// A value that is the same in every lane, kept in a scalar register (integer divisions leave theirs in vector ones).
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Loader and reader of one operand's tile: ROWS indices (m or n) by 64 k.  `w64` is the wave's first thread.
 template <int ROWS, int THREADS, bool KROWS>
 struct Operand;
 
@@ -77,9 +80,9 @@ struct Operand<ROWS, THREADS, false> {  // [m][k]
   __device__ __forceinline__ const uint16_t* at(const uint16_t* p, size_t first, int k0, int ld) const {
     return p + first * ld + k0;
   }
-  __device__ __forceinline__ void load(const uint16_t* p, int, uint16_t* lds) const {
+  __device__ __forceinline__ void load(const uint16_t* p, int, uint16_t* lds, int w64) const {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) to_lds16(p + off[i], lds + (i * THREADS + (threadIdx.x & ~63)) * 8);
+    for (int i = 0; i < kLoads; ++i) to_lds16(p + off[i], lds + (i * THREADS + w64) * 8);
   }
   // the last step of a reduction that is no multiple of 64: `left` k are there, the others become zeros
   __device__ __forceinline__ void load_tail(const uint16_t* p, int, int left, uint16_t* lds) const {
@@ -114,9 +117,9 @@ struct Operand<ROWS, THREADS, true> {  // [k][m]
   __device__ __forceinline__ const uint16_t* at(const uint16_t* p, size_t first, int k0, int ld) const {
     return p + (size_t)k0 * ld + first;
   }
-  __device__ __forceinline__ void load(const uint16_t* p, int ld, uint16_t* lds) const {
+  __device__ __forceinline__ void load(const uint16_t* p, int ld, uint16_t* lds, int w64) const {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) to_lds16(p + off + (uint32_t)i * kPer * ld, lds + (i * THREADS + (threadIdx.x & ~63)) * 8);
+    for (int i = 0; i < kLoads; ++i) to_lds16(p + off + (uint32_t)i * kPer * ld, lds + (i * THREADS + w64) * 8);
   }
   __device__ __forceinline__ void load_tail(const uint16_t* p, int ld, int left, uint16_t* lds) const {
 #pragma unroll
@@ -161,14 +164,14 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
   constexpr int cols = PAIR ? TN / 2 : TN;  // output columns per tile
   const int tm = (p.M + TM - 1) / TM, tn = (p.epi.N + cols - 1) / cols;
   const int item = die_item(b, total);
-  const int part = item / (tm * tn);
+  const int part = uniform(item / (tm * tn));
   // tiles in bands of 8 row tiles, walked column by column
   const int tile = item - part * tm * tn;
   const int band = tile / (8 * tn), in_band = tile - band * 8 * tn;
   const int band_rows = min(8, tm - band * 8);
-  const int m0 = (band * 8 + in_band % band_rows) * TM, n0 = in_band / band_rows * cols;
+  const int m0 = uniform((band * 8 + in_band % band_rows) * TM), n0 = uniform(in_band / band_rows * cols);
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   Operand<TM, kThreads, AK> A;
   Operand<TN, kThreads, BK> B;
@@ -181,27 +184,36 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
   });
   const int seg_steps = (p.K + kBK - 1) / kBK;
   const int steps = seg_steps * p.nseg;
-  const int lo = (int)((int64_t)steps * part / p.split), hi = (int)((int64_t)steps * (part + 1) / p.split);
+  const int lo = uniform((int)((int64_t)steps * part / p.split)), hi = uniform((int)((int64_t)steps * (part + 1) / p.split));
 
   uint16_t* const base = reinterpret_cast<uint16_t*>(lds);
-  int seg = lo / seg_steps, kstep = lo - seg * seg_steps, next = lo;  // the step that is loaded next
+  int seg = uniform(lo / seg_steps), kstep = lo - seg * seg_steps, next = lo;  // the step that is loaded next
+  const int last = p.K - kBK;
+  const uint16_t *src_a, *src_b;
+  auto place = [&] {
+    src_a = A.at(p.A + ((p.sa >> (2 * seg)) & 3) * p.a_plane, m0, kstep * kBK, p.lda);
+    src_b = B.at(p.B + ((p.sb >> (2 * seg)) & 3) * p.b_plane, n0, kstep * kBK, p.ldb);
+  };
+  place();
+  const int64_t step_a = AK ? (int64_t)kBK * p.lda : kBK, step_b = BK ? (int64_t)kBK * p.ldb : kBK;
   auto load = [&](int buf) {
     uint16_t* la = base + buf * T::kStage;
     uint16_t* lb = la + TM * kBK;
     const int k0 = kstep * kBK;
-    const uint16_t* a = A.at(p.A + ((p.sa >> (2 * seg)) & 3) * p.a_plane, m0, k0, p.lda);
-    const uint16_t* c = B.at(p.B + ((p.sb >> (2 * seg)) & 3) * p.b_plane, n0, k0, p.ldb);
-    if (k0 + kBK <= p.K) {
-      A.load(a, p.lda, la);
-      B.load(c, p.ldb, lb);
+    if (k0 <= last) {
+      A.load(src_a, p.lda, la, 64 * wave);
+      B.load(src_b, p.ldb, lb, 64 * wave);
     } else {
-      A.load_tail(a, p.lda, p.K - k0, la);
-      B.load_tail(c, p.ldb, p.K - k0, lb);
+      A.load_tail(src_a, p.lda, p.K - k0, la);
+      B.load_tail(src_b, p.ldb, p.K - k0, lb);
     }
     if (++next < hi) {  // (past the part's end the last step is loaded again, into a buffer that nobody reads)
+      src_a += step_a;
+      src_b += step_b;
       if (++kstep == seg_steps) {
         kstep = 0;
         ++seg;
+        place();
       }
     }
   };
@@ -280,27 +292,33 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
         }
     }
     hand_over();
-#pragma unroll 2
-    for (int i = tid; i < kPassRows * kOutPieces; i += kThreads) {
-      const int r = i / kOutPieces, o = i % kOutPieces;
-      const int m = m0 + pass * kPassRows + r, n = n0 + 4 * o;
-      if (m >= p.M || n >= p.epi.N) continue;
-      constexpr int kH = TN / WN / 8;  // pieces of a wave's gate rows
-      const int c = PAIR ? (o / kH) * 2 * kH + o % kH : o;
-      float z[4], zu[4] = {0.f, 0.f, 0.f, 0.f};
-      const float4 v = *reinterpret_cast<const float4*>(tile_c + (r * kPieces + (c ^ (r & 15))) * 4);
+    // a thread keeps to four columns and walks down the rows
+    static_assert(kThreads % kOutPieces == 0, "columns per thread");
+    const int o = tid % kOutPieces, n = n0 + 4 * o;
+    constexpr int kH = TN / WN / 8;  // PAIR: pieces of a wave's gate rows
+    const int c = PAIR ? (o / kH) * 2 * kH + o % kH : o;
+    constexpr int kStep = kThreads / kOutPieces;
+    const int r0 = tid / kOutPieces, m = m0 + pass * kPassRows + r0;
+    const int rows = n < p.epi.N ? min(kPassRows - r0, p.M - m) : 0;  // counted from r0 on, in steps of kStep
+    auto piece = [&](int r, int at, float (&z)[4]) {
+      const float4 v = *reinterpret_cast<const float4*>(tile_c + (r * kPieces + (at ^ (r & 15))) * 4);
       z[0] = v.x; z[1] = v.y; z[2] = v.z; z[3] = v.w;
-      if constexpr (PAIR) {
-        const float4 u = *reinterpret_cast<const float4*>(tile_c + (r * kPieces + ((c + kH) ^ (r & 15))) * 4);
-        zu[0] = u.x; zu[1] = u.y; zu[2] = u.z; zu[3] = u.w;
-      }
-      if (split) {
-        float* out = p.partial + ((size_t)part * p.M + m) * p.ldp + n;
+    };
+    auto value = [&](int d, float (&z)[4], float (&zu)[4]) {  // row r0 + d
+      piece(r0 + d, c, z);
+      if constexpr (PAIR) piece(r0 + d, c + kH, zu);
+    };
+    if (split) {
+      float* out = p.partial + ((size_t)part * p.M + m) * p.ldp + n;
+      for (int d = 0; d < rows; d += kStep) {
+        float z[4], zu[4];
+        value(d, z, zu);
         put_part(out, n, p.epi.N, p.epi.vec, z);
         if constexpr (PAIR) put_part(out + p.epi.N, n, p.epi.N, p.epi.vec, zu);
-      } else {
-        epi_four(p.epi, m, n, z, zu);
+        out += (size_t)kStep * p.ldp;
       }
+    } else {
+      epi_rows<PAIR, kStep>(p.epi, m, n, rows, value);
     }
   }
 }
@@ -357,7 +375,15 @@ __global__ __launch_bounds__(256) void join_kernel(Join jn) {
           }
       }
     }
-    epi_four(p.epi, m, n, z, zu);
+    const auto value = [&](int, float (&a)[4], float (&u)[4]) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        a[r] = z[r];
+        u[r] = zu[r];
+      }
+    };
+    if (pair) epi_rows<true, 1>(p.epi, m, n, 1, value);
+    else epi_rows<false, 1>(p.epi, m, n, 1, value);
     return;
   }
   // 64 columns a workgroup; its four waves take every fourth row, and their sums are added in wave order
