@@ -19,7 +19,8 @@
 // stretch s of row k lies at s ^ (k % 4 + 4 (k / 8 % 2)), which spreads the 8 rows that 32 lanes touch over 256 bytes.
 //
 // Two tile shapes.  256 x 256 (8 waves, 128 KB of LDS, one workgroup per CU) reads half as much per product as
-// 128 x 128 (4 waves, two workgroups per CU), but needs enough tiles to fill 256 CUs evenly: see pick_tile.
+// 128 x 128 (4 waves, two workgroups per CU), but needs enough tiles to fill 256 CUs evenly: see
+// plan_products.
 #include <algorithm>
 
 #include "linear_dev.hpp"
@@ -59,6 +60,13 @@ __device__ __forceinline__ void to_lds16(const uint16_t* g, uint16_t* l) {
 
 // A value that is the same in every lane, kept in a scalar register (integer divisions leave theirs in vector ones).
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Four values of a column by ds_read_b64_tr_b16.  The compiler takes a read it knows nothing about to wait for every
+// load into LDS that is under way; `p` being restrict tells it that this one does not (hand_over below orders the two).
+// Without it the gradient's products waited for each step's loads right after issuing them.
+__device__ __forceinline__ s16x4_t read_tr(const uint16_t* __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
+}
 
 // Loader and reader of one operand's tile: ROWS indices (m or n) by 64 k.  `w64` is the wave's first thread.
 template <int ROWS, int THREADS, bool KROWS>
@@ -138,8 +146,8 @@ struct Operand<ROWS, THREADS, true> {  // [k][m]
 #pragma unroll
     for (int i = 0; i < F; ++i) {
       const uint16_t* s = p + (((base >> 4) + i) ^ g) * 16;
-      const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)s);
-      const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(s + 4 * ROWS));
+      const s16x4_t a = read_tr(s);
+      const s16x4_t b = read_tr(s + 4 * ROWS);
       f[i] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
@@ -408,43 +416,57 @@ bool epi_vec(const Epi& e) {
 int64_t tiles_of(const Shape& s, int side) { return ceil_div(s.M, side) * ceil_div(s.R, side); }
 int64_t steps_of(const Shape& s) { return ceil_div(s.K, kBK) * s.nseg; }
 
-// How many parts a reduction of `steps` K-steps is cut into, where the launch's tiles make `work` K-steps in all and
-// `slots` workgroups run at once: as many as it takes for a part to be no longer than an even share of the work, but
-// no part below 8 K-steps (each costs about as much again to start, and its fp32 sums go through memory).
-int split_of(int64_t steps, int64_t work, int64_t slots) {
-  const int64_t share = std::max<int64_t>(8, ceil_div(work, slots));
-  return (int)std::max<int64_t>(1, std::min<int64_t>(16, steps / share));
+// Time of a launch in microseconds, from measurements of both tile shapes over 1 to 64 K-steps and 64 to 1,024 tiles:
+// a workgroup costs a start and an epilogue besides its K-steps, less of each while it has a CU to itself, and a cut
+// reduction costs a second launch and its parts' way through memory.
+//   8192 x 2048 x 1024: 128 x 128 tiles 37.5 us, 256 x 256 (half the CUs idle) 54, in two parts 41 + 15 for the join
+//   8192 x 1024 x 2048: 43.8 against 38.8;  8192 x 4096 x 4096: 261 against 224
+//   1024 x 8192 x 2048 in parts: one 117, two 57, four 47 us
+struct Rates {
+  int slots, side;              // workgroups at once, tile side
+  double start, step;           // with all slots taken
+  double start_alone, step_alone;  // up to half of them
+};
+constexpr Rates kRates[2] = {{512, 128, 7.5, 0.85, 4.5, 0.60}, {256, 256, 13.0, 1.50, 10.5, 1.19}};
+
+double cost_of(const Rates& r, const Shape* s, const int* split, int count) {
+  int64_t blocks = 0;
+  double parts = 0;  // bytes of fp32 sums
+  for (int i = 0; i < count; ++i) {
+    blocks += tiles_of(s[i], r.side) * split[i];
+    if (split[i] > 1) parts += 4.0 * split[i] * s[i].M * s[i].R;
+  }
+  const bool alone = blocks <= r.slots / 2;
+  double sum = 0, longest = 0;
+  for (int i = 0; i < count; ++i) {
+    const int64_t steps = ceil_div(steps_of(s[i]), split[i]);
+    const double d = alone ? r.start_alone + r.step_alone * steps : r.start + r.step * steps;
+    const int64_t n = tiles_of(s[i], r.side) * split[i];
+    sum += d * (count == 1 ? (double)(ceil_div(n, r.slots) * r.slots) : (double)n);
+    longest = std::max(longest, d);
+  }
+  // 2 us of launch; parts are read again at about 5 TB/s, by a launch of 4 us (1024 x 8192 x 2048 in four parts: 8 us)
+  return 2.0 + std::max(sum / r.slots, longest) + (parts > 0 ? 4.0 + parts / 5.0e6 : 0.0);
 }
 
 }  // namespace
 
-// The tile shape and the parts of one or two products launched together.  A round of 256 x 256 tiles (256 at once)
-// measured 1.72 times as long as one of 128 x 128 tiles (512 at once) at the same K, for twice the work: 8192 x 4096 x
-// 4096 takes 224 us with the large tile (2 rounds) against 261 us (4 rounds), 8192 x 2048 x 1024 takes 52 us (half the
-// CUs idle) against 36.5.  So the shape with the lower estimate is taken.
+// The tile shape and the parts of one or two products launched together: the cheapest of a few cuts by cost_of.
 Plan plan_products(const Shape* s, int count) {
-  int64_t work[2] = {0, 0};
-  for (int i = 0; i < count; ++i) {
-    work[0] += tiles_of(s[i], 128) * steps_of(s[i]);
-    work[1] += tiles_of(s[i], 256) * steps_of(s[i]);
-  }
-  double cost[2] = {0, 0};
   Plan best{};
-  for (int large = 0; large < 2; ++large) {
-    const int slots = large ? 256 : 512, side = large ? 256 : 128;
-    Plan p{};
-    p.large = large;
-    int64_t blocks = 0, longest = 0;
-    for (int i = 0; i < count; ++i) {
-      p.split[i] = split_of(steps_of(s[i]), work[large], slots);
-      blocks += tiles_of(s[i], side) * p.split[i];
-      longest = std::max(longest, ceil_div(steps_of(s[i]), p.split[i]));
+  double least = 0;
+  for (int large = 0; large < 2; ++large)
+    for (int share = 1 << 20; share >= 8; share = share > 128 ? 128 : share / 2) {  // K-steps of a part, about
+      Plan p{};
+      p.large = large;
+      for (int i = 0; i < count; ++i)
+        p.split[i] = (int)std::max<int64_t>(1, std::min<int64_t>(16, (steps_of(s[i]) + share / 2) / share));
+      const double c = cost_of(kRates[large], s, p.split, count);
+      if (least == 0 || c < least) {
+        least = c;
+        best = p;
+      }
     }
-    const double even = (double)work[large] / slots;
-    const double rounds = (double)ceil_div(blocks, slots) * work[large] / std::max<int64_t>(blocks, 1);
-    cost[large] = std::max({even, rounds, (double)longest}) * (large ? 1.72 : 1.0);
-    if (large == 0 || cost[1] < cost[0]) best = p;
-  }
   return best;
 }
 
