@@ -437,18 +437,25 @@ def decode_workspace_bytes(layer: ExpertLayer, T: int, k: int) -> int:
 _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
 
 
-def _arg(t: torch.Tensor, name: str, shape: tuple, dtypes: tuple, device=None):
+# What a call costs on the host decides how fast small steps run (a decode-size product's kernel takes 3 to 5 us), so
+# the checks below are plain comparisons, and the current stream and device are asked for without their wrappers.
+_current_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _arg(t: torch.Tensor, name: str, shape: tuple, dtypes: tuple, index: int | None = None):
     """Checks an argument's shape, type, layout and device; returns its address."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other tensors are on {device}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the other tensors are on cuda:{index}")
     return t.data_ptr()
 
 
@@ -465,17 +472,34 @@ def _ws(ws: torch.Tensor | None, need: int, device):
             return None, None, 0
         ws = torch.empty(need, dtype=torch.uint8, device=device)
     else:
-        _arg(ws, "ws", tuple(ws.shape), (torch.uint8,), device)
+        _arg(ws, "ws", ws.shape, (torch.uint8,), device.index)
     return ws, ws.data_ptr(), ws.numel()
+
+
+class _Here:
+    """The context of a call on the current stream: nothing to switch."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
 
 
 def _launch(fn, device, stream, *args):
     """One library call on `stream` (or `device`'s current stream) with `device` current."""
-    if device.index != torch.cuda.current_device():
+    index = device.index
+    s = _current_stream(index) if stream is None else _stream(stream, device)
+    if index != _current_device():
         with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream, device)))
+            status = fn(*args, s)
     else:
-        _check(fn(*args, _stream(stream, device)))
+        status = fn(*args, s)
+    if status != MOE_OK:
+        _check(status)
 
 
 def balance_loss(logits: torch.Tensor, ids: torch.Tensor, mask: torch.Tensor | None = None,
@@ -488,9 +512,10 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, mask: torch.Tensor | N
     k = _rows(ids, "ids", 2)[1]
     a_logits = _arg(logits, "logits", (T, E), (_F32,))
     dev = logits.device
-    a_ids = _arg(ids, "ids", (T, k), (_I32,), dev)
-    a_mask = None if mask is None else _arg(mask, "mask", (T,), (torch.bool, torch.uint8), dev)
-    with _on(stream, dev):
+    at = dev.index
+    a_ids = _arg(ids, "ids", (T, k), (_I32,), at)
+    a_mask = None if mask is None else _arg(mask, "mask", (T,), (torch.bool, torch.uint8), at)
+    with _HERE if stream is None else _on(stream, dev):
         if loss is None:
             loss = torch.empty(2, dtype=_F32, device=dev)
         if counts is None:
@@ -499,8 +524,8 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, mask: torch.Tensor | N
             lse = torch.empty(T, dtype=_F32, device=dev)
         ws, a_ws, n_ws = _ws(ws, int(lib.moe_balance_loss_workspace_bytes(T, E)), dev)
     _launch(lib.moe_balance_loss, dev, stream, a_logits, a_ids, a_mask, T, E, k,
-            _arg(loss, "loss", (2,), (_F32,), dev), _arg(counts, "counts", (E + 1,), (_I32,), dev),
-            _arg(lse, "lse", (T,), (_F32,), dev), a_ws, n_ws)
+            _arg(loss, "loss", (2,), (_F32,), at), _arg(counts, "counts", (E + 1,), (_I32,), at),
+            _arg(lse, "lse", (T,), (_F32,), at), a_ws, n_ws)
     return loss, counts, lse
 
 
@@ -521,18 +546,19 @@ def route_backward(logits: torch.Tensor, ids: torch.Tensor, w: torch.Tensor | No
         raise ValueError("neither gate weights (w, dw) nor losses (lse, counts, dloss)")
     a_logits = _arg(logits, "logits", (T, E), (_F32,))
     dev = logits.device
-    a_ids = _arg(ids, "ids", (T, k), (_I32,), dev)
+    at = dev.index
+    a_ids = _arg(ids, "ids", (T, k), (_I32,), at)
     a_w = a_dw = a_lse = a_counts = a_dloss = None
     if w is not None:
-        a_w, a_dw = _arg(w, "w", (T, k), (_F32,), dev), _arg(dw, "dw", (T, k), (_F32,), dev)
+        a_w, a_dw = _arg(w, "w", (T, k), (_F32,), at), _arg(dw, "dw", (T, k), (_F32,), at)
     if lse is not None:
-        a_lse, a_counts = _arg(lse, "lse", (T,), (_F32,), dev), _arg(counts, "counts", (E + 1,), (_I32,), dev)
-        a_dloss = _arg(dloss, "dloss", (2,), (_F32,), dev)
+        a_lse, a_counts = _arg(lse, "lse", (T,), (_F32,), at), _arg(counts, "counts", (E + 1,), (_I32,), at)
+        a_dloss = _arg(dloss, "dloss", (2,), (_F32,), at)
     if dlogits is None:
-        with _on(stream, dev):
+        with _HERE if stream is None else _on(stream, dev):
             dlogits = torch.empty((T, E), dtype=_F32, device=dev)
     _launch(lib.moe_route_backward, dev, stream, a_logits, a_ids, a_w, a_dw, a_lse, a_counts, a_dloss, T, E, k,
-            _arg(dlogits, "dlogits", (T, E), (_F32,), dev))
+            _arg(dlogits, "dlogits", (T, E), (_F32,), at))
     return dlogits
 
 
@@ -545,8 +571,9 @@ def combine_backward(y: torch.Tensor, w: torch.Tensor, dout: torch.Tensor, dw: t
         raise ValueError('need holds "dw", "dy" or both')
     a_y = _arg(y, "y", (T, k, H), (_F32, _BF16))
     dev = y.device
-    a_w, a_dout = _arg(w, "w", (T, k), (_F32,), dev), _arg(dout, "dout", (T, H), (_F32, _BF16), dev)
-    with _on(stream, dev):
+    at = dev.index
+    a_w, a_dout = _arg(w, "w", (T, k), (_F32,), at), _arg(dout, "dout", (T, H), (_F32, _BF16), at)
+    with _HERE if stream is None else _on(stream, dev):
         if "dw" not in need:
             dw = None
         elif dw is None:
@@ -556,8 +583,8 @@ def combine_backward(y: torch.Tensor, w: torch.Tensor, dout: torch.Tensor, dw: t
         elif dy is None:
             dy = torch.empty((T, k, H), dtype=y.dtype, device=dev)
     _launch(lib.moe_combine_backward, dev, stream, a_y, _dtype_code(y), a_w, a_dout, _dtype_code(dout), T, k, H,
-            None if dw is None else _arg(dw, "dw", (T, k), (_F32,), dev),
-            None if dy is None else _arg(dy, "dy", (T, k, H), (y.dtype,), dev))
+            None if dw is None else _arg(dw, "dw", (T, k), (_F32,), at),
+            None if dy is None else _arg(dy, "dy", (T, k, H), (y.dtype,), at))
     return dw, dy
 
 
@@ -584,15 +611,16 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, a
     code, N = _act_rows(w, act)
     a_x = _arg(x, "x", (T, K), (_F32, _BF16))
     dev = x.device
-    a_w = _arg(w, "w", (R, K), (_BF16,), dev)
-    a_bias = None if bias is None else _arg(bias, "bias", (R,), (_F32,), dev)
-    a_res = None if residual is None else _arg(residual, "residual", (T, N), (_F32, _BF16), dev)
+    at = dev.index
+    a_w = _arg(w, "w", (R, K), (_BF16,), at)
+    a_bias = None if bias is None else _arg(bias, "bias", (R,), (_F32,), at)
+    a_res = None if residual is None else _arg(residual, "residual", (T, N), (_F32, _BF16), at)
     x_t, r_t = _dtype_code(x), MOE_F32 if residual is None else _dtype_code(residual)
-    with _on(stream, dev):
+    with _HERE if stream is None else _on(stream, dev):
         if y is None:
             y = torch.empty((T, N), dtype=x.dtype if y_dtype is None else y_dtype, device=dev)
-        a_y, y_t = _arg(y, "y", (T, N), (_F32, _BF16), dev), _dtype_code(y)
-        a_pre = None if pre is None else _arg(pre, "pre", (T, R), (y.dtype,), dev)
+        a_y, y_t = _arg(y, "y", (T, N), (_F32, _BF16), at), _dtype_code(y)
+        a_pre = None if pre is None else _arg(pre, "pre", (T, R), (y.dtype,), at)
         ws, a_ws, n_ws = _ws(ws, int(lib.moe_linear_workspace_bytes(T, K, N, code, x_t, y_t)), dev)
     _launch(lib.moe_linear, dev, stream, a_x, x_t, a_w, a_bias, code, a_res, r_t, T, K, N, a_y, y_t, a_pre, a_ws, n_ws)
     return y
@@ -624,8 +652,9 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str
         raise ValueError(f"act {act!r} needs pre")
     a_dy = _arg(dy, "dy", (T, N), (_F32, _BF16))
     dev = dy.device
-    a_x, a_w = _arg(x, "x", (T, K), (_F32, _BF16), dev), _arg(w, "w", (R, K), (_BF16,), dev)
-    a_pre = None if act == "none" else _arg(pre, "pre", (T, R), (dy.dtype,), dev)
+    at = dev.index
+    a_x, a_w = _arg(x, "x", (T, K), (_F32, _BF16), at), _arg(w, "w", (R, K), (_BF16,), at)
+    a_pre = None if act == "none" else _arg(pre, "pre", (T, R), (dy.dtype,), at)
     bits = 0
     for n in need:
         bits |= _NEED[n]
@@ -634,19 +663,19 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str
     db = None if "db" not in need else db
     a_dx = a_dw = a_db = None
     dx_t = dw_t = MOE_BF16
-    with _on(stream, dev):
+    with _HERE if stream is None else _on(stream, dev):
         if "dx" in need:
             if dx is None:
                 dx = torch.empty((T, K), dtype=x.dtype if dx_dtype is None else dx_dtype, device=dev)
-            a_dx, dx_t = _arg(dx, "dx", (T, K), (_F32, _BF16), dev), _dtype_code(dx)
+            a_dx, dx_t = _arg(dx, "dx", (T, K), (_F32, _BF16), at), _dtype_code(dx)
         if "dw" in need:
             if dw is None:
                 dw = torch.empty((R, K), dtype=dw_dtype, device=dev)
-            a_dw, dw_t = _arg(dw, "dw", (R, K), (_F32, _BF16), dev), _dtype_code(dw)
+            a_dw, dw_t = _arg(dw, "dw", (R, K), (_F32, _BF16), at), _dtype_code(dw)
         if "db" in need:
             if db is None:
                 db = torch.empty(R, dtype=_F32, device=dev)
-            a_db = _arg(db, "db", (R,), (_F32,), dev)
+            a_db = _arg(db, "db", (R,), (_F32,), at)
         x_t, dy_t = _dtype_code(x), _dtype_code(dy)
         ws, a_ws, n_ws = _ws(ws, int(lib.moe_linear_backward_workspace_bytes(T, K, N, code, dy_t, x_t, dx_t, dw_t,
                                                                              bits)), dev)
