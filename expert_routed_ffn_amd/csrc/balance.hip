@@ -13,12 +13,10 @@
 // columns in every row of its wave, so the column sums of p stay in registers too and reach memory once per
 // workgroup.  No atomics on floats: counts are integer LDS atomics, sums go through fixed-order partials, and two
 // calls on the same inputs give the same bits.
-#include "internal.hpp"
+#include "wave_dev.hpp"
 
 namespace moe {
 namespace {
-
-constexpr float kNegInf = -__builtin_huge_valf();
 
 // e^t for t <= 0 from the hardware's 2^h: the part of t log2(e) that h = fl(t log2 e) rounds off is put back to first
 // order, 2^(h + l) = 2^h (1 + l ln 2 + O(l^2)) with |l| below 2^-17.  Without it the relative error grows with |t|
@@ -29,29 +27,6 @@ __device__ __forceinline__ float exp_neg(float t) {
   const float l = __builtin_fmaf(t, 1.92596299e-8f, __builtin_fmaf(t, 1.44269502f, -h));
   const float r = __builtin_amdgcn_exp2f(h);
   return __builtin_fmaf(r, l * 0.693147181f, r);
-}
-
-// Sum or maximum over the wave, in every lane: four shifts within rows of 16 lanes, two broadcasts across rows, all on
-// the vector ALU (butterflies through LDS took the loss of an 8,192 x 512 chunk 18.6 us, these 7).
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp(float v, float other) {
-  return __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(other), __float_as_uint(v), CTRL, ROWS, 0xF, false));
-}
-template <typename Op>
-__device__ __forceinline__ float wave_all(float v, float unit, Op op) {
-  v = op(v, dpp<0x111, 0xF>(v, unit));  // row_shr:1
-  v = op(v, dpp<0x112, 0xF>(v, unit));
-  v = op(v, dpp<0x114, 0xF>(v, unit));
-  v = op(v, dpp<0x118, 0xF>(v, unit));
-  v = op(v, dpp<0x142, 0xA>(v, unit));  // lane 15 of rows 0 and 2 to rows 1 and 3
-  v = op(v, dpp<0x143, 0xC>(v, unit));  // lane 31 to rows 2 and 3
-  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
-}
-__device__ __forceinline__ float wave_sum(float v) {
-  return wave_all(v, 0.0f, [](float a, float b) { return a + b; });
-}
-__device__ __forceinline__ float wave_max(float v) {
-  return wave_all(v, kNegInf, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // Which columns a lane owns: with VEC (E % 4 == 0, 16-byte aligned rows) value i is column 256 (i / 4) + 4 lane +

@@ -65,6 +65,7 @@ struct Epi {
   int act;
   int res_bf16, y_bf16;
   int vec;            // rows start on 16-byte (fp32) / 8-byte (bf16) boundaries and N % 4 == 0
+  int vec_part;       // the same of the parts' rows, which are padded: false for SwiGLU's up columns behind odd N
 };
 
 __device__ __forceinline__ float load_any(const void* p, int bf16, size_t i) {
@@ -160,22 +161,43 @@ __device__ __forceinline__ void epi_rows_act(const Epi& e, int m, int n, int row
 }
 template <bool PAIR, int STEP, typename Value>
 __device__ __forceinline__ void epi_rows(const Epi& e, int m, int n, int rows, Value value) {
-  if (!e.vec) {
-    for (int d = 0; d < rows; d += STEP) {
-      float z[4], zu[4] = {0.f, 0.f, 0.f, 0.f};
-      value(d, z, zu);
+  if (PAIR) epi_rows_act<PAIR, STEP, MOE_ACT_SWIGLU>(e, m, n, rows, value);
+  else if (e.act == MOE_ACT_GELU) epi_rows_act<PAIR, STEP, MOE_ACT_GELU>(e, m, n, rows, value);
+  else if (e.act == MOE_ACT_SILU) epi_rows_act<PAIR, STEP, MOE_ACT_SILU>(e, m, n, rows, value);
+  else epi_rows_act<PAIR, STEP, MOE_ACT_NONE>(e, m, n, rows, value);
+}
+// The same element by element, for results whose rows do not start on such boundaries (odd N, odd addresses): columns
+// n, n + CSTEP, n + 2 CSTEP, n + 3 CSTEP, those below N, of rows m, m + STEP, ...; value(d, j, z, zu).  With CSTEP the
+// number of threads on a row, neighbouring threads store neighbouring elements.
+template <bool PAIR, int STEP, int CSTEP, typename Value>
+__device__ __forceinline__ void epi_rows_single(const Epi& e, int m, int n, int rows, Value value) {
+  float b[4], bu[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (n + r < e.N) epi_one(e, m + d, n + r, z[r], zu[r]);
+  for (int j = 0; j < 4; ++j) {
+    const bool in = e.bias && n + CSTEP * j < e.N;
+    b[j] = in ? e.bias[n + CSTEP * j] : 0.0f;
+    bu[j] = PAIR && in ? e.bias[e.N + n + CSTEP * j] : 0.0f;
+  }
+  size_t i = (size_t)m * e.N + n, ip = (size_t)m * e.R + n;
+  for (int d = 0; d < rows; d += STEP) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (n + CSTEP * j < e.N) {
+        float z, zu = 0.0f;
+        value(d, j, z, zu);
+        z += b[j];
+        zu += bu[j];
+        if (e.pre) {
+          store_any(e.pre, e.y_bf16, ip + CSTEP * j, z);
+          if (PAIR) store_any(e.pre, e.y_bf16, ip + CSTEP * j + e.N, zu);
+        }
+        float v = PAIR ? z * sigmoid(z) * zu : act_value(e.act, z);
+        if (e.res) v += load_any(e.res, e.res_bf16, i + CSTEP * j);
+        store_any(e.y, e.y_bf16, i + CSTEP * j, v);
+      }
     }
-  } else if (PAIR) {
-    epi_rows_act<PAIR, STEP, MOE_ACT_SWIGLU>(e, m, n, rows, value);
-  } else if (e.act == MOE_ACT_GELU) {
-    epi_rows_act<PAIR, STEP, MOE_ACT_GELU>(e, m, n, rows, value);
-  } else if (e.act == MOE_ACT_SILU) {
-    epi_rows_act<PAIR, STEP, MOE_ACT_SILU>(e, m, n, rows, value);
-  } else {
-    epi_rows_act<PAIR, STEP, MOE_ACT_NONE>(e, m, n, rows, value);
+    i += (size_t)STEP * e.N;
+    ip += (size_t)STEP * e.R;
   }
 }
 

@@ -19,14 +19,21 @@
 namespace moe {
 namespace {
 
-constexpr int kPrepRows = 64, kPrepCols = 256;  // of dy per workgroup: 32 threads of 8 columns by 8 rows at a time
+// Of dy per workgroup: 32 threads of 8 columns by 8 rows at a time, up to 64 rows; fewer where that leaves less than
+// 512 workgroups (8,192 x 512 SwiGLU: 18 us with 64 rows, 12.5 with 32; 333 x 201: 31 us with 64, 6.6 with 8).
+constexpr int kPrepCols = 256;
+int prep_rows(int T, int N) {
+  int rows = 64;
+  while (rows > 8 && ceil_div(T, rows) * ceil_div(N, kPrepCols) < 512) rows /= 2;
+  return rows;
+}
 
 struct Prep {
   const void *dy, *pre;
   uint16_t* dz;            // planes [T][ldz], or null
   int64_t dz_plane;
   float* db_part;          // [row tiles][R], or null
-  int T, N, R, ldz, terms;
+  int T, N, R, ldz, terms, rows;
   int act, bf16;           // dy's and pre's type
   int vec;                 // N % 8 == 0 and dy and pre start on 16-byte boundaries
   int blocks, tiles_n;
@@ -36,9 +43,11 @@ struct Prep {
   int x_terms;
 };
 
-// 8 values from element i on, those past `valid` as zeros.
-__device__ __forceinline__ void load8_any(const void* p, int bf16, size_t i, int vec, int valid, float (&v)[8]) {
-  if (vec && valid >= 8) {
+// A thread's 8 values of a row: with VEC the 8 columns from `i` on in one 16-byte load or two, otherwise (odd N, odd
+// addresses) columns i, i + 32, ..., so that neighbouring threads read neighbouring elements; those past N as zeros.
+template <bool VEC>
+__device__ __forceinline__ void load8_any(const void* p, int bf16, size_t i, int left, float (&v)[8]) {
+  if constexpr (VEC) {
     if (bf16) {
       const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i);
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -53,15 +62,15 @@ __device__ __forceinline__ void load8_any(const void* p, int bf16, size_t i, int
       v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
       v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     }
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int r = 0; r < 8; ++r) v[r] = r < valid ? load_any(p, bf16, i + r) : 0.0f;
+    for (int r = 0; r < 8; ++r) v[r] = 32 * r < left ? load_any(p, bf16, i + 32 * r) : 0.0f;
+  }
 }
 
-// 8 values as terms at element `at` of each plane.
-__device__ __forceinline__ void write8(uint16_t* dst, int64_t plane, int terms, size_t at, int aligned, int valid,
-                                       const float (&v)[8]) {
+// Those 8 values as terms at element `at` of each plane.
+template <bool VEC>
+__device__ __forceinline__ void write8(uint16_t* dst, int64_t plane, int terms, size_t at, int left, const float (&v)[8]) {
   uint16_t t[8][3];
 #pragma unroll
   for (int i = 0; i < 8; ++i) bf16_terms(v[i], t[i]);
@@ -69,36 +78,35 @@ __device__ __forceinline__ void write8(uint16_t* dst, int64_t plane, int terms, 
   for (int k = 0; k < 3; ++k) {
     if (k >= terms) continue;
     uint16_t* o = dst + k * plane + at;
-    if (aligned && valid >= 8) {
+    if constexpr (VEC) {
       *reinterpret_cast<uint4*>(o) =
           make_uint4(t[0][k] | (uint32_t)t[1][k] << 16, t[2][k] | (uint32_t)t[3][k] << 16,
                      t[4][k] | (uint32_t)t[5][k] << 16, t[6][k] | (uint32_t)t[7][k] << 16);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < valid) o[i] = t[i][k];
+        if (32 * i < left) o[32 * i] = t[i][k];
     }
   }
 }
 
-template <bool PAIR>
+template <bool PAIR, bool VEC>
 __device__ void prep_dz(const Prep& p, int b, float (&sums)[2][8][kPrepCols]) {
   const int tid = threadIdx.x;
   const int tt = b / p.tiles_n, n0 = (b % p.tiles_n) * kPrepCols;
-  const int cx = (tid & 31) * 8, ry = tid >> 5, n = n0 + cx;
-  const int valid = max(0, min(8, p.N - n));
-  const int t_end = min(p.T, (tt + 1) * kPrepRows);
+  const int ry = tid >> 5, cx = VEC ? (tid & 31) * 8 : tid & 31, n = n0 + cx, left = p.N - n;
+  const int t_first = tt * p.rows + ry, t_end = min(p.T, (tt + 1) * p.rows);
   float sa[8], su[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sa[j] = su[j] = 0.0f;
-  if (valid) {
-    for (int t = tt * kPrepRows + ry; t < t_end; t += 8) {
+  if (left > 0) {
+    for (int t = t_first; t < t_end; t += 8) {
       float g[8], a[8], u[8];
-      load8_any(p.dy, p.bf16, (size_t)t * p.N + n, p.vec, valid, g);
+      load8_any<VEC>(p.dy, p.bf16, (size_t)t * p.N + n, left, g);
       if constexpr (PAIR) {
         float zg[8], zu[8];
-        load8_any(p.pre, p.bf16, (size_t)t * p.R + n, p.vec, valid, zg);
-        load8_any(p.pre, p.bf16, (size_t)t * p.R + p.N + n, p.vec, valid, zu);
+        load8_any<VEC>(p.pre, p.bf16, (size_t)t * p.R + n, left, zg);
+        load8_any<VEC>(p.pre, p.bf16, (size_t)t * p.R + p.N + n, left, zu);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float h = sigmoid(zg[j]);
@@ -110,32 +118,33 @@ __device__ void prep_dz(const Prep& p, int b, float (&sums)[2][8][kPrepCols]) {
         for (int j = 0; j < 8; ++j) a[j] = g[j];
       } else {
         float z[8];
-        load8_any(p.pre, p.bf16, (size_t)t * p.N + n, p.vec, valid, z);
+        load8_any<VEC>(p.pre, p.bf16, (size_t)t * p.N + n, left, z);
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] = g[j] * act_slope(p.act, z[j]);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (j < valid) {
+        if (VEC || 32 * j < left) {
           sa[j] += a[j];
           if (PAIR) su[j] += u[j];
         }
       }
       if (p.dz) {
         const size_t at = (size_t)t * p.ldz + n;
-        write8(p.dz, p.dz_plane, p.terms, at, 1, valid, a);
-        if constexpr (PAIR) write8(p.dz, p.dz_plane, p.terms, at + p.N, p.N % 8 == 0, valid, u);
-        if (n + 8 >= p.N)  // the last columns' thread also fills the row's padding
-          for (int c = p.R; c < p.ldz; ++c)
-            for (int k = 0; k < p.terms; ++k) p.dz[k * p.dz_plane + (size_t)t * p.ldz + c] = 0;
+        write8<VEC>(p.dz, p.dz_plane, p.terms, at, left, a);
+        if constexpr (PAIR) write8<VEC>(p.dz, p.dz_plane, p.terms, at + p.N, left, u);
       }
     }
   }
+  if (!VEC && p.dz && n0 + kPrepCols >= p.N && (tid & 31) < p.ldz - p.R)  // the rows' padding: at most 7 columns
+    for (int t = t_first; t < t_end; t += 8)
+      for (int k = 0; k < p.terms; ++k) p.dz[k * p.dz_plane + (size_t)t * p.ldz + p.R + (tid & 31)] = 0;
   if (!p.db_part) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    sums[0][ry][cx + j] = sa[j];
-    if (PAIR) sums[1][ry][cx + j] = su[j];
+    const int c = VEC ? cx + j : cx + 32 * j;
+    sums[0][ry][c] = sa[j];
+    if (PAIR) sums[1][ry][c] = su[j];
   }
   __syncthreads();
 #pragma unroll
@@ -151,7 +160,7 @@ template <bool PAIR>
 __global__ __launch_bounds__(256) void linear_prep_kernel(Prep p) {
   __shared__ float sums[2][8][kPrepCols];
   if ((int)blockIdx.x < p.blocks) {
-    prep_dz<PAIR>(p, blockIdx.x, sums);
+    p.vec ? prep_dz<PAIR, true>(p, blockIdx.x, sums) : prep_dz<PAIR, false>(p, blockIdx.x, sums);
     return;
   }
   const int64_t step = (int64_t)(gridDim.x - p.blocks) * 256;
@@ -203,7 +212,7 @@ GradPlan grad_plan(int T, int K, int N, int act, moe_dtype dy_t, moe_dtype x_t, 
   GradPlan p{};
   p.R = act == MOE_ACT_SWIGLU ? 2 * N : N;
   p.ldr = (int)(ceil_div(p.R, 8) * 8);
-  p.tiles_t = (int)ceil_div(T, kPrepRows);
+  p.tiles_t = (int)ceil_div(T, prep_rows(T, N));
   p.dx = need & MOE_NEED_DX;
   p.dw = need & MOE_NEED_DW;
   p.db = need & MOE_NEED_DB;
@@ -278,6 +287,7 @@ moe_status launch_linear_backward(const void* dy, moe_dtype dy_t, const void* pr
   p.bf16 = dy_t == MOE_BF16;
   p.ldz = pl.ldr;
   p.terms = pl.terms;
+  p.rows = prep_rows(T, N);
   p.dz_plane = (int64_t)T * pl.ldr;
   if ((pl.dx || pl.dw) && !direct) p.dz = u16(pl.dz);
   if (pl.db) p.db_part = f32(pl.db_part);
@@ -323,7 +333,7 @@ moe_status launch_linear_backward(const void* dy, moe_dtype dy_t, const void* pr
     q.split = split;
     q.partial = partial;
     q.ldp = K;
-    q.epi = Epi{nullptr, nullptr, out, nullptr, K, K, MOE_ACT_NONE, 0, out_t == MOE_BF16, 0};
+    q.epi = Epi{nullptr, nullptr, out, nullptr, K, K, MOE_ACT_NONE, 0, out_t == MOE_BF16, 0, 0};
     g[count++] = q;
   };
   if (pl.dw)

@@ -153,7 +153,7 @@ struct Operand<ROWS, THREADS, true> {  // [k][m]
   }
 };
 
-// Four columns n ... of a part's row, those below N.
+// Four columns n ... of a part's row: with vec all of them (rows are padded to 4), else those below N.
 __device__ __forceinline__ void put_part(float* out, int n, int N, int vec, const float (&z)[4]) {
   if (vec) {
     if (n < N) *reinterpret_cast<float4*>(out) = make_float4(z[0], z[1], z[2], z[3]);
@@ -321,12 +321,21 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
       for (int d = 0; d < rows; d += kStep) {
         float z[4], zu[4];
         value(d, z, zu);
-        put_part(out, n, p.epi.N, p.epi.vec, z);
-        if constexpr (PAIR) put_part(out + p.epi.N, n, p.epi.N, p.epi.vec, zu);
+        put_part(out, n, p.epi.N, p.epi.vec_part, z);
+        if constexpr (PAIR) put_part(out + p.epi.N, n, p.epi.N, p.epi.vec_part, zu);
         out += (size_t)kStep * p.ldp;
       }
-    } else {
+    } else if (p.epi.vec) {
       epi_rows<PAIR, kStep>(p.epi, m, n, rows, value);
+    } else {
+      auto single = [&](int d, int j, float& z, float& zu) {  // row r0 + d, column n0 + o + kOutPieces j
+        const int r = r0 + d, l = o + kOutPieces * j, at = l >> 2;
+        const int c1 = PAIR ? (at / kH) * 2 * kH + at % kH : at;
+        z = tile_c[(r * kPieces + (c1 ^ (r & 15))) * 4 + (l & 3)];
+        if constexpr (PAIR) zu = tile_c[(r * kPieces + ((c1 + kH) ^ (r & 15))) * 4 + (l & 3)];
+      };
+      const int first = n0 + o;
+      epi_rows_single<PAIR, kStep, kOutPieces>(p.epi, m, first, first < p.epi.N ? min(kPassRows - r0, p.M - m) : 0, single);
     }
   }
 }
@@ -363,7 +372,7 @@ __global__ __launch_bounds__(256) void join_kernel(Join jn) {
     float z[4] = {0.f, 0.f, 0.f, 0.f}, zu[4] = {0.f, 0.f, 0.f, 0.f};
     const size_t step = (size_t)p.M * p.ldp;
     const float* in = p.partial + (size_t)m * p.ldp + n;
-    if (p.epi.vec) {
+    if (p.epi.vec_part) {
 #pragma unroll 4
       for (int s = 0; s < p.split; ++s) {
         const float4 q = *reinterpret_cast<const float4*>(in + s * step);
@@ -390,8 +399,12 @@ __global__ __launch_bounds__(256) void join_kernel(Join jn) {
         u[r] = zu[r];
       }
     };
-    if (pair) epi_rows<true, 1>(p.epi, m, n, 1, value);
-    else epi_rows<false, 1>(p.epi, m, n, 1, value);
+    const auto single = [&](int, int r, float& a, float& u) {
+      a = z[r];
+      u = zu[r];
+    };
+    if (p.epi.vec) pair ? epi_rows<true, 1>(p.epi, m, n, 1, value) : epi_rows<false, 1>(p.epi, m, n, 1, value);
+    else pair ? epi_rows_single<true, 1, 1>(p.epi, m, n, 1, single) : epi_rows_single<false, 1, 1>(p.epi, m, n, 1, single);
     return;
   }
   // 64 columns a workgroup; its four waves take every fourth row, and their sums are added in wave order
@@ -477,6 +490,7 @@ moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool g
   Join j{};
   for (int i = 0; i < count; ++i) {
     p[i].epi.vec = epi_vec(p[i].epi);
+    p[i].epi.vec_part = p[i].epi.act != MOE_ACT_SWIGLU || p[i].epi.N % 4 == 0;
     blocks[i] = tiles_of(Shape{p[i].M, p[i].R, p[i].K, p[i].nseg}, side) * p[i].split;
     // (SwiGLU tiles hold half as many output columns, of which there are half as many as rows of W)
     if (p[i].epi.act == MOE_ACT_SWIGLU) blocks[i] = ceil_div(p[i].M, side) * ceil_div(p[i].epi.N, side / 2) * p[i].split;
