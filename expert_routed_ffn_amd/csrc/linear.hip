@@ -194,7 +194,7 @@ moe_status launch_linear(const void* x, moe_dtype x_t, const uint16_t* w, const 
                          const void* residual, moe_dtype r_t, int T, int K, int N, void* y, moe_dtype y_t, void* pre,
                          void* ws, hipStream_t s) {
   const LinearPlan pl = linear_plan(T, K, N, act, x_t, y_t);
-  Epi e{bias, residual, y, pre, N, pl.R, act, r_t == MOE_BF16, y_t == MOE_BF16, 0, 0};
+  Epi e{bias, residual, y, pre, N, pl.R, act, r_t == MOE_BF16, y_t == MOE_BF16};
   if (pl.few) {
     const dim3 grid((unsigned)ceil_div(N, act == MOE_ACT_SWIGLU ? 8 : 16));
     auto go = [&](auto kernel) { launch_k(MOE_KERNEL_LINEAR, kernel, grid, dim3(64 * kFewWaves), 0, s, x, w, T, K, e); };

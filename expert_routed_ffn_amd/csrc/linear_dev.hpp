@@ -55,6 +55,33 @@ __device__ __forceinline__ float act_slope(int act, float z) {
   return 1.0f;
 }
 
+// Four or eight consecutive elements of a row at any element boundary: global memory takes 8- and 16-byte accesses at
+// addresses that are only aligned to their elements, so rows of odd length cost no more than others.  (Element by
+// element, an 8,192 x 1,001 result took 66 us against 44 with 1,000 columns, and its gradient's first launch 47 against
+// 20.)
+typedef uint32_t u32x2_at2_t __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x4_at2_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_at4_t __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ void load4(const void* p, int bf16, size_t i, float (&v)[4]) {
+  if (bf16) {
+    const u32x2_at2_t q = *reinterpret_cast<const u32x2_at2_t*>(reinterpret_cast<const uint16_t*>(p) + i);
+    v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xFFFF0000u);
+  } else {
+    const u32x4_at4_t q = *reinterpret_cast<const u32x4_at4_t*>(reinterpret_cast<const float*>(p) + i);
+    v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y); v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
+  }
+}
+__device__ __forceinline__ void store4(void* p, int bf16, size_t i, const float (&v)[4]) {
+  if (bf16)
+    *reinterpret_cast<u32x2_at2_t*>(reinterpret_cast<uint16_t*>(p) + i) =
+        u32x2_at2_t{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
+  else
+    *reinterpret_cast<u32x4_at4_t*>(reinterpret_cast<float*>(p) + i) =
+        u32x4_at4_t{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+}
+
 // What becomes of an element z of the product: y = act(z + bias) + residual, z + bias kept in `pre`.
 struct Epi {
   const float* bias;  // [R] or null
@@ -64,8 +91,6 @@ struct Epi {
   int N, R;           // output columns; product columns (2 N for SwiGLU, else N)
   int act;
   int res_bf16, y_bf16;
-  int vec;            // rows start on 16-byte (fp32) / 8-byte (bf16) boundaries and N % 4 == 0
-  int vec_part;       // the same of the parts' rows, which are padded: false for SwiGLU's up columns behind odd N
 };
 
 __device__ __forceinline__ float load_any(const void* p, int bf16, size_t i) {
@@ -75,13 +100,6 @@ __device__ __forceinline__ void store_any(void* p, int bf16, size_t i, float v) 
   if (bf16) reinterpret_cast<uint16_t*>(p)[i] = f32_to_bf16(v);
   else reinterpret_cast<float*>(p)[i] = v;
 }
-__device__ __forceinline__ void store4(void* p, int bf16, size_t i, const float (&v)[4]) {
-  if (bf16)
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + i) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
-  else
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
-}
-
 // One element; zu is the up value of a SwiGLU pair.
 __device__ __forceinline__ void epi_one(const Epi& e, int m, int n, float z, float zu) {
   const bool pair = e.act == MOE_ACT_SWIGLU;
@@ -98,21 +116,16 @@ __device__ __forceinline__ void epi_one(const Epi& e, int m, int n, float z, flo
   if (e.res) v += load_any(e.res, e.res_bf16, i);
   store_any(e.y, e.y_bf16, i, v);
 }
-// Columns n .. n + 3 (n % 4 == 0, n < N; those past N are left out) of rows m, m + STEP, ...: `rows` rows from m on,
-// whose products value(d, z, zu) gives for row m + d.  Addresses advance by a constant and the flags are the same for
-// all threads, so what a row costs is its loads, its stores and the activation; residuals of four rows are read ahead.
-// (With addresses computed for each row, 64-bit products among them, the epilogue of an 8,192 x 1,024 result took 9 us
-// longer.)
+// Columns n .. n + 3 (n < N; those past N are left out) of rows m, m + STEP, ...: `rows` rows from m on, whose products
+// value(d, z, zu) gives for row m + d.  Addresses advance by a constant and the flags are the same for all threads, so
+// what a row costs is its loads, its stores and the activation; residuals of four rows are read ahead.  (With addresses
+// computed for each row, 64-bit products among them, the epilogue of an 8,192 x 1,024 result took 9 us longer.)
 template <bool PAIR, int STEP, int ACT, typename Value>
 __device__ __forceinline__ void epi_rows_act(const Epi& e, int m, int n, int rows, Value value) {
   float b[4] = {0.f, 0.f, 0.f, 0.f}, bu[4] = {0.f, 0.f, 0.f, 0.f};
   if (e.bias) {
-    const float4 q = *reinterpret_cast<const float4*>(e.bias + n);
-    b[0] = q.x; b[1] = q.y; b[2] = q.z; b[3] = q.w;
-    if constexpr (PAIR) {
-      const float4 u = *reinterpret_cast<const float4*>(e.bias + e.N + n);
-      bu[0] = u.x; bu[1] = u.y; bu[2] = u.z; bu[3] = u.w;
-    }
+    load4(e.bias, 0, n, b);
+    if constexpr (PAIR) load4(e.bias, 0, (size_t)e.N + n, bu);
   }
   size_t i = (size_t)m * e.N + n, ip = (size_t)m * e.R + n;
   const size_t di = (size_t)STEP * e.N, dp = (size_t)STEP * e.R;
@@ -121,16 +134,7 @@ __device__ __forceinline__ void epi_rows_act(const Epi& e, int m, int n, int row
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       res[k][0] = res[k][1] = res[k][2] = res[k][3] = 0.0f;
-      if (e.res && d + k * STEP < rows) {
-        if (e.res_bf16) {
-          const uint2 q = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(e.res) + i + k * di);
-          res[k][0] = __uint_as_float(q.x << 16); res[k][1] = __uint_as_float(q.x & 0xFFFF0000u);
-          res[k][2] = __uint_as_float(q.y << 16); res[k][3] = __uint_as_float(q.y & 0xFFFF0000u);
-        } else {
-          const float4 q = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(e.res) + i + k * di);
-          res[k][0] = q.x; res[k][1] = q.y; res[k][2] = q.z; res[k][3] = q.w;
-        }
-      }
+      if (e.res && d + k * STEP < rows) load4(e.res, e.res_bf16, i + k * di, res[k]);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -161,43 +165,22 @@ __device__ __forceinline__ void epi_rows_act(const Epi& e, int m, int n, int row
 }
 template <bool PAIR, int STEP, typename Value>
 __device__ __forceinline__ void epi_rows(const Epi& e, int m, int n, int rows, Value value) {
-  if (PAIR) epi_rows_act<PAIR, STEP, MOE_ACT_SWIGLU>(e, m, n, rows, value);
-  else if (e.act == MOE_ACT_GELU) epi_rows_act<PAIR, STEP, MOE_ACT_GELU>(e, m, n, rows, value);
-  else if (e.act == MOE_ACT_SILU) epi_rows_act<PAIR, STEP, MOE_ACT_SILU>(e, m, n, rows, value);
-  else epi_rows_act<PAIR, STEP, MOE_ACT_NONE>(e, m, n, rows, value);
-}
-// The same element by element, for results whose rows do not start on such boundaries (odd N, odd addresses): columns
-// n, n + CSTEP, n + 2 CSTEP, n + 3 CSTEP, those below N, of rows m, m + STEP, ...; value(d, j, z, zu).  With CSTEP the
-// number of threads on a row, neighbouring threads store neighbouring elements.
-template <bool PAIR, int STEP, int CSTEP, typename Value>
-__device__ __forceinline__ void epi_rows_single(const Epi& e, int m, int n, int rows, Value value) {
-  float b[4], bu[4];
+  if (n + 4 > e.N) {  // the last columns of rows whose length is no multiple of 4
+    for (int d = 0; d < rows; d += STEP) {
+      float z[4], zu[4] = {0.f, 0.f, 0.f, 0.f};
+      value(d, z, zu);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const bool in = e.bias && n + CSTEP * j < e.N;
-    b[j] = in ? e.bias[n + CSTEP * j] : 0.0f;
-    bu[j] = PAIR && in ? e.bias[e.N + n + CSTEP * j] : 0.0f;
-  }
-  size_t i = (size_t)m * e.N + n, ip = (size_t)m * e.R + n;
-  for (int d = 0; d < rows; d += STEP) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (n + CSTEP * j < e.N) {
-        float z, zu = 0.0f;
-        value(d, j, z, zu);
-        z += b[j];
-        zu += bu[j];
-        if (e.pre) {
-          store_any(e.pre, e.y_bf16, ip + CSTEP * j, z);
-          if (PAIR) store_any(e.pre, e.y_bf16, ip + CSTEP * j + e.N, zu);
-        }
-        float v = PAIR ? z * sigmoid(z) * zu : act_value(e.act, z);
-        if (e.res) v += load_any(e.res, e.res_bf16, i + CSTEP * j);
-        store_any(e.y, e.y_bf16, i + CSTEP * j, v);
-      }
+      for (int r = 0; r < 3; ++r)
+        if (n + r < e.N) epi_one(e, m + d, n + r, z[r], zu[r]);
     }
-    i += (size_t)STEP * e.N;
-    ip += (size_t)STEP * e.R;
+  } else if (PAIR) {
+    epi_rows_act<PAIR, STEP, MOE_ACT_SWIGLU>(e, m, n, rows, value);
+  } else if (e.act == MOE_ACT_GELU) {
+    epi_rows_act<PAIR, STEP, MOE_ACT_GELU>(e, m, n, rows, value);
+  } else if (e.act == MOE_ACT_SILU) {
+    epi_rows_act<PAIR, STEP, MOE_ACT_SILU>(e, m, n, rows, value);
+  } else {
+    epi_rows_act<PAIR, STEP, MOE_ACT_NONE>(e, m, n, rows, value);
   }
 }
 
@@ -213,7 +196,7 @@ struct Prob {
   uint32_t sa, sb;         // two bits per segment: its plane of A and of B
   int split;               // parts of the reduction, each a workgroup
   float* partial;          // [split][M][ldp] when split > 1
-  int ldp;                 // R rounded up to 4
+  int ldp;                 // elements per row of a part
   Epi epi;
 };
 struct Join {  // sums of partials: up to two products, and column sums

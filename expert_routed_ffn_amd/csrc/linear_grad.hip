@@ -35,7 +35,6 @@ struct Prep {
   float* db_part;          // [row tiles][R], or null
   int T, N, R, ldz, terms, rows;
   int act, bf16;           // dy's and pre's type
-  int vec;                 // N % 8 == 0 and dy and pre start on 16-byte boundaries
   int blocks, tiles_n;
   const float* x;          // fp32 activations to `x_terms` planes, or null
   uint16_t* xt;
@@ -43,13 +42,11 @@ struct Prep {
   int x_terms;
 };
 
-// A thread's 8 values of a row: with VEC the 8 columns from `i` on in one 16-byte load or two, otherwise (odd N, odd
-// addresses) columns i, i + 32, ..., so that neighbouring threads read neighbouring elements; those past N as zeros.
-template <bool VEC>
-__device__ __forceinline__ void load8_any(const void* p, int bf16, size_t i, int left, float (&v)[8]) {
-  if constexpr (VEC) {
+// Columns i ... i + 8 of a row, those past `left` as zeros.
+__device__ __forceinline__ void load8(const void* p, int bf16, size_t i, int left, float (&v)[8]) {
+  if (left >= 8) {
     if (bf16) {
-      const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i);
+      const u32x4_at2_t q = *reinterpret_cast<const u32x4_at2_t*>(reinterpret_cast<const uint16_t*>(p) + i);
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -57,19 +54,22 @@ __device__ __forceinline__ void load8_any(const void* p, int bf16, size_t i, int
         v[2 * r + 1] = __uint_as_float(w[r] & 0xFFFF0000u);
       }
     } else {
-      const float4 a = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i)[0];
-      const float4 b = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i)[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      float a[4], b[4];
+      load4(p, 0, i, a);
+      load4(p, 0, i + 4, b);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        v[r] = a[r];
+        v[4 + r] = b[r];
+      }
     }
   } else {
 #pragma unroll
-    for (int r = 0; r < 8; ++r) v[r] = 32 * r < left ? load_any(p, bf16, i + 32 * r) : 0.0f;
+    for (int r = 0; r < 8; ++r) v[r] = r < left ? load_any(p, bf16, i + r) : 0.0f;
   }
 }
 
 // Those 8 values as terms at element `at` of each plane.
-template <bool VEC>
 __device__ __forceinline__ void write8(uint16_t* dst, int64_t plane, int terms, size_t at, int left, const float (&v)[8]) {
   uint16_t t[8][3];
 #pragma unroll
@@ -78,23 +78,23 @@ __device__ __forceinline__ void write8(uint16_t* dst, int64_t plane, int terms, 
   for (int k = 0; k < 3; ++k) {
     if (k >= terms) continue;
     uint16_t* o = dst + k * plane + at;
-    if constexpr (VEC) {
-      *reinterpret_cast<uint4*>(o) =
-          make_uint4(t[0][k] | (uint32_t)t[1][k] << 16, t[2][k] | (uint32_t)t[3][k] << 16,
-                     t[4][k] | (uint32_t)t[5][k] << 16, t[6][k] | (uint32_t)t[7][k] << 16);
+    if (left >= 8) {
+      *reinterpret_cast<u32x4_at2_t*>(o) =
+          u32x4_at2_t{t[0][k] | (uint32_t)t[1][k] << 16, t[2][k] | (uint32_t)t[3][k] << 16,
+                      t[4][k] | (uint32_t)t[5][k] << 16, t[6][k] | (uint32_t)t[7][k] << 16};
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (32 * i < left) o[32 * i] = t[i][k];
+      for (int i = 0; i < 7; ++i)
+        if (i < left) o[i] = t[i][k];
     }
   }
 }
 
-template <bool PAIR, bool VEC>
+template <bool PAIR>
 __device__ void prep_dz(const Prep& p, int b, float (&sums)[2][8][kPrepCols]) {
   const int tid = threadIdx.x;
   const int tt = b / p.tiles_n, n0 = (b % p.tiles_n) * kPrepCols;
-  const int ry = tid >> 5, cx = VEC ? (tid & 31) * 8 : tid & 31, n = n0 + cx, left = p.N - n;
+  const int ry = tid >> 5, cx = (tid & 31) * 8, n = n0 + cx, left = p.N - n;
   const int t_first = tt * p.rows + ry, t_end = min(p.T, (tt + 1) * p.rows);
   float sa[8], su[8];
 #pragma unroll
@@ -102,11 +102,11 @@ __device__ void prep_dz(const Prep& p, int b, float (&sums)[2][8][kPrepCols]) {
   if (left > 0) {
     for (int t = t_first; t < t_end; t += 8) {
       float g[8], a[8], u[8];
-      load8_any<VEC>(p.dy, p.bf16, (size_t)t * p.N + n, left, g);
+      load8(p.dy, p.bf16, (size_t)t * p.N + n, left, g);
       if constexpr (PAIR) {
         float zg[8], zu[8];
-        load8_any<VEC>(p.pre, p.bf16, (size_t)t * p.R + n, left, zg);
-        load8_any<VEC>(p.pre, p.bf16, (size_t)t * p.R + p.N + n, left, zu);
+        load8(p.pre, p.bf16, (size_t)t * p.R + n, left, zg);
+        load8(p.pre, p.bf16, (size_t)t * p.R + p.N + n, left, zu);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float h = sigmoid(zg[j]);
@@ -118,33 +118,32 @@ __device__ void prep_dz(const Prep& p, int b, float (&sums)[2][8][kPrepCols]) {
         for (int j = 0; j < 8; ++j) a[j] = g[j];
       } else {
         float z[8];
-        load8_any<VEC>(p.pre, p.bf16, (size_t)t * p.N + n, left, z);
+        load8(p.pre, p.bf16, (size_t)t * p.N + n, left, z);
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] = g[j] * act_slope(p.act, z[j]);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (VEC || 32 * j < left) {
+        if (j < left) {
           sa[j] += a[j];
           if (PAIR) su[j] += u[j];
         }
       }
       if (p.dz) {
         const size_t at = (size_t)t * p.ldz + n;
-        write8<VEC>(p.dz, p.dz_plane, p.terms, at, left, a);
-        if constexpr (PAIR) write8<VEC>(p.dz, p.dz_plane, p.terms, at + p.N, left, u);
+        write8(p.dz, p.dz_plane, p.terms, at, left, a);
+        if constexpr (PAIR) write8(p.dz, p.dz_plane, p.terms, at + p.N, left, u);
+        if (left <= 8)  // the last columns' thread also fills the row's padding
+          for (int c = p.R; c < p.ldz; ++c)
+            for (int k = 0; k < p.terms; ++k) p.dz[k * p.dz_plane + (size_t)t * p.ldz + c] = 0;
       }
     }
   }
-  if (!VEC && p.dz && n0 + kPrepCols >= p.N && (tid & 31) < p.ldz - p.R)  // the rows' padding: at most 7 columns
-    for (int t = t_first; t < t_end; t += 8)
-      for (int k = 0; k < p.terms; ++k) p.dz[k * p.dz_plane + (size_t)t * p.ldz + p.R + (tid & 31)] = 0;
   if (!p.db_part) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int c = VEC ? cx + j : cx + 32 * j;
-    sums[0][ry][c] = sa[j];
-    if (PAIR) sums[1][ry][c] = su[j];
+    sums[0][ry][cx + j] = sa[j];
+    if (PAIR) sums[1][ry][cx + j] = su[j];
   }
   __syncthreads();
 #pragma unroll
@@ -160,7 +159,7 @@ template <bool PAIR>
 __global__ __launch_bounds__(256) void linear_prep_kernel(Prep p) {
   __shared__ float sums[2][8][kPrepCols];
   if ((int)blockIdx.x < p.blocks) {
-    p.vec ? prep_dz<PAIR, true>(p, blockIdx.x, sums) : prep_dz<PAIR, false>(p, blockIdx.x, sums);
+    prep_dz<PAIR>(p, blockIdx.x, sums);
     return;
   }
   const int64_t step = (int64_t)(gridDim.x - p.blocks) * 256;
@@ -291,7 +290,6 @@ moe_status launch_linear_backward(const void* dy, moe_dtype dy_t, const void* pr
   p.dz_plane = (int64_t)T * pl.ldr;
   if ((pl.dx || pl.dw) && !direct) p.dz = u16(pl.dz);
   if (pl.db) p.db_part = f32(pl.db_part);
-  p.vec = N % 8 == 0 && (reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(pre)) % 16 == 0;
   p.tiles_n = (int)ceil_div(N, kPrepCols);
   const int64_t blocks = p.dz || p.db_part ? (int64_t)p.tiles_n * pl.tiles_t : 0;
   int64_t x_blocks = 0;
@@ -333,7 +331,7 @@ moe_status launch_linear_backward(const void* dy, moe_dtype dy_t, const void* pr
     q.split = split;
     q.partial = partial;
     q.ldp = K;
-    q.epi = Epi{nullptr, nullptr, out, nullptr, K, K, MOE_ACT_NONE, 0, out_t == MOE_BF16, 0, 0};
+    q.epi = Epi{nullptr, nullptr, out, nullptr, K, K, MOE_ACT_NONE, 0, out_t == MOE_BF16};
     g[count++] = q;
   };
   if (pl.dw)

@@ -153,13 +153,13 @@ struct Operand<ROWS, THREADS, true> {  // [k][m]
   }
 };
 
-// Four columns n ... of a part's row: with vec all of them (rows are padded to 4), else those below N.
-__device__ __forceinline__ void put_part(float* out, int n, int N, int vec, const float (&z)[4]) {
-  if (vec) {
-    if (n < N) *reinterpret_cast<float4*>(out) = make_float4(z[0], z[1], z[2], z[3]);
+// Four columns n ... of a part's row, those below N.
+__device__ __forceinline__ void put_part(float* out, int n, int N, const float (&z)[4]) {
+  if (n + 4 <= N) {
+    store4(out, 0, 0, z);
   } else {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < 3; ++r)
       if (n + r < N) out[r] = z[r];
   }
 }
@@ -321,21 +321,12 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
       for (int d = 0; d < rows; d += kStep) {
         float z[4], zu[4];
         value(d, z, zu);
-        put_part(out, n, p.epi.N, p.epi.vec_part, z);
-        if constexpr (PAIR) put_part(out + p.epi.N, n, p.epi.N, p.epi.vec_part, zu);
+        put_part(out, n, p.epi.N, z);
+        if constexpr (PAIR) put_part(out + p.epi.N, n, p.epi.N, zu);
         out += (size_t)kStep * p.ldp;
       }
-    } else if (p.epi.vec) {
-      epi_rows<PAIR, kStep>(p.epi, m, n, rows, value);
     } else {
-      auto single = [&](int d, int j, float& z, float& zu) {  // row r0 + d, column n0 + o + kOutPieces j
-        const int r = r0 + d, l = o + kOutPieces * j, at = l >> 2;
-        const int c1 = PAIR ? (at / kH) * 2 * kH + at % kH : at;
-        z = tile_c[(r * kPieces + (c1 ^ (r & 15))) * 4 + (l & 3)];
-        if constexpr (PAIR) zu = tile_c[(r * kPieces + ((c1 + kH) ^ (r & 15))) * 4 + (l & 3)];
-      };
-      const int first = n0 + o;
-      epi_rows_single<PAIR, kStep, kOutPieces>(p.epi, m, first, first < p.epi.N ? min(kPassRows - r0, p.M - m) : 0, single);
+      epi_rows<PAIR, kStep>(p.epi, m, n, rows, value);
     }
   }
 }
@@ -372,20 +363,23 @@ __global__ __launch_bounds__(256) void join_kernel(Join jn) {
     float z[4] = {0.f, 0.f, 0.f, 0.f}, zu[4] = {0.f, 0.f, 0.f, 0.f};
     const size_t step = (size_t)p.M * p.ldp;
     const float* in = p.partial + (size_t)m * p.ldp + n;
-    if (p.epi.vec_part) {
+    if (n + 4 <= p.epi.N) {
 #pragma unroll 4
       for (int s = 0; s < p.split; ++s) {
-        const float4 q = *reinterpret_cast<const float4*>(in + s * step);
-        z[0] += q.x; z[1] += q.y; z[2] += q.z; z[3] += q.w;
+        float q[4];
+        load4(in + s * step, 0, 0, q);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z[r] += q[r];
         if (pair) {
-          const float4 u = *reinterpret_cast<const float4*>(in + s * step + p.epi.N);
-          zu[0] += u.x; zu[1] += u.y; zu[2] += u.z; zu[3] += u.w;
+          load4(in + s * step, 0, p.epi.N, q);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) zu[r] += q[r];
         }
       }
     } else {
       for (int s = 0; s < p.split; ++s) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 3; ++r)
           if (n + r < p.epi.N) {
             z[r] += in[s * step + r];
             if (pair) zu[r] += in[s * step + p.epi.N + r];
@@ -399,12 +393,7 @@ __global__ __launch_bounds__(256) void join_kernel(Join jn) {
         u[r] = zu[r];
       }
     };
-    const auto single = [&](int, int r, float& a, float& u) {
-      a = z[r];
-      u = zu[r];
-    };
-    if (p.epi.vec) pair ? epi_rows<true, 1>(p.epi, m, n, 1, value) : epi_rows<false, 1>(p.epi, m, n, 1, value);
-    else pair ? epi_rows_single<true, 1, 1>(p.epi, m, n, 1, single) : epi_rows_single<false, 1, 1>(p.epi, m, n, 1, single);
+    pair ? epi_rows<true, 1>(p.epi, m, n, 1, value) : epi_rows<false, 1>(p.epi, m, n, 1, value);
     return;
   }
   // 64 columns a workgroup; its four waves take every fourth row, and their sums are added in wave order
@@ -419,11 +408,6 @@ __global__ __launch_bounds__(256) void join_kernel(Join jn) {
   part[wave][lane] = v;
   __syncthreads();
   if (wave == 0 && c < jn.db_n) jn.db[c] = part[0][lane] + part[1][lane] + part[2][lane] + part[3][lane];
-}
-
-bool epi_vec(const Epi& e) {
-  auto ok = [](const void* q, int bf16) { return reinterpret_cast<uintptr_t>(q) % (bf16 ? 8 : 16) == 0; };
-  return e.N % 4 == 0 && ok(e.y, e.y_bf16) && ok(e.pre, e.y_bf16) && ok(e.res, e.res_bf16) && ok(e.bias, 0);
 }
 
 int64_t tiles_of(const Shape& s, int side) { return ceil_div(s.M, side) * ceil_div(s.R, side); }
@@ -489,8 +473,6 @@ moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool g
   int64_t blocks[2] = {0, 0};
   Join j{};
   for (int i = 0; i < count; ++i) {
-    p[i].epi.vec = epi_vec(p[i].epi);
-    p[i].epi.vec_part = p[i].epi.act != MOE_ACT_SWIGLU || p[i].epi.N % 4 == 0;
     blocks[i] = tiles_of(Shape{p[i].M, p[i].R, p[i].K, p[i].nseg}, side) * p[i].split;
     // (SwiGLU tiles hold half as many output columns, of which there are half as many as rows of W)
     if (p[i].epi.act == MOE_ACT_SWIGLU) blocks[i] = ceil_div(p[i].M, side) * ceil_div(p[i].epi.N, side / 2) * p[i].split;
