@@ -212,7 +212,7 @@ struct Shape {
   int M, R, K, nseg;
 };
 struct Plan {
-  int large;     // 256 x 256 tiles
+  int shape;     // 64, 128 or 256 squared tiles
   int split[2];
 };
 Plan plan_products(const Shape* s, int count);

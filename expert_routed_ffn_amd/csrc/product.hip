@@ -9,8 +9,7 @@
 // 241 us on 8192 x 4096 x 4096).  Tiles go from memory straight to LDS (16 bytes a lane, two buffers of 64 k), and
 // the step's loop is turned so that neither the loads nor the LDS reads are waited for with the matrix units idle:
 // fragments of one 32-k half are read while the other half is multiplied, and the barrier that hands over the buffers
-// stands before the last half's products.  Memory latency behind deeper rings (3 or 4 buffers of 32 k) measured no
-// better.
+// stands before the last half's products.
 //
 // LDS places: 64 banks of 4 bytes serve 16 lanes of a 16-byte read at once.  [m][k] tiles are rows of 128 bytes whose
 // 16-byte piece c lies at c ^ (row / 2 % 8): the 16 rows that such a group reads at one piece fall on 16 different
@@ -18,9 +17,10 @@
 // ds_read_b64_tr_b16, where 16 lanes take 4 k of 16 columns and each receives its column's 4 values; the 32-byte
 // stretch s of row k lies at s ^ (k % 4 + 4 (k / 8 % 2)), which spreads the 8 rows that 32 lanes touch over 256 bytes.
 //
-// Two tile shapes.  256 x 256 (8 waves, 128 KB of LDS, one workgroup per CU) reads half as much per product as
-// 128 x 128 (4 waves, two workgroups per CU), but needs enough tiles to fill 256 CUs evenly: see
-// plan_products.
+// Three tile shapes, chosen by plan_products.  256 x 256 (8 waves, 128 KB of LDS, one workgroup per CU) reads half as
+// much per product as 128 x 128 (4 waves, two workgroups per CU), but needs enough tiles to fill 256 CUs evenly.  64 x 64
+// tiles are for products of few tiles, whose time is the latency of their loads: four buffers keep three steps' loads
+// under way.  (Rings of 3 or 4 buffers of 32 k under the large tiles measured no better than two of 64.)
 #include <algorithm>
 
 #include "linear_dev.hpp"
@@ -31,17 +31,18 @@ namespace {
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 constexpr int kBK = 64;
 
-template <int TM_, int TN_, int WM_, int WN_>
+template <int TM_, int TN_, int WM_, int WN_, int BUFFERS = 2>
 struct Tile {
-  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_;
+  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, kRing = BUFFERS;
   static constexpr int kThreads = 64 * WM * WN;
   static constexpr int kFM = TM / WM / 16, kFN = TN / WN / 16;  // 16 x 16 fragments per wave
   static constexpr int kStage = (TM + TN) * kBK;                // bf16 values of one buffer
-  static constexpr int kBuffers = 2 * kStage * 2;               // bytes
+  static constexpr int kBuffers = kRing * kStage * 2;           // bytes
   // the fp32 tile passes through the same LDS, in one piece or by rows of waves
   static constexpr int kPasses = TM * TN * 4 <= 64 * 1024 ? 1 : WM;
   static constexpr int kLds = std::max(kBuffers, TM * TN * 4 / kPasses);
 };
+using Tiny = Tile<64, 64, 2, 2, 4>;
 using Small = Tile<128, 128, 2, 2>;
 using Large = Tile<256, 256, 2, 4>;
 static_assert(Small::kLds <= 80 * 1024 && Large::kLds <= 160 * 1024, "LDS of a CU");
@@ -114,11 +115,16 @@ struct Operand<ROWS, THREADS, false> {  // [m][k]
 template <int ROWS, int THREADS>
 struct Operand<ROWS, THREADS, true> {  // [k][m]
   static constexpr int kSlots = ROWS / 8, kPer = THREADS / kSlots, kLoads = kBK / kPer;  // 16-byte pieces of a row; k per load
+  static_assert(kPer % 16 == 0, "the turn repeats");
   uint32_t off;
+  // what row k's stretches are turned by; of 64 columns two rows fill 256 bytes, so every other k turns
+  static __device__ __forceinline__ int turn(int k_mod4, int k8) {
+    return ROWS >= 128 ? k_mod4 | k8 << 2 : k_mod4 >> 1 | k8 << 1;
+  }
   template <typename Row>
   __device__ __forceinline__ void init(int ld, int cols, Row) {
     const int k = threadIdx.x / kSlots, s = threadIdx.x % kSlots;
-    const int c = s ^ (((k & 3) | ((k >> 1) & 4)) << 1);  // kPer is a multiple of 16: the same for each load
+    const int c = s ^ (turn(k & 3, (k >> 3) & 1) << 1);  // kPer is a multiple of 16: the same for each load
     // `cols` columns are there from the tile's first on (a multiple of 8); further ones repeat the last and are not stored
     off = (uint32_t)k * ld + min(c * 8, cols - 8);
   }
@@ -140,7 +146,7 @@ struct Operand<ROWS, THREADS, true> {  // [k][m]
   template <int F>
   __device__ __forceinline__ void read(const uint16_t* lds, int base, int kk, bf16x8_t (&f)[F]) const {
     const int l16 = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
-    const int g = (l16 >> 2) | (q & 1) << 2;
+    const int g = turn(l16 >> 2, q & 1);
     // lane l16 of a group of 16 reads 4 columns (l16 % 4) of k = 8 q + l16 / 4 (then 4 further) and gets column l16
     const uint16_t* p = lds + (32 * kk + 8 * q + (l16 >> 2)) * ROWS + (l16 & 3) * 4;
 #pragma unroll
@@ -261,7 +267,31 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  if (lo < hi) {
+  if constexpr (T::kRing > 2) {
+    // Few tiles: the time is the latency of the loads, so kRing - 1 steps of them are kept under way.  A step's own have
+    // landed once no more are outstanding than the later steps issued; the tail's go through registers, whose wait
+    // covers all loads before them.
+    constexpr int kPer = decltype(A)::kLoads + decltype(B)::kLoads, kLeft = (T::kRing - 2) * kPer;
+    static_assert(kLeft < 16, "vmcnt's low bits");
+    if (lo < hi) {
+#pragma unroll
+      for (int i = 0; i < T::kRing - 1; ++i) load(i);
+      int now = 0, free = T::kRing - 1;
+      for (int s = lo; s < hi; ++s) {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x0070 | kLeft);  // vmcnt(kLeft) lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        load(free);
+        read(now, 0, 0);
+        read(now, 1, 1);
+        mma(0);
+        mma(1);
+        now = now + 1 == T::kRing ? 0 : now + 1;
+        free = free + 1 == T::kRing ? 0 : free + 1;
+      }
+    }
+  } else if (lo < hi) {
     load(0);
     hand_over();
     load(1);
@@ -413,9 +443,10 @@ __global__ __launch_bounds__(256) void join_kernel(Join jn) {
 int64_t tiles_of(const Shape& s, int side) { return ceil_div(s.M, side) * ceil_div(s.R, side); }
 int64_t steps_of(const Shape& s) { return ceil_div(s.K, kBK) * s.nseg; }
 
-// Time of a launch in microseconds, from measurements of both tile shapes over 1 to 64 K-steps and 64 to 1,024 tiles:
+// Time of a launch in microseconds, from measurements of the tile shapes over 1 to 64 K-steps and 32 to 4,096 tiles:
 // a workgroup costs a start and an epilogue besides its K-steps, less of each while it has a CU to itself, and a cut
 // reduction costs a second launch and its parts' way through memory.
+//   500 x 2048 x 1024: 64 x 64 tiles 12.1 us, 128 x 128 22.1;  65 x 4096 x 4096: 64 x 64 20.8 us, in four parts 14.6
 //   8192 x 2048 x 1024: 128 x 128 tiles 37.5 us, 256 x 256 (half the CUs idle) 54, in two parts 41 + 15 for the join
 //   8192 x 1024 x 2048: 43.8 against 38.8;  8192 x 4096 x 4096: 261 against 224
 //   1024 x 8192 x 2048 in parts: one 117, two 57, four 47 us
@@ -424,7 +455,7 @@ struct Rates {
   double start, step;           // with all slots taken
   double start_alone, step_alone;  // up to half of them
 };
-constexpr Rates kRates[2] = {{512, 128, 7.5, 0.85, 4.5, 0.60}, {256, 256, 13.0, 1.50, 10.5, 1.19}};
+constexpr Rates kRates[3] = {{512, 64, 2.2, 0.40, 1.9, 0.262}, {512, 128, 3.5, 0.96, 2.7, 0.58}, {256, 256, 13.0, 1.50, 10.5, 1.19}};
 
 double cost_of(const Rates& r, const Shape* s, const int* split, int count) {
   int64_t blocks = 0;
@@ -452,13 +483,13 @@ double cost_of(const Rates& r, const Shape* s, const int* split, int count) {
 Plan plan_products(const Shape* s, int count) {
   Plan best{};
   double least = 0;
-  for (int large = 0; large < 2; ++large)
+  for (int shape = 0; shape < 3; ++shape)
     for (int share = 1 << 20; share >= 8; share = share > 128 ? 128 : share / 2) {  // K-steps of a part, about
       Plan p{};
-      p.large = large;
+      p.shape = shape;
       for (int i = 0; i < count; ++i)
         p.split[i] = (int)std::max<int64_t>(1, std::min<int64_t>(16, (steps_of(s[i]) + share / 2) / share));
-      const double c = cost_of(kRates[large], s, p.split, count);
+      const double c = cost_of(kRates[shape], s, p.split, count);
       if (least == 0 || c < least) {
         least = c;
         best = p;
@@ -469,7 +500,7 @@ Plan plan_products(const Shape* s, int count) {
 
 moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool grad, bool first_is_dw,
                            const float* db_part, int db_rows, int db_n, float* db, hipStream_t s, const char* what) {
-  const int side = plan.large ? 256 : 128;
+  const int side = kRates[plan.shape].side;
   int64_t blocks[2] = {0, 0};
   Join j{};
   for (int i = 0; i < count; ++i) {
@@ -488,11 +519,15 @@ moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool g
       launch_k(kid, kernel, grid, dim3((unsigned)threads), 0, s, p[0], p[count - 1], n);
     };
     const bool pair = p[0].epi.act == MOE_ACT_SWIGLU;
-    if (grad) plan.large ? bwd(grad_products_kernel<Large>, Large::kThreads) : bwd(grad_products_kernel<Small>, Small::kThreads);
-    else if (plan.large && pair) fwd(linear_product_kernel<Large, true>, Large::kThreads);
-    else if (plan.large) fwd(linear_product_kernel<Large, false>, Large::kThreads);
-    else if (pair) fwd(linear_product_kernel<Small, true>, Small::kThreads);
-    else fwd(linear_product_kernel<Small, false>, Small::kThreads);
+    auto go = [&](auto tile) {
+      using T = decltype(tile);
+      if (grad) bwd(grad_products_kernel<T>, T::kThreads);
+      else if (pair) fwd(linear_product_kernel<T, true>, T::kThreads);
+      else fwd(linear_product_kernel<T, false>, T::kThreads);
+    };
+    if (plan.shape == 0) go(Tiny{});
+    else if (plan.shape == 1) go(Small{});
+    else go(Large{});
     if (moe_status st = check_launch(what)) return st;
   }
   j.db_part = db_part;
