@@ -101,6 +101,11 @@ struct Operand<ROWS, THREADS, false> {  // [m][k]
       *reinterpret_cast<uint4*>(lds + (i * THREADS + threadIdx.x) * 8) = v;
     }
   }
+  // a last step of 32 k whose second half is not multiplied: its place takes the first half's values again
+  __device__ __forceinline__ void load_half(const uint16_t* p, int, uint16_t* lds, int w64) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) to_lds16(p + off[i] - (chunk >= 4 ? 32 : 0), lds + (i * THREADS + w64) * 8);
+  }
   template <int F>
   __device__ __forceinline__ void read(const uint16_t* lds, int base, int kk, bf16x8_t (&f)[F]) const {
     const int r16 = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
@@ -142,6 +147,12 @@ struct Operand<ROWS, THREADS, true> {  // [k][m]
       const uint4 v = in ? *reinterpret_cast<const uint4*>(p + off + (uint32_t)i * kPer * ld) : make_uint4(0, 0, 0, 0);
       *reinterpret_cast<uint4*>(lds + (i * THREADS + threadIdx.x) * 8) = v;
     }
+  }
+  __device__ __forceinline__ void load_half(const uint16_t* p, int ld, uint16_t* lds, int w64) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      to_lds16(p + off + (uint32_t)i * kPer * ld - (i * kPer + (int)threadIdx.x / kSlots >= 32 ? 32u * ld : 0u),
+               lds + (i * THREADS + w64) * 8);
   }
   template <int F>
   __device__ __forceinline__ void read(const uint16_t* lds, int base, int kk, bf16x8_t (&f)[F]) const {
@@ -203,6 +214,8 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
   uint16_t* const base = reinterpret_cast<uint16_t*>(lds);
   int seg = uniform(lo / seg_steps), kstep = lo - seg * seg_steps, next = lo;  // the step that is loaded next
   const int last = p.K - kBK;
+  // a last step of 32 k needs no zeros where its second half can be left out: the ring's loop does
+  const bool half_end = T::kRing > 2 && p.K % kBK == 32;
   const uint16_t *src_a, *src_b;
   auto place = [&] {
     src_a = A.at(p.A + ((p.sa >> (2 * seg)) & 3) * p.a_plane, m0, kstep * kBK, p.lda);
@@ -217,6 +230,9 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
     if (k0 <= last) {
       A.load(src_a, p.lda, la, 64 * wave);
       B.load(src_b, p.ldb, lb, 64 * wave);
+    } else if (half_end) {
+      A.load_half(src_a, p.lda, la, 64 * wave);
+      B.load_half(src_b, p.ldb, lb, 64 * wave);
     } else {
       A.load_tail(src_a, p.lda, p.K - k0, la);
       B.load_tail(src_b, p.ldb, p.K - k0, lb);
@@ -269,14 +285,14 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
   };
   if constexpr (T::kRing > 2) {
     // Few tiles: the time is the latency of the loads, so kRing - 1 steps of them are kept under way.  A step's own have
-    // landed once no more are outstanding than the later steps issued; the tail's go through registers, whose wait
+    // landed once no more are outstanding than the later steps issued; where a tail's go through registers, their wait
     // covers all loads before them.
     constexpr int kPer = decltype(A)::kLoads + decltype(B)::kLoads, kLeft = (T::kRing - 2) * kPer;
     static_assert(kLeft < 16, "vmcnt's low bits");
     if (lo < hi) {
 #pragma unroll
       for (int i = 0; i < T::kRing - 1; ++i) load(i);
-      int now = 0, free = T::kRing - 1;
+      int now = 0, free = T::kRing - 1, left = seg_steps - lo % seg_steps;  // steps to the segment's end
       for (int s = lo; s < hi; ++s) {
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(0x0070 | kLeft);  // vmcnt(kLeft) lgkmcnt(0)
@@ -286,7 +302,12 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
         read(now, 0, 0);
         read(now, 1, 1);
         mma(0);
-        mma(1);
+        if (--left == 0) {
+          left = seg_steps;
+          if (!half_end) mma(1);
+        } else {
+          mma(1);
+        }
         now = now + 1 == T::kRing ? 0 : now + 1;
         free = free + 1 == T::kRing ? 0 : free + 1;
       }
@@ -455,7 +476,7 @@ struct Rates {
   double start, step;           // with all slots taken
   double start_alone, step_alone;  // up to half of them
 };
-constexpr Rates kRates[3] = {{512, 64, 2.2, 0.40, 1.9, 0.262}, {512, 128, 3.5, 0.96, 2.7, 0.58}, {256, 256, 13.0, 1.50, 10.5, 1.19}};
+constexpr Rates kRates[3] = {{512, 64, 2.2, 0.40, 1.9, 0.262}, {512, 128, 3.5, 0.99, 2.7, 0.58}, {256, 256, 13.0, 1.50, 10.5, 1.19}};
 
 double cost_of(const Rates& r, const Shape* s, const int* split, int count) {
   int64_t blocks = 0;

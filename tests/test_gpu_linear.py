@@ -55,7 +55,7 @@ def test_linear(moe, T, K, N, act):
 
 
 GRAD_SHAPES = [(1, 32, 1), (3, 96, 7), (16, 64, 64), (65, 160, 19), (63, 32, 130), (128, 544, 8), (200, 224, 201),
-               (700, 96, 36)]
+               (700, 96, 36), (160, 64, 96), (96, 32, 32)]
 
 
 @pytest.mark.parametrize("T,K,N", GRAD_SHAPES)
