@@ -84,6 +84,13 @@ moe_status check_shape(const char* fn, int H, int I, int bits) {
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
+// Whether two buffers (null: none) share a byte.
+bool overlap(const void* p, uint64_t n, const void* q, uint64_t m) {
+  if (!p || !q || n == 0 || m == 0) return false;
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return a < b + m && b < a + n;
+}
+
 }  // namespace
 
 extern "C" {
@@ -387,6 +394,11 @@ moe_status moe_route_backward(const float* logits, const int32_t* ids, const flo
   if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(w, 4) || !aligned(dw, 4) || !aligned(lse, 4) ||
       !aligned(counts, 4) || !aligned(dloss, 4) || !aligned(dlogits, 4))
     return fail(MOE_EINVAL, "moe_route_backward: misaligned buffer");
+  const uint64_t te = (uint64_t)T * E * 4, tk = (uint64_t)T * k * 4;
+  if (overlap(dlogits, te, lse ? logits : nullptr, te) || overlap(dlogits, te, w, tk) || overlap(dlogits, te, dw, tk) ||
+      overlap(dlogits, te, w ? ids : nullptr, tk) || overlap(dlogits, te, lse, (uint64_t)T * 4) ||
+      overlap(dlogits, te, counts, (uint64_t)E * 4 + 4) || overlap(dlogits, te, dloss, 8))
+    return fail(MOE_EINVAL, "moe_route_backward: dlogits overlaps an input");
   return launch_route_backward(logits, ids, w, dw, lse, counts, dloss, T, E, k, dlogits, stream);
 }
 
@@ -403,6 +415,12 @@ moe_status moe_combine_backward(const void* y, moe_dtype y_t, const float* w, co
   if (!dout || (dw && !y) || (dy && !w)) return fail(MOE_EINVAL, "moe_combine_backward: null pointer");
   if (!aligned(y, 16) || !aligned(dy, 16) || !aligned(dout, 16) || !aligned(w, 4) || !aligned(dw, 4))
     return fail(MOE_EINVAL, "moe_combine_backward: misaligned buffer");
+  const uint64_t ny = (uint64_t)T * k * H * (y_t == MOE_F32 ? 4 : 2), nd = (uint64_t)T * H * (dout_t == MOE_F32 ? 4 : 2),
+                 nw = (uint64_t)T * k * 4;
+  if (overlap(dy, ny, dw ? y : nullptr, ny) || overlap(dy, ny, dout, nd) || overlap(dy, ny, w, nw) ||
+      overlap(dw, nw, y, ny) || overlap(dw, nw, dout, nd) || overlap(dw, nw, dy ? w : nullptr, nw) ||
+      overlap(dw, nw, dy, ny))
+    return fail(MOE_EINVAL, "moe_combine_backward: an output overlaps another buffer");
   return launch_combine_backward(y, y_t, w, dout, dout_t, T, k, H, dw, dy, stream);
 }
 
@@ -452,6 +470,15 @@ moe_status moe_linear(const void* x, moe_dtype x_t, const void* w, const float* 
   if (need > 0 && (!ws || ws_bytes < need))
     return fail(MOE_EWORKSPACE, fmt("moe_linear: workspace %lld bytes, needs %lld", (long long)ws_bytes,
                                     (long long)need));
+  const uint64_t R = act == MOE_ACT_SWIGLU ? 2 * (uint64_t)N : N;
+  const uint64_t nx = (uint64_t)T * K * elem(x_t), nw = R * K * 2, ny = (uint64_t)T * N * elem(y_t),
+                 np = (uint64_t)T * R * elem(y_t), nr = (uint64_t)T * N * elem(r_t);
+  const bool in_place = residual == y && r_t == y_t;
+  const void* const r = in_place ? nullptr : residual;
+  if (overlap(y, ny, x, nx) || overlap(y, ny, w, nw) || overlap(y, ny, bias, R * 4) || overlap(y, ny, r, nr) ||
+      overlap(y, ny, pre, np) || overlap(pre, np, x, nx) || overlap(pre, np, w, nw) || overlap(pre, np, bias, R * 4) ||
+      overlap(pre, np, residual, nr))
+    return fail(MOE_EINVAL, "moe_linear: an output overlaps another buffer (y may only be the residual itself)");
   return launch_linear(x, x_t, reinterpret_cast<const uint16_t*>(w), bias, act, residual, r_t, T, K, N, y, y_t, pre, ws,
                        stream);
 }
@@ -480,6 +507,22 @@ moe_status moe_linear_backward(const void* dy, moe_dtype dy_t, const void* pre, 
   if (need > 0 && (!ws || ws_bytes < need))
     return fail(MOE_EWORKSPACE, fmt("moe_linear_backward: workspace %lld bytes, needs %lld", (long long)ws_bytes,
                                     (long long)need));
+  const uint64_t R = act == MOE_ACT_SWIGLU ? 2 * (uint64_t)N : N;
+  struct Span {
+    const void* p;
+    uint64_t n;
+  };
+  const Span out[3] = {{dx, (uint64_t)T * K * elem(dx_t)}, {dw, R * K * elem(dw_t)}, {db, R * 4}};
+  const Span in[4] = {{dy, (uint64_t)T * N * elem(dy_t)},
+                      {act == MOE_ACT_NONE ? nullptr : pre, (uint64_t)T * R * elem(dy_t)},
+                      {dw ? x : nullptr, (uint64_t)T * K * elem(x_t)},
+                      {dx ? w : nullptr, R * K * 2}};
+  for (int i = 0; i < 3; ++i) {
+    bool bad = false;
+    for (const Span& s : in) bad = bad || overlap(out[i].p, out[i].n, s.p, s.n);
+    for (int j = 0; j < i; ++j) bad = bad || overlap(out[i].p, out[i].n, out[j].p, out[j].n);
+    if (bad) return fail(MOE_EINVAL, "moe_linear_backward: an output overlaps another buffer");
+  }
   return launch_linear_backward(dy, dy_t, pre, x, x_t, reinterpret_cast<const uint16_t*>(w), act, T, K, N, dx, dx_t, dw,
                                 dw_t, db, ws, stream);
 }

@@ -426,6 +426,7 @@ moe_status moe_route_backward(const float* logits, const int32_t* ids, const flo
  *   w     [T x k] fp32 (may be NULL without dy).
  *   dout  [T x H], dtype dout_t.
  * y, dy and dout must be 16-byte aligned, H a multiple of 4, k in [1, 16].
+ * Outputs may not overlap the inputs or each other.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED.
  */
 moe_status moe_combine_backward(const void* y, moe_dtype y_t, const float* w, const void* dout, moe_dtype dout_t,
@@ -473,7 +474,8 @@ enum { MOE_NEED_DX = 1, MOE_NEED_DW = 2, MOE_NEED_DB = 4 };
  *   db   NULL or [R] fp32 out.  With T == 0, dw and db are set to zero.
  *   ws   moe_linear_backward_workspace_bytes(...) bytes, 256-byte aligned, `need`
  *        the MOE_NEED_* bits of the outputs that are not NULL.
- * dx and dw must be 16-byte aligned.  Sums in fp32.  An fp32 dx or dw comes from dz (and x) at
+ * dx and dw must be 16-byte aligned; outputs may not overlap the inputs that are
+ * read or each other.  Sums in fp32.  An fp32 dx or dw comes from dz (and x) at
  * full precision; a bf16 one from dz rounded to bf16.
  * Errors: MOE_EINVAL (no output wanted among that), MOE_EUNSUPPORTED, MOE_EWORKSPACE.
  */

@@ -106,6 +106,37 @@ def test_linear_backward_no_rows_without_sums():
     assert _back(T=0, dw=None, db=None) == OK
 
 
+def _at(mb):
+    return ctypes.c_void_p(mb << 20)
+
+
+def test_overlapping_buffers_are_refused():
+    """Buffers at made-up addresses a MB apart (all needs here are far smaller); one of them moved onto another."""
+    def check(fn, names, call):
+        for a, b in names:
+            places = {n: _at(16 + i) for i, n in enumerate("abcdefghij")}
+            places[a] = ctypes.c_void_p(places[b].value + 16)
+            assert int(call(places)) == EINVAL, (fn, a, b)
+            assert b"overlap" in L.moe_last_error(), (fn, a, b)
+
+    # logits, ids, w, dw, lse, counts, dloss, dlogits = a .. h
+    check("route", [("h", "a"), ("h", "b"), ("h", "c"), ("h", "d"), ("h", "e"), ("h", "f")], lambda p: L.moe_route_backward(
+        p["a"], p["b"], p["c"], p["d"], p["e"], p["f"], p["g"], 64, 16, 4, p["h"], None))
+    # y, w, dout, dw, dy = a .. e
+    check("combine", [("e", "a"), ("e", "c"), ("d", "a"), ("d", "c"), ("d", "e")], lambda p: L.moe_combine_backward(
+        p["a"], F32, p["b"], p["c"], F32, 16, 4, 64, p["d"], p["e"], None) if p["a"].value % 16 == 0 else EINVAL)
+    # x, w, bias, residual, y, pre, ws = a .. g
+    check("linear", [("e", "a"), ("e", "b"), ("e", "d"), ("f", "a"), ("f", "d"), ("e", "f")], lambda p: L.moe_linear(
+        p["a"], BF16, p["b"], p["c"], 2, p["d"], BF16, 16, 64, 32, p["e"], BF16, p["f"], p["g"], 0, None))
+    # y on the residual is allowed only as the very buffer of the same type
+    assert int(L.moe_linear(_at(16), BF16, _at(17), None, 0, _at(18), F32, 16, 64, 32, _at(18), BF16, None, None, 0,
+                            None)) == EINVAL
+    # dy, pre, x, w, dx, dw, db = a .. g
+    check("backward", [("e", "a"), ("e", "b"), ("e", "c"), ("e", "d"), ("f", "a"), ("f", "c"), ("g", "a"), ("e", "f")],
+          lambda p: L.moe_linear_backward(p["a"], BF16, p["b"], p["c"], BF16, p["d"], 2, 16, 64, 32, p["e"], BF16, p["f"],
+                                          F32, p["g"], _at(64), 8 << 20, None))
+
+
 def test_workspaces():
     assert int(L.moe_balance_loss_workspace_bytes(0, 512)) == 0
     assert int(L.moe_balance_loss_workspace_bytes(12, 512)) == 0
