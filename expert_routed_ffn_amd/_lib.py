@@ -465,41 +465,35 @@ def _rows(t: torch.Tensor, name: str, dims: int):
     return t.shape
 
 
-def _ws(ws: torch.Tensor | None, need: int, device):
-    """The caller's workspace, or a new one of `need` bytes: (tensor to keep, address, bytes)."""
+def _ws(ws: torch.Tensor | None, need: int, like: torch.Tensor, index: int, stream):
+    """The caller's workspace, or a new one of `need` bytes on like's device: (tensor to keep, address, bytes)."""
     if ws is None:
         if need == 0:
             return None, None, 0
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = _new(like, need, torch.uint8, stream)
     else:
-        _arg(ws, "ws", ws.shape, (torch.uint8,), device.index)
+        _arg(ws, "ws", ws.shape, (torch.uint8,), index)
     return ws, ws.data_ptr(), ws.numel()
 
 
-class _Here:
-    """The context of a call on the current stream: nothing to switch."""
-
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_HERE = _Here()
-
-
-def _launch(fn, device, stream, *args):
-    """One library call on `stream` (or `device`'s current stream) with `device` current."""
-    index = device.index
-    s = _current_stream(index) if stream is None else _stream(stream, device)
+def _launch(fn, index: int, stream, *args):
+    """One library call on `stream` (or device `index`'s current stream) with that device current."""
+    s = _current_stream(index) if stream is None else _stream(stream, index)
     if index != _current_device():
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = fn(*args, s)
     else:
         status = fn(*args, s)
     if status != MOE_OK:
         _check(status)
+
+
+def _new(like: torch.Tensor, shape, dtype, stream):
+    """An uninitialised tensor on like's device, belonging to the stream that will write it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _on(stream, like.device):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def balance_loss(logits: torch.Tensor, ids: torch.Tensor, mask: torch.Tensor | None = None,
@@ -511,19 +505,17 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, mask: torch.Tensor | N
     T, E = _rows(logits, "logits", 2)
     k = _rows(ids, "ids", 2)[1]
     a_logits = _arg(logits, "logits", (T, E), (_F32,))
-    dev = logits.device
-    at = dev.index
+    at = logits.get_device()
     a_ids = _arg(ids, "ids", (T, k), (_I32,), at)
     a_mask = None if mask is None else _arg(mask, "mask", (T,), (torch.bool, torch.uint8), at)
-    with _HERE if stream is None else _on(stream, dev):
-        if loss is None:
-            loss = torch.empty(2, dtype=_F32, device=dev)
-        if counts is None:
-            counts = torch.empty(E + 1, dtype=_I32, device=dev)
-        if lse is None:
-            lse = torch.empty(T, dtype=_F32, device=dev)
-        ws, a_ws, n_ws = _ws(ws, int(lib.moe_balance_loss_workspace_bytes(T, E)), dev)
-    _launch(lib.moe_balance_loss, dev, stream, a_logits, a_ids, a_mask, T, E, k,
+    if loss is None:
+        loss = _new(logits, 2, _F32, stream)
+    if counts is None:
+        counts = _new(logits, E + 1, _I32, stream)
+    if lse is None:
+        lse = _new(logits, T, _F32, stream)
+    ws, a_ws, n_ws = _ws(ws, lib.moe_balance_loss_workspace_bytes(T, E), logits, at, stream)
+    _launch(lib.moe_balance_loss, at, stream, a_logits, a_ids, a_mask, T, E, k,
             _arg(loss, "loss", (2,), (_F32,), at), _arg(counts, "counts", (E + 1,), (_I32,), at),
             _arg(lse, "lse", (T,), (_F32,), at), a_ws, n_ws)
     return loss, counts, lse
@@ -540,13 +532,12 @@ def route_backward(logits: torch.Tensor, ids: torch.Tensor, w: torch.Tensor | No
     k = _rows(ids, "ids", 2)[1]
     if (w is None) != (dw is None):
         raise ValueError("w and dw go together")
-    if len({lse is None, counts is None, dloss is None}) != 1:
+    if (lse is None) != (counts is None) or (lse is None) != (dloss is None):
         raise ValueError("lse, counts and dloss go together")
     if w is None and lse is None:
         raise ValueError("neither gate weights (w, dw) nor losses (lse, counts, dloss)")
     a_logits = _arg(logits, "logits", (T, E), (_F32,))
-    dev = logits.device
-    at = dev.index
+    at = logits.get_device()
     a_ids = _arg(ids, "ids", (T, k), (_I32,), at)
     a_w = a_dw = a_lse = a_counts = a_dloss = None
     if w is not None:
@@ -555,11 +546,15 @@ def route_backward(logits: torch.Tensor, ids: torch.Tensor, w: torch.Tensor | No
         a_lse, a_counts = _arg(lse, "lse", (T,), (_F32,), at), _arg(counts, "counts", (E + 1,), (_I32,), at)
         a_dloss = _arg(dloss, "dloss", (2,), (_F32,), at)
     if dlogits is None:
-        with _HERE if stream is None else _on(stream, dev):
-            dlogits = torch.empty((T, E), dtype=_F32, device=dev)
-    _launch(lib.moe_route_backward, dev, stream, a_logits, a_ids, a_w, a_dw, a_lse, a_counts, a_dloss, T, E, k,
+        dlogits = _new(logits, (T, E), _F32, stream)
+    _launch(lib.moe_route_backward, at, stream, a_logits, a_ids, a_w, a_dw, a_lse, a_counts, a_dloss, T, E, k,
             _arg(dlogits, "dlogits", (T, E), (_F32,), at))
     return dlogits
+
+
+def _needs(need, names: tuple):
+    if not need or any(n not in names for n in need):
+        raise ValueError("need holds some of " + ", ".join(f'"{n}"' for n in names))
 
 
 def combine_backward(y: torch.Tensor, w: torch.Tensor, dout: torch.Tensor, dw: torch.Tensor | None = None,
@@ -567,35 +562,39 @@ def combine_backward(y: torch.Tensor, w: torch.Tensor, dout: torch.Tensor, dw: t
     """moe_combine_backward: (dw [T, k] fp32, dy [T, k, H] of y's type) from dout [T, H]; None for what `need` leaves
     out.  The gradient of combine's residual is dout itself."""
     T, k, H = _rows(y, "y", 3)
-    if not need or set(need) - {"dw", "dy"}:
-        raise ValueError('need holds "dw", "dy" or both')
+    _needs(need, ("dw", "dy"))
     a_y = _arg(y, "y", (T, k, H), (_F32, _BF16))
-    dev = y.device
-    at = dev.index
+    at = y.get_device()
     a_w, a_dout = _arg(w, "w", (T, k), (_F32,), at), _arg(dout, "dout", (T, H), (_F32, _BF16), at)
-    with _HERE if stream is None else _on(stream, dev):
-        if "dw" not in need:
-            dw = None
-        elif dw is None:
-            dw = torch.empty((T, k), dtype=_F32, device=dev)
-        if "dy" not in need:
-            dy = None
-        elif dy is None:
-            dy = torch.empty((T, k, H), dtype=y.dtype, device=dev)
-    _launch(lib.moe_combine_backward, dev, stream, a_y, _dtype_code(y), a_w, a_dout, _dtype_code(dout), T, k, H,
-            None if dw is None else _arg(dw, "dw", (T, k), (_F32,), at),
-            None if dy is None else _arg(dy, "dy", (T, k, H), (y.dtype,), at))
+    a_dw = a_dy = None
+    if "dw" in need:
+        if dw is None:
+            dw = _new(y, (T, k), _F32, stream)
+        a_dw = _arg(dw, "dw", (T, k), (_F32,), at)
+    else:
+        dw = None
+    if "dy" in need:
+        if dy is None:
+            dy = _new(y, (T, k, H), y.dtype, stream)
+        a_dy = _arg(dy, "dy", (T, k, H), (y.dtype,), at)
+    else:
+        dy = None
+    _launch(lib.moe_combine_backward, at, stream, a_y, _dtype_code(y), a_w, a_dout, _dtype_code(dout), T, k, H, a_dw,
+            a_dy)
     return dw, dy
 
 
 def _act_rows(w: torch.Tensor, act: str):
     """(activation code, output columns) of weight rows w."""
-    if act not in ACTS:
+    code = ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {', '.join(ACTS)}, got {act!r}")
     R = w.shape[0]
-    if act == "swiglu" and R % 2:
+    if code != 3:
+        return code, R
+    if R % 2:
         raise ValueError("swiglu needs an even number of weight rows (gate rows, then up rows)")
-    return ACTS[act], R // 2 if act == "swiglu" else R
+    return code, R // 2
 
 
 def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
@@ -605,32 +604,41 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, a
 
     w is bf16, x and residual fp32 or bf16, bias fp32, y of y_dtype (x's by default).  act is "none", "gelu" (tanh
     form), "silu" or "swiglu", whose w holds N gate rows, then N up rows (R = 2 N; else R = N).  `pre` [T, R], of y's
-    type, receives the values before the activation, which linear_backward needs."""
+    type, receives the values before the activation, which linear_backward needs.  y may be the residual itself."""
     T, K = _rows(x, "x", 2)
     R = _rows(w, "w", 2)[0]
     code, N = _act_rows(w, act)
     a_x = _arg(x, "x", (T, K), (_F32, _BF16))
-    dev = x.device
-    at = dev.index
+    at = x.get_device()
     a_w = _arg(w, "w", (R, K), (_BF16,), at)
     a_bias = None if bias is None else _arg(bias, "bias", (R,), (_F32,), at)
-    a_res = None if residual is None else _arg(residual, "residual", (T, N), (_F32, _BF16), at)
-    x_t, r_t = _dtype_code(x), MOE_F32 if residual is None else _dtype_code(residual)
-    with _HERE if stream is None else _on(stream, dev):
-        if y is None:
-            y = torch.empty((T, N), dtype=x.dtype if y_dtype is None else y_dtype, device=dev)
-        a_y, y_t = _arg(y, "y", (T, N), (_F32, _BF16), at), _dtype_code(y)
-        a_pre = None if pre is None else _arg(pre, "pre", (T, R), (y.dtype,), at)
-        ws, a_ws, n_ws = _ws(ws, int(lib.moe_linear_workspace_bytes(T, K, N, code, x_t, y_t)), dev)
-    _launch(lib.moe_linear, dev, stream, a_x, x_t, a_w, a_bias, code, a_res, r_t, T, K, N, a_y, y_t, a_pre, a_ws, n_ws)
+    a_res, r_t = None, MOE_F32
+    if residual is not None:
+        a_res, r_t = _arg(residual, "residual", (T, N), (_F32, _BF16), at), _dtype_code(residual)
+    x_t = _dtype_code(x)
+    if y is None:
+        y = _new(x, (T, N), x.dtype if y_dtype is None else y_dtype, stream)
+    a_y, y_t = _arg(y, "y", (T, N), (_F32, _BF16), at), _dtype_code(y)
+    a_pre = None if pre is None else _arg(pre, "pre", (T, R), (y.dtype,), at)
+    ws, a_ws, n_ws = _ws(ws, lib.moe_linear_workspace_bytes(T, K, N, code, x_t, y_t), x, at, stream)
+    _launch(lib.moe_linear, at, stream, a_x, x_t, a_w, a_bias, code, a_res, r_t, T, K, N, a_y, y_t, a_pre, a_ws, n_ws)
     return y
+
+
+def _size_codes(act: str, *dtypes):
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, got {act!r}")
+    for d in dtypes:
+        if d not in (_F32, _BF16):
+            raise TypeError(f"unsupported dtype {d} (float32 or bfloat16)")
+    return ACTS[act], [MOE_F32 if d == _F32 else MOE_BF16 for d in dtypes]
 
 
 def linear_workspace_bytes(T: int, K: int, N: int, act: str = "none", x_dtype=torch.bfloat16,
                            y_dtype=torch.bfloat16) -> int:
     """Bytes of linear's workspace for N output columns."""
-    t = {_F32: MOE_F32, _BF16: MOE_BF16}
-    return int(lib.moe_linear_workspace_bytes(T, K, N, ACTS[act], t[x_dtype], t[y_dtype]))
+    code, t = _size_codes(act, x_dtype, y_dtype)
+    return int(lib.moe_linear_workspace_bytes(T, K, N, code, *t))
 
 
 _NEED = {"dx": 1, "dw": 2, "db": 4}
@@ -646,40 +654,38 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str
     T, K = _rows(x, "x", 2)
     R = _rows(w, "w", 2)[0]
     code, N = _act_rows(w, act)
-    if not need or set(need) - set(_NEED):
-        raise ValueError('need holds some of "dx", "dw", "db"')
-    if act != "none" and pre is None:
+    _needs(need, ("dx", "dw", "db"))
+    if code and pre is None:
         raise ValueError(f"act {act!r} needs pre")
     a_dy = _arg(dy, "dy", (T, N), (_F32, _BF16))
-    dev = dy.device
-    at = dev.index
+    at = dy.get_device()
     a_x, a_w = _arg(x, "x", (T, K), (_F32, _BF16), at), _arg(w, "w", (R, K), (_BF16,), at)
-    a_pre = None if act == "none" else _arg(pre, "pre", (T, R), (dy.dtype,), at)
+    a_pre = _arg(pre, "pre", (T, R), (dy.dtype,), at) if code else None
     bits = 0
-    for n in need:
-        bits |= _NEED[n]
-    dx = None if "dx" not in need else dx
-    dw = None if "dw" not in need else dw
-    db = None if "db" not in need else db
     a_dx = a_dw = a_db = None
     dx_t = dw_t = MOE_BF16
-    with _HERE if stream is None else _on(stream, dev):
-        if "dx" in need:
-            if dx is None:
-                dx = torch.empty((T, K), dtype=x.dtype if dx_dtype is None else dx_dtype, device=dev)
-            a_dx, dx_t = _arg(dx, "dx", (T, K), (_F32, _BF16), at), _dtype_code(dx)
-        if "dw" in need:
-            if dw is None:
-                dw = torch.empty((R, K), dtype=dw_dtype, device=dev)
-            a_dw, dw_t = _arg(dw, "dw", (R, K), (_F32, _BF16), at), _dtype_code(dw)
-        if "db" in need:
-            if db is None:
-                db = torch.empty(R, dtype=_F32, device=dev)
-            a_db = _arg(db, "db", (R,), (_F32,), at)
-        x_t, dy_t = _dtype_code(x), _dtype_code(dy)
-        ws, a_ws, n_ws = _ws(ws, int(lib.moe_linear_backward_workspace_bytes(T, K, N, code, dy_t, x_t, dx_t, dw_t,
-                                                                             bits)), dev)
-    _launch(lib.moe_linear_backward, dev, stream, a_dy, dy_t, a_pre, a_x, x_t, a_w, code, T, K, N, a_dx, dx_t, a_dw,
+    if "dx" in need:
+        if dx is None:
+            dx = _new(x, (T, K), x.dtype if dx_dtype is None else dx_dtype, stream)
+        a_dx, dx_t, bits = _arg(dx, "dx", (T, K), (_F32, _BF16), at), _dtype_code(dx), 1
+    else:
+        dx = None
+    if "dw" in need:
+        if dw is None:
+            dw = _new(x, (R, K), dw_dtype, stream)
+        a_dw, dw_t, bits = _arg(dw, "dw", (R, K), (_F32, _BF16), at), _dtype_code(dw), bits | 2
+    else:
+        dw = None
+    if "db" in need:
+        if db is None:
+            db = _new(x, R, _F32, stream)
+        a_db, bits = _arg(db, "db", (R,), (_F32,), at), bits | 4
+    else:
+        db = None
+    x_t, dy_t = _dtype_code(x), _dtype_code(dy)
+    ws, a_ws, n_ws = _ws(ws, lib.moe_linear_backward_workspace_bytes(T, K, N, code, dy_t, x_t, dx_t, dw_t, bits), x, at,
+                         stream)
+    _launch(lib.moe_linear_backward, at, stream, a_dy, dy_t, a_pre, a_x, x_t, a_w, code, T, K, N, a_dx, dx_t, a_dw,
             dw_t, a_db, a_ws, n_ws)
     return dx, dw, db
 
@@ -688,9 +694,9 @@ def linear_backward_workspace_bytes(T: int, K: int, N: int, act: str = "none", d
                                     x_dtype=torch.bfloat16, dx_dtype=torch.bfloat16, dw_dtype=torch.float32,
                                     need=("dx", "dw", "db")) -> int:
     """Bytes of linear_backward's workspace for N output columns."""
-    t = {_F32: MOE_F32, _BF16: MOE_BF16}
-    return int(lib.moe_linear_backward_workspace_bytes(T, K, N, ACTS[act], t[dy_dtype], t[x_dtype], t[dx_dtype],
-                                                       t[dw_dtype], sum(_NEED[n] for n in set(need))))
+    code, t = _size_codes(act, dy_dtype, x_dtype, dx_dtype, dw_dtype)
+    _needs(need, ("dx", "dw", "db"))
+    return int(lib.moe_linear_backward_workspace_bytes(T, K, N, code, *t, sum(_NEED[n] for n in set(need))))
 
 
 # ---- slot table -------------------------------------------------------------------------
