@@ -226,7 +226,7 @@ moe_status launch_linear(const void* x, moe_dtype x_t, const uint16_t* w, const 
   p.partial = reinterpret_cast<float*>(base + pl.partial);
   p.ldp = pl.ldp;
   p.epi = e;
-  return launch_products(MOE_KERNEL_LINEAR, pl.plan, &p, 1, false, false, nullptr, 0, 0, nullptr, s, "linear");
+  return launch_products(MOE_KERNEL_LINEAR, pl.plan, &p, 1, false, false, DbSum{}, s, "linear");
 }
 
 }  // namespace moe

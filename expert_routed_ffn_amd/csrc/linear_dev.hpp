@@ -199,12 +199,15 @@ struct Prob {
   int ldp;                 // elements per row of a part
   Epi epi;
 };
-struct Join {  // sums of partials: up to two products, and column sums
+struct DbSum {  // column sums of dz from the parts that the prep launch left; db null: not wanted
+  const float* part;  // [rows][n]
+  float* db;          // [n]
+  int rows, n;
+};
+struct Join {  // sums of the parts of up to two products, or db's
   Prob p[2];
-  int n0, n1;            // workgroups of each product (0: not split)
-  const float* db_part;  // [db_rows][db_n]
-  float* db;
-  int db_rows, db_n;
+  int n0, n1;  // workgroups of each product (0: not split)
+  DbSum db;
 };
 
 // Sizes of a product, and how a launch of up to two cuts them.
@@ -216,9 +219,9 @@ struct Plan {
   int split[2];
 };
 Plan plan_products(const Shape* s, int count);
-// Launches a forward product (`grad` false, count = 1) or the gradient's (dW first where both are there), then what
-// joins their parts and adds db's.
-moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool grad, bool first_is_dw,
-                           const float* db_part, int db_rows, int db_n, float* db, hipStream_t s, const char* what);
+// Launches a forward product (`grad` false, count = 1) or the gradient's (dW first where both are there) with db's sum,
+// then what joins the products' parts.
+moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool grad, bool first_is_dw, const DbSum& db,
+                           hipStream_t s, const char* what);
 
 }  // namespace moe

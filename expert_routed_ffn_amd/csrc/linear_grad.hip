@@ -2,12 +2,13 @@
 //   dz = dy act'(pre)   (SwiGLU: dz_gate = dy z_up silu'(z_gate), dz_up = dy silu(z_gate))
 //   dx = dz W     dW = dz^T x     db = sum_t dz_t     (the residual's gradient is dy itself)
 //
-// Two launches and, where a reduction was cut or db is wanted, a third:
+// Two launches and, where a reduction was cut, a third:
 //   1. prep: dz is computed once from dy and the kept pre-activations and written as bf16 term planes [T][R]; fp32 x
 //      becomes term planes too, and each workgroup adds its rows of dz in fp32 for db.  Left out where dy is dz as the
 //      products take it (bf16, no activation) and db is not wanted.
-//   2. products: both in one launch of the tiled kernel, which reads dz, W and x in place in either direction.
-//   3. join: parts of cut reductions, and db's parts, in a fixed order.
+//   2. products: both in one launch of the tiled kernel, which reads dz, W and x in place in either direction; db's
+//      parts are added in workgroups behind the tiles.
+//   3. join: parts of cut reductions, in a fixed order.
 // Precision goes by the output's type.  An fp32 dx or dW is computed from operands held exactly: dz, and x where it
 // is fp32, enter as three bf16 terms, and products of terms below 2^-24 of the whole are left out.  A bf16 dx or dW
 // takes dz rounded once to bf16 (relative error at most 2^-9 per element, which adds to the same size of error from
@@ -338,8 +339,9 @@ moe_status launch_linear_backward(const void* dy, moe_dtype dy_t, const void* pr
     product(p.x ? p.xt : reinterpret_cast<const uint16_t*>(x), p.x_plane, pl.R, T, pl.segs_dw, pl.dw_sa, pl.dw_sb,
             pl.split_dw, f32(pl.part_dw), dw, dw_t);
   if (pl.dx) product(w, 0, T, pl.R, pl.segs_dx, pl.dx_sa, pl.dx_sb, pl.split_dx, f32(pl.part_dx), dx, dx_t);
-  return launch_products(MOE_KERNEL_LINEAR_BACKWARD, pl.plan, g, count, true, pl.dw, p.db_part, pl.tiles_t, pl.R, db, s,
-                         "linear_backward");
+  if (count == 0 && !db) return MOE_OK;
+  return launch_products(MOE_KERNEL_LINEAR_BACKWARD, pl.plan, g, count, true, pl.dw, DbSum{p.db_part, db, pl.tiles_t, pl.R},
+                         s, "linear_backward");
 }
 
 }  // namespace moe

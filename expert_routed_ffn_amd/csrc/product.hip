@@ -389,18 +389,36 @@ __global__ __launch_bounds__(T::kThreads, 2) void linear_product_kernel(Prob p) 
   product_tile<T, false, false, PAIR>(p, blockIdx.x, gridDim.x, lds);
 }
 
+// db from its parts: 64 columns a workgroup; four waves take every fourth part, and their sums are added in wave order.
+__device__ __forceinline__ void add_db(const DbSum& d, int group, float* lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = group * 64 + lane;
+  if (wave < 4) {
+    float v = 0.0f;
+    if (c < d.n) {
+#pragma unroll 8
+      for (int r = wave; r < d.rows; r += 4) v += d.part[(size_t)r * d.n + c];
+    }
+    lds[64 * wave + lane] = v;
+  }
+  __syncthreads();
+  if (wave == 0 && c < d.n) d.db[c] = lds[lane] + lds[64 + lane] + lds[128 + lane] + lds[192 + lane];
+}
+
 // The gradient's two products in one grid, so that the tiles of one fill what the other leaves idle: first dW (the
-// longer reduction as a rule), then dx.
+// longer reduction as a rule), then dx, then db's column groups.
 template <typename T>
-__global__ __launch_bounds__(T::kThreads, 2) void grad_products_kernel(Prob dw, Prob dx, int dw_blocks) {
+__global__ __launch_bounds__(T::kThreads, 2) void grad_products_kernel(Prob dw, Prob dx, int dw_blocks, int dx_blocks,
+                                                                       DbSum db) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[T::kLds];
   const int b = blockIdx.x;
   if (b < dw_blocks) product_tile<T, true, true, false>(dw, b, dw_blocks, lds);
-  else product_tile<T, false, true, false>(dx, b - dw_blocks, gridDim.x - dw_blocks, lds);
+  else if (b < dw_blocks + dx_blocks) product_tile<T, false, true, false>(dx, b - dw_blocks, dx_blocks, lds);
+  else add_db(db, b - dw_blocks - dx_blocks, reinterpret_cast<float*>(lds));
 }
 
-// Adds the parts of split products in part order and applies their epilogue; the workgroups after those add the
-// column sums' parts.  Four columns per thread.
+// Adds the parts of split products in part order and applies their epilogue; without any, adds db's.  Four columns per
+// thread.
 __global__ __launch_bounds__(256) void join_kernel(Join jn) {
   int b = blockIdx.x;
   if (b < jn.n0 + jn.n1) {
@@ -447,18 +465,8 @@ __global__ __launch_bounds__(256) void join_kernel(Join jn) {
     pair ? epi_rows<true, 1>(p.epi, m, n, 1, value) : epi_rows<false, 1>(p.epi, m, n, 1, value);
     return;
   }
-  // 64 columns a workgroup; its four waves take every fourth row, and their sums are added in wave order
-  __shared__ float part[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = (b - jn.n0 - jn.n1) * 64 + lane;
-  float v = 0.0f;
-  if (c < jn.db_n) {
-#pragma unroll 8
-    for (int r = wave; r < jn.db_rows; r += 4) v += jn.db_part[(size_t)r * jn.db_n + c];
-  }
-  part[wave][lane] = v;
-  __syncthreads();
-  if (wave == 0 && c < jn.db_n) jn.db[c] = part[0][lane] + part[1][lane] + part[2][lane] + part[3][lane];
+  __shared__ float lds[256];
+  add_db(jn.db, b, lds);
 }
 
 int64_t tiles_of(const Shape& s, int side) { return ceil_div(s.M, side) * ceil_div(s.R, side); }
@@ -519,9 +527,10 @@ Plan plan_products(const Shape* s, int count) {
   return best;
 }
 
-moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool grad, bool first_is_dw,
-                           const float* db_part, int db_rows, int db_n, float* db, hipStream_t s, const char* what) {
+moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool grad, bool first_is_dw, const DbSum& db,
+                           hipStream_t s, const char* what) {
   const int side = kRates[plan.shape].side;
+  const int64_t db_blocks = db.db ? ceil_div(db.n, 64) : 0;
   int64_t blocks[2] = {0, 0};
   Join j{};
   for (int i = 0; i < count; ++i) {
@@ -531,33 +540,32 @@ moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool g
     j.p[i] = p[i];
     if (p[i].split > 1) (i ? j.n1 : j.n0) = (int)ceil_div((int64_t)p[i].M * ((p[i].epi.N + 3) / 4), 256);
   }
-  if (blocks[0] + blocks[1] > 0x7FFFFFFF) return fail(MOE_EUNSUPPORTED, std::string(what) + ": too many tiles");
-  if (count > 0) {
-    const dim3 grid((unsigned)(blocks[0] + blocks[1]));
-    auto fwd = [&](auto kernel, int threads) { launch_k(kid, kernel, grid, dim3((unsigned)threads), 0, s, p[0]); };
-    auto bwd = [&](auto kernel, int threads) {
-      const int n = first_is_dw ? (int)blocks[0] : 0;
-      launch_k(kid, kernel, grid, dim3((unsigned)threads), 0, s, p[0], p[count - 1], n);
-    };
-    const bool pair = p[0].epi.act == MOE_ACT_SWIGLU;
-    auto go = [&](auto tile) {
-      using T = decltype(tile);
-      if (grad) bwd(grad_products_kernel<T>, T::kThreads);
-      else if (pair) fwd(linear_product_kernel<T, true>, T::kThreads);
-      else fwd(linear_product_kernel<T, false>, T::kThreads);
-    };
-    if (plan.shape == 0) go(Tiny{});
-    else if (plan.shape == 1) go(Small{});
-    else go(Large{});
-    if (moe_status st = check_launch(what)) return st;
+  const int64_t total = blocks[0] + blocks[1] + db_blocks;
+  if (total > 0x7FFFFFFF) return fail(MOE_EUNSUPPORTED, std::string(what) + ": too many tiles");
+  if (count == 0) {
+    j.db = db;
+    join_kernel<<<dim3((unsigned)db_blocks), 256, 0, s>>>(j);
+    return check_launch(what);
   }
-  j.db_part = db_part;
-  j.db = db;
-  j.db_rows = db_rows;
-  j.db_n = db ? db_n : 0;
-  const int64_t jb = (int64_t)j.n0 + j.n1 + ceil_div(j.db_n, 64);
-  if (jb > 0) {
-    join_kernel<<<dim3((unsigned)jb), 256, 0, s>>>(j);
+  const dim3 grid((unsigned)total);
+  const bool pair = p[0].epi.act == MOE_ACT_SWIGLU;
+  auto go = [&](auto tile) {
+    using T = decltype(tile);
+    const dim3 threads((unsigned)T::kThreads);
+    if (grad)
+      launch_k(kid, grad_products_kernel<T>, grid, threads, 0, s, p[0], p[count - 1], first_is_dw ? (int)blocks[0] : 0,
+               first_is_dw ? (int)blocks[1] : (int)blocks[0], db);
+    else if (pair)
+      launch_k(kid, linear_product_kernel<T, true>, grid, threads, 0, s, p[0]);
+    else
+      launch_k(kid, linear_product_kernel<T, false>, grid, threads, 0, s, p[0]);
+  };
+  if (plan.shape == 0) go(Tiny{});
+  else if (plan.shape == 1) go(Small{});
+  else go(Large{});
+  if (moe_status st = check_launch(what)) return st;
+  if (j.n0 + j.n1 > 0) {
+    join_kernel<<<dim3((unsigned)(j.n0 + j.n1)), 256, 0, s>>>(j);
     return check_launch(what);
   }
   return MOE_OK;
