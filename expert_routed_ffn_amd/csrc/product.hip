@@ -22,6 +22,7 @@
 // tiles are for products of few tiles, whose time is the latency of their loads: four buffers keep three steps' loads
 // under way.  (Rings of 3 or 4 buffers of 32 k under the large tiles measured no better than two of 64.)
 #include <algorithm>
+#include <type_traits>
 
 #include "linear_dev.hpp"
 
@@ -101,10 +102,10 @@ struct Operand<ROWS, THREADS, false> {  // [m][k]
       *reinterpret_cast<uint4*>(lds + (i * THREADS + threadIdx.x) * 8) = v;
     }
   }
-  // a last step of 32 k whose second half is not multiplied: its place takes the first half's values again
-  __device__ __forceinline__ void load_half(const uint16_t* p, int, uint16_t* lds, int w64) const {
+  // a last step whose fragments are masked when they are read: what is not there takes the first values again
+  __device__ __forceinline__ void load_short(const uint16_t* p, int, int left, uint16_t* lds, int w64) const {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) to_lds16(p + off[i] - (chunk >= 4 ? 32 : 0), lds + (i * THREADS + w64) * 8);
+    for (int i = 0; i < kLoads; ++i) to_lds16(p + off[i] - (chunk * 8 < left ? 0 : chunk * 8), lds + (i * THREADS + w64) * 8);
   }
   template <int F>
   __device__ __forceinline__ void read(const uint16_t* lds, int base, int kk, bf16x8_t (&f)[F]) const {
@@ -148,11 +149,12 @@ struct Operand<ROWS, THREADS, true> {  // [k][m]
       *reinterpret_cast<uint4*>(lds + (i * THREADS + threadIdx.x) * 8) = v;
     }
   }
-  __device__ __forceinline__ void load_half(const uint16_t* p, int ld, uint16_t* lds, int w64) const {
+  __device__ __forceinline__ void load_short(const uint16_t* p, int ld, int left, uint16_t* lds, int w64) const {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      to_lds16(p + off + (uint32_t)i * kPer * ld - (i * kPer + (int)threadIdx.x / kSlots >= 32 ? 32u * ld : 0u),
-               lds + (i * THREADS + w64) * 8);
+    for (int i = 0; i < kLoads; ++i) {
+      const int k = i * kPer + (int)threadIdx.x / kSlots;
+      to_lds16(p + off + (uint32_t)i * kPer * ld - (k < left ? 0u : (uint32_t)k * ld), lds + (i * THREADS + w64) * 8);
+    }
   }
   template <int F>
   __device__ __forceinline__ void read(const uint16_t* lds, int base, int kk, bf16x8_t (&f)[F]) const {
@@ -169,6 +171,20 @@ struct Operand<ROWS, THREADS, true> {  // [k][m]
     }
   }
 };
+
+// Fragments with k = first + 8 (lane / 16) ... : values at `left` and past it become zeros.
+template <int F>
+__device__ __forceinline__ void mask_k(bf16x8_t (&f)[F], int first, int left) {
+  const int k = first + 8 * ((threadIdx.x >> 4) & 3);
+#pragma unroll
+  for (int i = 0; i < F; ++i) {
+    uint4 q = __builtin_bit_cast(uint4, f[i]);
+    uint32_t* w = &q.x;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) w[d] &= (k + 2 * d < left ? 0xFFFFu : 0u) | (k + 2 * d + 1 < left ? 0xFFFF0000u : 0u);
+    f[i] = __builtin_bit_cast(bf16x8_t, q);
+  }
+}
 
 // Four columns n ... of a part's row, those below N.
 __device__ __forceinline__ void put_part(float* out, int n, int N, const float (&z)[4]) {
@@ -214,8 +230,6 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
   uint16_t* const base = reinterpret_cast<uint16_t*>(lds);
   int seg = uniform(lo / seg_steps), kstep = lo - seg * seg_steps, next = lo;  // the step that is loaded next
   const int last = p.K - kBK;
-  // a last step of 32 k needs no zeros where its second half can be left out: the ring's loop does
-  const bool half_end = T::kRing > 2 && p.K % kBK == 32;
   const uint16_t *src_a, *src_b;
   auto place = [&] {
     src_a = A.at(p.A + ((p.sa >> (2 * seg)) & 3) * p.a_plane, m0, kstep * kBK, p.lda);
@@ -230,9 +244,9 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
     if (k0 <= last) {
       A.load(src_a, p.lda, la, 64 * wave);
       B.load(src_b, p.ldb, lb, 64 * wave);
-    } else if (half_end) {
-      A.load_half(src_a, p.lda, la, 64 * wave);
-      B.load_half(src_b, p.ldb, lb, 64 * wave);
+    } else if (T::kRing > 2) {
+      A.load_short(src_a, p.lda, p.K - k0, la, 64 * wave);
+      B.load_short(src_b, p.ldb, p.K - k0, lb, 64 * wave);
     } else {
       A.load_tail(src_a, p.lda, p.K - k0, la);
       B.load_tail(src_b, p.ldb, p.K - k0, lb);
@@ -285,15 +299,16 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
   };
   if constexpr (T::kRing > 2) {
     // Few tiles: the time is the latency of the loads, so kRing - 1 steps of them are kept under way.  A step's own have
-    // landed once no more are outstanding than the later steps issued; where a tail's go through registers, their wait
-    // covers all loads before them.
+    // landed once no more are outstanding than the later steps issued.  The last step of a reduction that is no multiple
+    // of 64 is no exception: it loads what it can and masks both operands' fragments.
     constexpr int kPer = decltype(A)::kLoads + decltype(B)::kLoads, kLeft = (T::kRing - 2) * kPer;
     static_assert(kLeft < 16, "vmcnt's low bits");
     if (lo < hi) {
 #pragma unroll
       for (int i = 0; i < T::kRing - 1; ++i) load(i);
-      int now = 0, free = T::kRing - 1, left = seg_steps - lo % seg_steps;  // steps to the segment's end
-      for (int s = lo; s < hi; ++s) {
+      const int rem = p.K % kBK;
+      int now = 0, free = T::kRing - 1;
+      auto step = [&](auto masked) {
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(0x0070 | kLeft);  // vmcnt(kLeft) lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
@@ -301,15 +316,27 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
         load(free);
         read(now, 0, 0);
         read(now, 1, 1);
-        mma(0);
-        if (--left == 0) {
-          left = seg_steps;
-          if (!half_end) mma(1);
-        } else {
-          mma(1);
+        if constexpr (decltype(masked)::value) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            mask_k(af[w], 32 * w, rem);
+            mask_k(bf[w], 32 * w, rem);
+          }
         }
+        mma(0);
+        mma(1);
         now = now + 1 == T::kRing ? 0 : now + 1;
         free = free + 1 == T::kRing ? 0 : free + 1;
+      };
+      int whole = seg_steps - 1 - lo % seg_steps;  // steps before the segment's last
+      for (int s = lo; s < hi;) {
+        const int until = rem ? min(hi, s + whole) : hi;
+        for (; s < until; ++s) step(std::false_type{});
+        if (s < hi) {
+          step(std::true_type{});
+          ++s;
+          whole = seg_steps - 1;
+        }
       }
     }
   } else if (lo < hi) {

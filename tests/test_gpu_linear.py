@@ -240,3 +240,56 @@ def test_prompt_chunk(moe):
     within(dx, rx, bx.cpu(), "dx")
     within(dw, rw, bw.cpu(), "dw")
     within(db, rb, bb.cpu(), "db")
+
+
+def _big(T, K, N, act, xt, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    R = rows_of(act, N)
+    return (torch.randn((T, K), generator=g, device="cuda").to(xt),
+            (torch.randn((R, K), generator=g, device="cuda") / K ** 0.5).to(BF16),
+            torch.randn((R,), generator=g, device="cuda"), torch.randn((T, N), generator=g, device="cuda"), g)
+
+
+# sizes that take 128 x 128 and 256 x 256 tiles, with last steps of 32 k, odd columns and rows past the last tile
+@pytest.mark.parametrize("T,K,N,act,xt,yt", [(2100, 544, 1001, "silu", BF16, BF16), (2100, 544, 1003, "swiglu", BF16, F32),
+                                             (4000, 1056, 1500, "none", F32, F32), (4000, 4128, 4094, "gelu", BF16, BF16),
+                                             (4000, 2080, 2047, "swiglu", BF16, BF16)])
+def test_large_tiles(moe, T, K, N, act, xt, yt):
+    x, w, b, r, _ = _big(T, K, N, act, xt, seed=N)
+    pre = torch.empty((T, w.shape[0]), dtype=yt, device="cuda")
+    y = moe.linear(x, w, bias=b, act=act, residual=r, y_dtype=yt, pre=pre)
+    ry, rz = linear64(x, w, b, act, r)
+    by, bz = linear_bounds(x, w, b, act, r, yt, False)
+    within(y, ry, by.cpu(), "y")
+    within(pre, rz, bz.cpu(), "pre")
+
+
+# both products on 128 x 128 tiles with dW's reduction cut (and odd columns), and on 256 x 256 tiles from fp32
+@pytest.mark.parametrize("T,K,N,act,xt,gt,dxt,dwt", [(4000, 2048, 1001, "silu", BF16, BF16, BF16, F32),
+                                                     (8200, 2048, 515, "swiglu", BF16, BF16, BF16, BF16),
+                                                     (3000, 1024, 2000, "none", F32, F32, F32, F32)])
+def test_large_tiles_gradient(moe, T, K, N, act, xt, gt, dxt, dwt):
+    x, w, _, r, g = _big(T, K, N, act, xt, seed=N)
+    dy, pre = r.to(gt), torch.randn((T, w.shape[0]), generator=g, device="cuda").to(gt)
+    dx, dw, db = moe.linear_backward(dy, x, w, act=act, pre=pre, dx_dtype=dxt, dw_dtype=dwt)
+    rx, rw, rb, _ = linear_grad64(dy, x, w, act, pre)
+    bx, bw, bb = linear_grad_bounds(dy, x, w, act, pre, dxt, dwt)
+    within(dx, rx, bx.cpu(), "dx")
+    within(dw, rw, bw.cpu(), "dw")
+    within(db, rb, bb.cpu(), "db")
+
+
+@pytest.mark.parametrize("T", [40, 150])
+def test_infinities_stay_where_they_are(moe, T):
+    """An infinite activation makes its own products infinite and no others, also in the last, partial step of a
+    reduction and for the rows and columns next to it."""
+    x, w, _, _ = _inputs(T, 96, 33, "none", BF16, seed=T)
+    x[T - 1, 95] = float("inf")
+    y = moe.linear(x.cuda(), w.cuda()).cpu()
+    assert torch.isfinite(y[:T - 1]).all()
+    want = torch.where(w[:, 95] > 0, float("inf"), torch.where(w[:, 95] < 0, -float("inf"), float("nan"))).float()
+    assert torch.equal(y[T - 1].float().nan_to_num(7, 1e38, -1e38), want.nan_to_num(7, 1e38, -1e38))
+    dy = torch.randn((T, 33), generator=torch.Generator().manual_seed(1)).to(BF16)
+    dx, dw, _ = moe.linear_backward(dy.cuda(), x.cuda(), w.cuda(), need=("dx", "dw"))
+    assert torch.isfinite(dx).all() and torch.isfinite(dw[:, :95]).all() and not torch.isfinite(dw[:, 95]).any()
+    assert torch.equal(torch.isinf(dw[:, 95]).cpu(), dy[T - 1] != 0)
