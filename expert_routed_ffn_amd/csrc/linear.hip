@@ -38,15 +38,17 @@ struct FewX<true> {
 
 // Grid: one workgroup per 16 rows of W (8 gate and 8 up rows for SwiGLU), 8 waves.  v_mfma_f32_16x16x32_bf16 takes
 // the 16 rows as its first operand and 16 tokens as its second; TF such token fragments share each weight fragment.
-// Wave w works through its eighth of the K-steps with the loads of U steps in flight, then the eight sums of an
-// element are added through LDS in wave order.  Rows of W past R and tokens past T read the last valid one and are
-// not stored.
+// Wave w works through its eighth of the K-steps with the loads of U steps in flight, then the eight sums of an element
+// are added through LDS in wave order.  fp32 activations are split as they are used; the steps of that are many, and the
+// code of more than a few of them costs more than it saves (2,048 -> 1,024 from one fp32 token: 7.8 us with four steps
+// unrolled and a split that tests for infinities, 4.9 with this one).  Rows of W past R and tokens past T read the last
+// valid one and are not stored.
 template <bool XF32, int TF>
 __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(const void* __restrict__ x,
                                                                     const uint16_t* __restrict__ w, int T, int K, Epi e) {
-  constexpr int U = TF == 4 ? 2 : 4;
+  constexpr int U = XF32 ? (TF == 1 ? 2 : 1) : TF == 4 ? 2 : 4;
   __shared__ __attribute__((aligned(16))) float red[kFewWaves][TF][64][4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool pair = e.act == MOE_ACT_SWIGLU;
   const int fr = lane & 15, fq = lane >> 4;
   int row;
@@ -65,46 +67,51 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(const void* 
   for (int f = 0; f < TF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int steps = K / 32;
   const int s0 = steps * wave / kFewWaves, s1 = steps * (wave + 1) / kFewWaves;
-  for (int s = s0; s < s1; s += U) {
-    uint4 wv[U];
-    FewX<XF32> xv[U][TF];
+  struct Stage {
+    uint4 w[U];
+    FewX<XF32> x[U][TF];
+  };
+  auto load = [&](Stage& st, int s) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (s + u < s1) {
-        wv[u] = *reinterpret_cast<const uint4*>(wrow + (s + u) * 32);
+        st.w[u] = *reinterpret_cast<const uint4*>(wrow + (s + u) * 32);
 #pragma unroll
-        for (int f = 0; f < TF; ++f) xv[u][f].load(x, xoff[f] + (size_t)(s + u) * 32);
+        for (int f = 0; f < TF; ++f) st.x[u][f].load(x, xoff[f] + (size_t)(s + u) * 32);
       } else {
-        wv[u] = make_uint4(0, 0, 0, 0);
+        st.w[u] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int f = 0; f < TF; ++f) xv[u][f].zero();
+        for (int f = 0; f < TF; ++f) st.x[u][f].zero();
       }
     }
+  };
+  auto multiply = [&](const Stage& st) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bf16x8_t wf = __builtin_bit_cast(bf16x8_t, wv[u]);
+      const bf16x8_t wf = __builtin_bit_cast(bf16x8_t, st.w[u]);
 #pragma unroll
       for (int f = 0; f < TF; ++f) {
         if constexpr (XF32) {
-          const float v[8] = {xv[u][f].a.x, xv[u][f].a.y, xv[u][f].a.z, xv[u][f].a.w,
-                              xv[u][f].b.x, xv[u][f].b.y, xv[u][f].b.z, xv[u][f].b.w};
-          uint16_t t[8][3];
+          const float4 a = st.x[u][f].a, b = st.x[u][f].b;
+          uint32_t t[4][3];
+          split_terms<3>(a.x, a.y, t[0]);
+          split_terms<3>(a.z, a.w, t[1]);
+          split_terms<3>(b.x, b.y, t[2]);
+          split_terms<3>(b.z, b.w, t[3]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) bf16_terms(v[i], t[i]);
-#pragma unroll
-          for (int q = 0; q < 3; ++q) {
-            uint4 p;
-            p.x = t[0][q] | (uint32_t)t[1][q] << 16;
-            p.y = t[2][q] | (uint32_t)t[3][q] << 16;
-            p.z = t[4][q] | (uint32_t)t[5][q] << 16;
-            p.w = t[6][q] | (uint32_t)t[7][q] << 16;
-            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8_t, p), acc[f], 0, 0, 0);
-          }
+          for (int q = 0; q < 3; ++q)
+            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                wf, __builtin_bit_cast(bf16x8_t, make_uint4(t[0][q], t[1][q], t[2][q], t[3][q])), acc[f], 0, 0, 0);
         } else {
-          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8_t, xv[u][f].q), acc[f], 0, 0, 0);
+          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8_t, st.x[u][f].q), acc[f], 0, 0, 0);
         }
       }
     }
+  };
+  for (int s = s0; s < s1; s += U) {
+    Stage st;
+    load(st, s);
+    multiply(st);
   }
   // lane: token 16 f + (lane & 15), rows 4 (lane >> 4) + r
 #pragma unroll
@@ -135,20 +142,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(const void* 
 // ---- more tokens ---------------------------------------------------------------------------
 
 // fp32 activations to bf16 term planes, `plane` elements apart.
+template <int TERMS>
 __global__ __launch_bounds__(256) void terms_kernel(const float* __restrict__ x, int64_t n4, uint16_t* __restrict__ planes,
-                                                    int64_t plane, int terms) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
-    const float4 q = reinterpret_cast<const float4*>(x)[i];
-    const float v[4] = {q.x, q.y, q.z, q.w};
-    uint16_t t[4][3];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) bf16_terms(v[j], t[j]);
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-      if (k < terms)
-        reinterpret_cast<uint2*>(planes + k * plane)[i] =
-            make_uint2(t[0][k] | (uint32_t)t[1][k] << 16, t[2][k] | (uint32_t)t[3][k] << 16);
-  }
+                                                    int64_t plane) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256)
+    write_terms<TERMS>(x, i, planes, plane);
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -180,9 +178,10 @@ LinearPlan linear_plan(int T, int K, int N, int act, moe_dtype x_t, moe_dtype y_
 
 }  // namespace
 
-moe_status launch_terms(const float* x, int64_t n, uint16_t* planes, int64_t plane, int terms, hipStream_t s) {
-  const int64_t n4 = n / 4;
-  terms_kernel<<<dim3((unsigned)std::min<int64_t>(2048, ceil_div(n4, 256))), 256, 0, s>>>(x, n4, planes, plane, terms);
+static moe_status launch_terms(const float* x, int64_t n, uint16_t* planes, int64_t plane, int terms, hipStream_t s) {
+  const dim3 grid((unsigned)std::min<int64_t>(2048, ceil_div(n / 4, 256)));
+  if (terms == 1) terms_kernel<1><<<grid, 256, 0, s>>>(x, n / 4, planes, plane);
+  else terms_kernel<3><<<grid, 256, 0, s>>>(x, n / 4, planes, plane);
   return check_launch("linear");
 }
 

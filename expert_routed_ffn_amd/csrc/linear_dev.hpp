@@ -29,6 +29,34 @@ __device__ __forceinline__ void bf16_terms(float f, uint16_t (&t)[3]) {
   t[2] = f32_to_bf16(r - bf16_to_f32(t[1]));
 }
 
+// Two values as TERMS packed bf16 terms each, for uses that take all of them: what does not fit a term, infinities and NaN
+// included, is left to the next (no term but the last exceeds the largest bf16), which costs fewer steps than testing
+// for them.
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+template <int TERMS>
+__device__ __forceinline__ void split_terms(float a, float b, uint32_t (&t)[TERMS]) {
+  constexpr float kMax = 3.38953139e38f;  // 0x7F7F0000
+#pragma unroll
+  for (int k = 0; k < TERMS; ++k) {
+    f32x2_t v = {a, b};
+    if (k < TERMS - 1) v = f32x2_t{__builtin_amdgcn_fmed3f(a, -kMax, kMax), __builtin_amdgcn_fmed3f(b, -kMax, kMax)};
+    t[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+    a -= __uint_as_float(t[k] << 16);
+    b -= __uint_as_float(t[k] & 0xFFFF0000u);
+  }
+}
+// Four values at x + 4 i to the term planes, `plane` elements apart.
+template <int TERMS>
+__device__ __forceinline__ void write_terms(const float* x, int64_t i, uint16_t* planes, int64_t plane) {
+  const float4 q = reinterpret_cast<const float4*>(x)[i];
+  uint32_t lo[TERMS], hi[TERMS];
+  split_terms<TERMS>(q.x, q.y, lo);
+  split_terms<TERMS>(q.z, q.w, hi);
+#pragma unroll
+  for (int k = 0; k < TERMS; ++k) reinterpret_cast<uint2*>(planes + k * plane)[i] = make_uint2(lo[k], hi[k]);
+}
+
 // 1 / (1 + e^-z): z -> -inf gives 0, z -> inf gives 1, NaN stays NaN.
 __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));

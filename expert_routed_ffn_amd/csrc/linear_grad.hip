@@ -165,16 +165,9 @@ __global__ __launch_bounds__(256) void linear_prep_kernel(Prep p) {
   }
   const int64_t step = (int64_t)(gridDim.x - p.blocks) * 256;
   for (int64_t i = (int64_t)(blockIdx.x - p.blocks) * 256 + threadIdx.x; i < p.x4; i += step) {
-    const float4 q = reinterpret_cast<const float4*>(p.x)[i];
-    const float v[4] = {q.x, q.y, q.z, q.w};
-    uint16_t t[4][3];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) bf16_terms(v[j], t[j]);
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-      if (k < p.x_terms)
-        reinterpret_cast<uint2*>(p.xt + k * p.x_plane)[i] =
-            make_uint2(t[0][k] | (uint32_t)t[1][k] << 16, t[2][k] | (uint32_t)t[3][k] << 16);
+    if (p.x_terms == 1) write_terms<1>(p.x, i, p.xt, p.x_plane);
+    else if (p.x_terms == 2) write_terms<2>(p.x, i, p.xt, p.x_plane);
+    else write_terms<3>(p.x, i, p.xt, p.x_plane);
   }
 }
 

@@ -280,10 +280,11 @@ def test_large_tiles_gradient(moe, T, K, N, act, xt, gt, dxt, dwt):
 
 
 @pytest.mark.parametrize("T", [40, 150])
-def test_infinities_stay_where_they_are(moe, T):
+@pytest.mark.parametrize("xt", [BF16, F32])
+def test_infinities_stay_where_they_are(moe, T, xt):
     """An infinite activation makes its own products infinite and no others, also in the last, partial step of a
     reduction and for the rows and columns next to it."""
-    x, w, _, _ = _inputs(T, 96, 33, "none", BF16, seed=T)
+    x, w, _, _ = _inputs(T, 96, 33, "none", xt, seed=T)
     x[T - 1, 95] = float("inf")
     y = moe.linear(x.cuda(), w.cuda()).cpu()
     assert torch.isfinite(y[:T - 1]).all()
