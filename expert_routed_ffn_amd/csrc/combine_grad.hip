@@ -5,6 +5,7 @@
 // before the first product; dy is written from the same registers.  HBM bounds it: T k H (read + write) elements.
 // Sums in fp32, over columns in an order that depends on H alone, so a token's dw does not depend on its neighbours
 // and two calls give the same bits.
+#include <algorithm>
 #include <type_traits>
 
 #include "wave_dev.hpp"
@@ -71,15 +72,16 @@ __device__ __forceinline__ void store_cols(uint16_t* p, const Cols<C>& v) {
 
 constexpr int kThreads = 256;
 
-// Grid: (T, k / J rounded up); workgroup (t, b) takes rows b J ... of token t.  Thread i owns columns C i ... of each
-// 256 C-column stretch.
+// Grid: (tokens, k / J rounded up, T / tokens rounded up), as one dimension holds less than 2^32 threads; workgroup
+// (t, b) takes rows b J ... of token t.  Thread i owns columns C i ... of each 256 C-column stretch.
 template <typename YT, typename GT, int C, int J>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(const YT* __restrict__ y, const float* __restrict__ w,
-                                                                    const GT* __restrict__ dout, int k, int H,
+                                                                    const GT* __restrict__ dout, int T, int k, int H,
                                                                     float* __restrict__ dw, YT* __restrict__ dy) {
   __shared__ float s_dot[kThreads / 64][J];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const size_t t = blockIdx.x;
+  const size_t t = (size_t)blockIdx.z * gridDim.x + blockIdx.x;
+  if (t >= (size_t)T) return;
   const int j0 = blockIdx.y * J, nj = min(J, k - j0);
   const size_t row0 = t * k + j0;
   float wj[J], dot[J];
@@ -132,9 +134,10 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(const YT* __
 // (12 tokens of 10 x 2,048 fp32: 9.4 us with 10 rows, 3.4 with 2).
 template <typename YT, typename GT, int C>
 void launch_c(const YT* y, const float* w, const GT* dout, int T, int k, int H, float* dw, YT* dy, hipStream_t s) {
+  constexpr int kTokens = 1 << 22;
   auto go = [&](auto kernel, int rows) {
-    launch_k(MOE_KERNEL_COMBINE_BACKWARD, kernel, dim3((unsigned)T, (unsigned)ceil_div(k, rows)), dim3(kThreads), 0, s, y, w,
-             dout, k, H, dw, dy);
+    const dim3 grid((unsigned)std::min(T, kTokens), (unsigned)ceil_div(k, rows), (unsigned)ceil_div(T, kTokens));
+    launch_k(MOE_KERNEL_COMBINE_BACKWARD, kernel, grid, dim3(kThreads), 0, s, y, w, dout, T, k, H, dw, dy);
   };
   if (T < 256 && k > 2) go(combine_backward_kernel<YT, GT, C, 2>, 2);
   else if (k > 8) go(combine_backward_kernel<YT, GT, C, kMaxK>, kMaxK);

@@ -85,3 +85,15 @@ def test_differences(moe):
         assert abs(num - float((dy.cpu().double() * vy.double()).sum())) <= 64 * U * (mag + 1) / eps * 4
         num = (loss(y, w + eps * vw) - loss(y, w - eps * vw)) / (2 * eps)
         assert abs(num - float((dw.cpu().double() * vw.double()).sum())) <= 64 * U * (mag + 1) / eps * 16
+
+
+def test_most_tokens(moe):
+    """T * k = 2^24 with k = 1: as many tokens as a call takes.  Small whole numbers: every product and sum is exact."""
+    T, H = 1 << 24, 4
+    g = torch.Generator(device="cuda").manual_seed(4)
+    y = torch.randint(-3, 4, (T, 1, H), generator=g, device="cuda").to(BF16)
+    w = torch.randint(-3, 4, (T, 1), generator=g, device="cuda").float()
+    dout = torch.randint(-3, 4, (T, H), generator=g, device="cuda").to(BF16)
+    dw, dy = moe.combine_backward(y, w, dout)
+    assert torch.equal(dw[:, 0], (y[:, 0].float() * dout.float()).sum(1))
+    assert torch.equal(dy[:, 0].float(), w * dout.float())
