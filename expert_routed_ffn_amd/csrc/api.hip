@@ -375,6 +375,19 @@ moe_status moe_balance_loss(const float* logits, const int32_t* ids, const uint8
   if (need > 0 && (!ws || ws_bytes < need))
     return fail(MOE_EWORKSPACE, fmt("moe_balance_loss: workspace %lld bytes, needs %lld", (long long)ws_bytes,
                                     (long long)need));
+  const uint64_t n_t = (uint64_t)T * 4;
+  struct Span {
+    const void* p;
+    uint64_t n;
+  };
+  const Span out[4] = {{loss, 8}, {counts, (uint64_t)E * 4 + 4}, {lse, n_t}, {ws, need}};
+  const Span in[3] = {{logits, n_t * E}, {ids, n_t * k}, {mask, (uint64_t)T}};
+  for (int i = 0; i < 4; ++i) {
+    bool bad = false;
+    for (const Span& s : in) bad = bad || overlap(out[i].p, out[i].n, s.p, s.n);
+    for (int j = 0; j < i; ++j) bad = bad || overlap(out[i].p, out[i].n, out[j].p, out[j].n);
+    if (bad) return fail(MOE_EINVAL, "moe_balance_loss: an output or ws overlaps another buffer");
+  }
   return launch_balance_loss(logits, ids, mask, T, E, k, loss, counts, lse, ws, stream);
 }
 

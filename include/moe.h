@@ -390,6 +390,7 @@ void moe_slot_table_destroy(moe_slot_table* t);
  *   loss    [2] fp32 out.      counts [E + 1] int32 out.
  *   lse     [T] fp32 out; -inf for tokens that take no part.
  *   ws      moe_balance_loss_workspace_bytes(T, E) bytes (0 for small T), 16-byte aligned.
+ * Outputs and ws may not overlap the inputs or each other.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED (E, k out of range, T*k above 2^24), MOE_EWORKSPACE.
  */
 size_t moe_balance_loss_workspace_bytes(int T, int E);

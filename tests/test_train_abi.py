@@ -182,3 +182,18 @@ BF = torch.bfloat16
 def test_binding_refusals(call, error, word):
     with pytest.raises(error, match=word):
         call()
+
+
+def test_balance_loss_overlaps_are_refused():
+    # logits, ids, mask, loss, counts, lse, ws = a .. g
+    def call(p):
+        return int(L.moe_balance_loss(p["a"], p["b"], p["c"], 128, 64, 4, p["d"], p["e"], p["f"], p["g"], 1 << 20, None))
+
+    for out in "defg":
+        for other in "abcdefg":
+            if out == other:
+                continue
+            places = {n: _at(16 + 2 * i) for i, n in enumerate("abcdefg")}
+            places[out] = places[other]
+            assert call(places) == EINVAL, (out, other)
+            assert b"overlap" in L.moe_last_error(), (out, other)
