@@ -462,6 +462,8 @@ def _arg(t: torch.Tensor, name: str, shape: tuple, dtypes: tuple, index: int | N
 def _rows(t: torch.Tensor, name: str, dims: int):
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    if max(t.shape) > 0x7FFFFFFF:  # (the library's sizes are 32-bit)
+        raise ValueError(f"{name} must have less than 2^31 rows and columns, got {tuple(t.shape)}")
     return t.shape
 
 

@@ -441,20 +441,24 @@ moe_status moe_combine_backward(const void* y, moe_dtype y_t, const float* w, co
 
 namespace {
 
-constexpr int kLinearMaxT = 1 << 20, kLinearMaxN = 16384;
+constexpr int kLinearMaxT = 1 << 20, kLinearMaxK = 16384, kLinearMaxN = 16384;
 
 moe_status check_linear(const char* fn, int T, int K, int N, moe_act act) {
   if (T < 0) return fail(MOE_EINVAL, std::string(fn) + ": T < 0");
   if (act != MOE_ACT_NONE && act != MOE_ACT_GELU && act != MOE_ACT_SILU && act != MOE_ACT_SWIGLU)
     return fail(MOE_EINVAL, std::string(fn) + ": activation");
   if (T > kLinearMaxT) return fail(MOE_EUNSUPPORTED, std::string(fn) + fmt(": T=%lld above 2^20", T));
-  if (K < 32 || K > 16384 || K % 32)
+  if (K < 32 || K > kLinearMaxK || K % 32)
     return fail(MOE_EUNSUPPORTED, std::string(fn) + fmt(": K=%lld (multiple of 32 in [32, 16384])", K));
   if (N < 1 || N > kLinearMaxN)
     return fail(MOE_EUNSUPPORTED, std::string(fn) + fmt(": N=%lld outside [1, 16384]", N));
   return MOE_OK;
 }
 
+// Sizes that a workspace is asked for: others, which the calls refuse or which have no rows, need none.
+bool sizes_in_range(int T, int K, int N) {
+  return T >= 1 && T <= kLinearMaxT && K >= 1 && K <= kLinearMaxK && N >= 1 && N <= kLinearMaxN;
+}
 bool is_dtype(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16; }
 uintptr_t elem(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }
 
@@ -463,7 +467,7 @@ uintptr_t elem(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }
 extern "C" {
 
 size_t moe_linear_workspace_bytes(int T, int K, int N, moe_act act, moe_dtype x_t, moe_dtype y_t) {
-  if (T < 1 || K < 1 || N < 1) return 0;
+  if (!sizes_in_range(T, K, N)) return 0;
   return linear_ws_bytes(T, K, N, act, x_t, y_t);
 }
 
@@ -498,7 +502,7 @@ moe_status moe_linear(const void* x, moe_dtype x_t, const void* w, const float* 
 
 size_t moe_linear_backward_workspace_bytes(int T, int K, int N, moe_act act, moe_dtype dy_t, moe_dtype x_t,
                                            moe_dtype dx_t, moe_dtype dw_t, int need) {
-  if (T < 1 || K < 1 || N < 1) return 0;
+  if (!sizes_in_range(T, K, N)) return 0;
   return linear_backward_ws_bytes(T, K, N, act, dy_t, x_t, dx_t, dw_t, need);
 }
 

@@ -451,7 +451,8 @@ typedef enum moe_act {
  *             may be the residual itself when r_t == y_t.
  *   pre       NULL or [T x R] out, dtype y_t: z, which moe_linear_backward needs
  *             for every activation but MOE_ACT_NONE.
- *   ws        moe_linear_workspace_bytes(T, K, N, act, x_t, y_t) bytes, 256-byte aligned.
+ *   ws        moe_linear_workspace_bytes(T, K, N, act, x_t, y_t) bytes, 256-byte aligned
+ *             (the query answers 0 for sizes that the call refuses).
  * Sums in fp32.  fp32 x is used to full precision when y is fp32 or T <= 64; a
  * bf16 y of more tokens takes x rounded to bf16.  T <= 2^20.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE.
@@ -478,6 +479,8 @@ enum { MOE_NEED_DX = 1, MOE_NEED_DW = 2, MOE_NEED_DB = 4 };
  * dx and dw must be 16-byte aligned; outputs may not overlap the inputs that are
  * read or each other.  Sums in fp32.  An fp32 dx or dw comes from dz (and x) at
  * full precision; a bf16 one from dz rounded to bf16.
+ * An infinite or NaN dz or x makes the elements it enters infinite or NaN, where
+ * an infinity may become a NaN.
  * Errors: MOE_EINVAL (no output wanted among that), MOE_EUNSUPPORTED, MOE_EWORKSPACE.
  */
 size_t moe_linear_backward_workspace_bytes(int T, int K, int N, moe_act act, moe_dtype dy_t, moe_dtype x_t,

@@ -197,3 +197,23 @@ def test_balance_loss_overlaps_are_refused():
             places[out] = places[other]
             assert call(places) == EINVAL, (out, other)
             assert b"overlap" in L.moe_last_error(), (out, other)
+
+
+@pytest.mark.parametrize("T,K,N", [(1 << 21, 64, 64), (100, 1 << 30, 64), (100, 64, 1 << 30), (100, 64, 16385)])
+def test_workspaces_of_refused_sizes_are_zero(T, K, N):
+    for act in ("none", "swiglu"):
+        assert m.linear_workspace_bytes(T, K, N, act, torch.float32, torch.float32) == 0
+        assert m.linear_backward_workspace_bytes(T, K, N, act, torch.float32, torch.float32) == 0
+
+
+@pytest.mark.parametrize("name,call", [
+    ("logits", lambda big: m.balance_loss(big, big.to(torch.int32))),
+    ("logits", lambda big: m.route_backward(big, big.to(torch.int32), w=big, dw=big)),
+    ("y", lambda big: m.combine_backward(big[:, :, None], big, big)),
+    ("x", lambda big: m.linear(big, _t(8, 64, dtype=BF))),
+    ("x", lambda big: m.linear_backward(big, big, _t(8, 64, dtype=BF)))])
+def test_rows_past_32_bits_are_refused(name, call):
+    """One row more than 2^32 would otherwise pass for a single one.  (Meta tensors: no memory behind the rows.)"""
+    big = torch.empty(((1 << 32) + 1, 1), device="meta")
+    with pytest.raises(ValueError, match=name + r".*2\^31"):
+        call(big)
