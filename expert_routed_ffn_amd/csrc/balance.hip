@@ -85,6 +85,7 @@ __device__ __forceinline__ bool row_softmax(float (&v)[N], float& inv, float& ls
 // ---- the loss --------------------------------------------------------------------
 
 constexpr int kLossWaves = 8;  // per workgroup
+constexpr int kLossParts = 256;  // workgroups at most
 
 struct LossParts {  // workspace
   double* cp;       // [column groups] sum of c_e P_e
@@ -236,18 +237,26 @@ __global__ __launch_bounds__(64 * kLossWaves) void balance_rows_kernel(
 
 // One workgroup of 16 waves per 64 columns: wave g adds parts g, g + 16, ... of its columns, the waves' shares are added
 // in wave order.  The workgroup that finishes last (a counter that the launch before set to 0) adds the column groups'
-// products, in column order whoever that is, and writes the losses.
+// products, in one order whoever that is, and writes the losses.  All of it is latency: the parts' other sums are read
+// by every workgroup's first wave at the start, beside its columns, and the products by one lane each at once.
 __global__ __launch_bounds__(1024) void balance_join_kernel(LossParts parts, int nparts, int E, int k,
                                                             float* __restrict__ loss, int32_t* __restrict__ counts) {
   __shared__ float s_p[16][kJoinCols];
   __shared__ int s_c[16][kJoinCols];
-  __shared__ uint32_t s_last;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int e = blockIdx.x * kJoinCols + lane;
-  float p = 0.0f;
-  int c = 0;
+  float p = 0.0f, zi[kLossParts / 64];
+  int c = 0, ni[kLossParts / 64];
+  if (wave == 0) {
+#pragma unroll
+    for (int i = 0; i < kLossParts / 64; ++i) {
+      const int r = 64 * i + lane;
+      zi[i] = r < nparts ? parts.z[r] : 0.0f;
+      ni[i] = r < nparts ? parts.n[r] : 0;
+    }
+  }
   if (e < E) {
-#pragma unroll 8
+#pragma unroll 16
     for (int r = wave; r < nparts; r += 16) {
       p += parts.p[(size_t)r * E + e];
       c += parts.c[(size_t)r * E + e];
@@ -263,31 +272,32 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(LossParts parts, int
     c += s_c[w][lane];
   }
   if (e < E) counts[e] = c;
-  const double cp = lanes_sum((double)p * c);
-  if (lane == 0) {
-    __hip_atomic_store(parts.cp + blockIdx.x, cp, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    s_last = __hip_atomic_fetch_add(parts.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+  double cp = lanes_sum((double)p * c);
+  if (gridDim.x > 1) {
+    uint32_t before = 0;
+    if (lane == 0) {
+      __hip_atomic_store(parts.cp + blockIdx.x, cp, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      before = __hip_atomic_fetch_add(parts.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (__builtin_amdgcn_readfirstlane(before) != gridDim.x - 1) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    cp = lane < (int)gridDim.x ? __hip_atomic_load(parts.cp + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+    cp = lanes_sum(cp);
   }
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  if (s_last != gridDim.x - 1) return;
-  float z = 0.0f;
+  double z = 0.0;
   int n = 0;
-  for (int r = lane; r < nparts; r += 64) {
-    z += parts.z[r];
-    n += parts.n[r];
+#pragma unroll
+  for (int i = 0; i < kLossParts / 64; ++i) {
+    z += zi[i];
+    n += ni[i];
   }
-  const double zt = lanes_sum((double)z);
+  z = lanes_sum(z);
   n = lanes_sum(n);
-  if (lane == 0) {
-    double all = 0.0;
-    for (int i = 0; i < (int)gridDim.x; ++i)
-      all += __hip_atomic_load(parts.cp + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    write_loss(all, zt, n, E, k, loss, counts);
-  }
+  if (lane == 0) write_loss(cp, z, n, E, k, loss, counts);
 }
 
 // Workgroups of balance_rows_kernel.  One takes all rows up to 64, which saves the second launch.
-constexpr int kLossAloneRows = 64, kLossParts = 256;
+constexpr int kLossAloneRows = 64;
 int loss_grid(int T) {
   if (T <= kLossAloneRows) return 1;
   return (int)std::min<int64_t>(kLossParts, ceil_div(T, kLossWaves));
