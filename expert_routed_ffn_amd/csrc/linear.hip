@@ -154,6 +154,7 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 struct LinearPlan {
   bool few;
   int terms;
+  bool split_first;  // fp32 x becomes term planes by a launch of its own
   Plan plan;
   size_t planes, partial, bytes;  // offsets and size of the workspace
   int R, ldp;
@@ -165,11 +166,12 @@ LinearPlan linear_plan(int T, int K, int N, int act, moe_dtype x_t, moe_dtype y_
   p.few = T <= kFewT;
   if (p.few) return p;
   p.terms = x_t == MOE_BF16 ? 1 : y_t == MOE_F32 ? 3 : 1;
-  const Shape shape{T, p.R, K, p.terms};
+  const Shape shape{T, p.R, K, p.terms, x_t == MOE_F32};
   p.plan = plan_products(&shape, 1);
   size_t o = 0;
   p.planes = o;
-  if (x_t == MOE_F32) o = up256(o + (size_t)p.terms * T * K * 2);
+  p.split_first = x_t == MOE_F32 && p.plan.shape != kDirect;
+  if (p.split_first) o = up256(o + (size_t)p.terms * T * K * 2);
   p.partial = o;
   if (p.plan.split[0] > 1) o = up256(o + (size_t)p.plan.split[0] * T * p.ldp * 4);
   p.bytes = o;
@@ -206,7 +208,7 @@ moe_status launch_linear(const void* x, moe_dtype x_t, const uint16_t* w, const 
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
   Prob p{};
   p.A = reinterpret_cast<const uint16_t*>(x);
-  if (x_t == MOE_F32) {
+  if (pl.split_first) {
     uint16_t* planes = reinterpret_cast<uint16_t*>(base + pl.planes);
     p.a_plane = (int64_t)T * K;
     if (moe_status st = launch_terms(reinterpret_cast<const float*>(x), (int64_t)T * K, planes, p.a_plane, pl.terms, s))
@@ -218,7 +220,8 @@ moe_status launch_linear(const void* x, moe_dtype x_t, const uint16_t* w, const 
   p.M = T;
   p.R = pl.R;
   p.K = K;
-  p.nseg = pl.terms;
+  p.nseg = pl.plan.shape == kDirect ? 1 : pl.terms;
+  p.terms = pl.terms;
   p.sa = 0 | 1u << 2 | 2u << 4;
   p.sb = 0;
   p.split = pl.plan.split[0];

@@ -220,7 +220,8 @@ struct Prob {
   int64_t a_plane, b_plane;
   int lda, ldb;            // elements per stored row, multiples of 8
   int M, R, K;             // C is M x R, K the reduction (a multiple of 8 where an operand is [index][k])
-  int nseg;
+  int nseg;                // of a plan of kDirect 1
+  int terms;               // kDirect: A is fp32 and enters as so many bf16 terms
   uint32_t sa, sb;         // two bits per segment: its plane of A and of B
   int split;               // parts of the reduction, each a workgroup
   float* partial;          // [split][M][ldp] when split > 1
@@ -241,9 +242,11 @@ struct Join {  // sums of the parts of up to two products, or db's
 // Sizes of a product, and how a launch of up to two cuts them.
 struct Shape {
   int M, R, K, nseg;
+  bool f32;      // A is fp32 in memory, its terms the segments: kDirect may split it as it reads it
 };
+constexpr int kDirect = 3;
 struct Plan {
-  int shape;     // 64, 128 or 256 squared tiles
+  int shape;     // 64, 128 or 256 squared tiles, or (kDirect) 64 squared ones of fp32 A
   int split[2];
 };
 Plan plan_products(const Shape* s, int count);

@@ -19,8 +19,14 @@
 //
 // Three tile shapes, chosen by plan_products.  256 x 256 (8 waves, 128 KB of LDS, one workgroup per CU) reads half as
 // much per product as 128 x 128 (4 waves, two workgroups per CU), but needs enough tiles to fill 256 CUs evenly.  64 x 64
-// tiles are for products of few tiles, whose time is the latency of their loads: four buffers keep three steps' loads
-// under way.  (Rings of 3 or 4 buffers of 32 k under the large tiles measured no better than two of 64.)
+// tiles are for products of few tiles, whose time is the latency of their loads: five buffers keep four steps' loads
+// under way, and two groups of four waves take half of each step's k (one group: 10 to 15% slower).  (Rings of 3 or 4
+// buffers of 32 k under the large tiles measured no better than two of 64.)
+//
+// fp32 A of the forward product (Direct): 64 x 64 tiles whose A stays fp32 up to the fragments, which are split into bf16
+// terms there, each value once per workgroup.  W's tile then meets all terms in one pass, and no launch writes term
+// planes: 777 x 1056 x 1001 in three terms 27.8 -> 14.4 us, 8192 x 2048 x 512 91 -> 67.  It takes three buffers (72 KB, two
+// workgroups per CU; 8192 x 2048 x 512 with four: 79).  Reading the next step's fragments ahead of the products cost 5%.
 #include <algorithm>
 #include <type_traits>
 
@@ -32,21 +38,24 @@ namespace {
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 constexpr int kBK = 64;
 
-template <int TM_, int TN_, int WM_, int WN_, int BUFFERS = 2>
+template <int TM_, int TN_, int WM_, int WN_, int BUFFERS = 2, int KG_ = 1, int A_BYTES = 2>
 struct Tile {
   static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, kRing = BUFFERS;
-  static constexpr int kThreads = 64 * WM * WN;
+  static constexpr int KG = KG_;  // groups of WM x WN waves: with two, each multiplies one 32-k half of every step
+  static constexpr int kThreads = 64 * WM * WN * KG;
   static constexpr int kFM = TM / WM / 16, kFN = TN / WN / 16;  // 16 x 16 fragments per wave
-  static constexpr int kStage = (TM + TN) * kBK;                // bf16 values of one buffer
+  static constexpr int kStageA = TM * kBK * A_BYTES / 2;        // 16-bit words of A's part of a buffer
+  static constexpr int kStage = kStageA + TN * kBK;             // and of all of it
   static constexpr int kBuffers = kRing * kStage * 2;           // bytes
   // the fp32 tile passes through the same LDS, in one piece or by rows of waves
   static constexpr int kPasses = TM * TN * 4 <= 64 * 1024 ? 1 : WM;
   static constexpr int kLds = std::max(kBuffers, TM * TN * 4 / kPasses);
 };
-using Tiny = Tile<64, 64, 2, 2, 4>;
+using Tiny = Tile<64, 64, 2, 2, 5, 2>;
+using Direct = Tile<64, 64, 4, 1, 3, 2, 4>;  // A is fp32
 using Small = Tile<128, 128, 2, 2>;
 using Large = Tile<256, 256, 2, 4>;
-static_assert(Small::kLds <= 80 * 1024 && Large::kLds <= 160 * 1024, "LDS of a CU");
+static_assert(std::max({Tiny::kLds, Direct::kLds, Small::kLds}) <= 80 * 1024 && Large::kLds <= 160 * 1024, "LDS of a CU");
 
 // Workgroup number to work item: each of the 8 dies (workgroup b runs on die b % 8) gets one contiguous range of
 // items, so that neighbouring tiles share its L2.
@@ -55,7 +64,7 @@ __device__ __forceinline__ int die_item(int b, int total) {
   return x * per + min(x, rem) + (b >> 3);
 }
 
-__device__ __forceinline__ void to_lds16(const uint16_t* g, uint16_t* l) {
+__device__ __forceinline__ void to_lds16(const void* g, uint16_t* l) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)g,
                                    (__attribute__((address_space(3))) uint32_t*)l, 16, 0, 0);
 }
@@ -69,6 +78,9 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 __device__ __forceinline__ s16x4_t read_tr(const uint16_t* __restrict__ p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
 }
+
+// (restrict for the same reason: with it 65 x 4096 x 4096 took 37 us, without 55)
+__device__ __forceinline__ f32x4_t read_f32(const float* __restrict__ p) { return *reinterpret_cast<const f32x4_t*>(p); }
 
 // Loader and reader of one operand's tile: ROWS indices (m or n) by 64 k.  `w64` is the wave's first thread.
 template <int ROWS, int THREADS, bool KROWS>
@@ -172,6 +184,52 @@ struct Operand<ROWS, THREADS, true> {  // [k][m]
   }
 };
 
+// [m][k] of fp32 values, split into TERMS bf16 terms as they are read (fragments of one row group: its terms in order).
+template <int ROWS, int THREADS, int TERMS>
+struct OperandF32 {
+  static constexpr int kPer = THREADS / 16, kLoads = ROWS / kPer;
+  uint32_t off[kLoads];
+  int chunk;  // which 16 bytes of a row's 256 this thread brings; piece c of row m lies at c ^ (m % 16)
+  template <typename Row>
+  __device__ __forceinline__ void init(int ld, int, Row row) {
+    const int r = threadIdx.x >> 4;
+    chunk = (threadIdx.x & 15) ^ (r & 15);  // kPer is a multiple of 16: the same for each load
+    static_assert(kPer % 16 == 0, "the turn repeats");
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) off[i] = (uint32_t)row(r + kPer * i) * ld + chunk * 4;
+  }
+  __device__ __forceinline__ const float* at(const float* p, size_t first, int k0, int ld) const {
+    return p + first * ld + k0;
+  }
+  __device__ __forceinline__ void load(const float* p, int, uint16_t* lds, int w64) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) to_lds16(p + off[i], lds + (i * THREADS + w64) * 8);
+  }
+  __device__ __forceinline__ void load_short(const float* p, int, int left, uint16_t* lds, int w64) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) to_lds16(p + off[i] - (chunk * 4 < left ? 0 : chunk * 4), lds + (i * THREADS + w64) * 8);
+  }
+  template <int F>
+  __device__ __forceinline__ void read(const uint16_t* lds, int base, int kk, bf16x8_t (&f)[F]) const {
+    const int r16 = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
+#pragma unroll
+    for (int i = 0; i < F / TERMS; ++i) {
+      const float* row = reinterpret_cast<const float*>(lds) + (base + 16 * i + r16) * kBK;
+      const int c = 8 * kk + 2 * q;
+      const f32x4_t a = read_f32(row + (c ^ r16) * 4);
+      const f32x4_t b = read_f32(row + ((c + 1) ^ r16) * 4);
+      uint32_t t[4][TERMS];
+      split_terms<TERMS>(a.x, a.y, t[0]);
+      split_terms<TERMS>(a.z, a.w, t[1]);
+      split_terms<TERMS>(b.x, b.y, t[2]);
+      split_terms<TERMS>(b.z, b.w, t[3]);
+#pragma unroll
+      for (int k = 0; k < TERMS; ++k)
+        f[i * TERMS + k] = __builtin_bit_cast(bf16x8_t, make_uint4(t[0][k], t[1][k], t[2][k], t[3][k]));
+    }
+  }
+};
+
 // Fragments with k = first + 8 (lane / 16) ... : values at `left` and past it become zeros.
 template <int F>
 __device__ __forceinline__ void mask_k(bf16x8_t (&f)[F], int first, int left) {
@@ -198,8 +256,9 @@ __device__ __forceinline__ void put_part(float* out, int n, int N, const float (
 }
 
 // One tile of one part of a product's reduction.  AK, BK: the operand is [k][index].  PAIR: SwiGLU, whose tiles hold
-// TN / 2 gate rows of W and the same up rows, each wave's gate rows before its up rows.
-template <typename T, bool AK, bool BK, bool PAIR>
+// TN / 2 gate rows of W and the same up rows, each wave's gate rows before its up rows.  TERMS: A is fp32 and enters as so
+// many bf16 terms, split here; 0: A is bf16.
+template <typename T, bool AK, bool BK, bool PAIR, int TERMS = 0>
 __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, uint8_t* lds) {
   constexpr int TM = T::TM, TN = T::TN, WM = T::WM, WN = T::WN, kFM = T::kFM, kFN = T::kFN, kThreads = T::kThreads;
   constexpr int cols = PAIR ? TN / 2 : TN;  // output columns per tile
@@ -213,8 +272,11 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
   const int m0 = uniform((band * 8 + in_band % band_rows) * TM), n0 = uniform(in_band / band_rows * cols);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  const int wm = wave / WN, wn = wave % WN;
-  Operand<TM, kThreads, AK> A;
+  const int kg = wave / (WM * WN), wm = wave / WN % WM, wn = wave % WN;
+  using LoaderA = std::conditional_t<TERMS != 0, OperandF32<TM, kThreads, std::max(TERMS, 1)>, Operand<TM, kThreads, AK>>;
+  using ValueA = std::conditional_t<TERMS != 0, float, uint16_t>;
+  constexpr int kTerms = std::max(TERMS, 1);
+  LoaderA A;
   Operand<TN, kThreads, BK> B;
   // rows past the end read the last one and are not stored
   A.init(p.lda, p.lda - m0, [&](int r) { return min(m0 + r, p.M - 1) - m0; });
@@ -230,21 +292,22 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
   uint16_t* const base = reinterpret_cast<uint16_t*>(lds);
   int seg = uniform(lo / seg_steps), kstep = lo - seg * seg_steps, next = lo;  // the step that is loaded next
   const int last = p.K - kBK;
-  const uint16_t *src_a, *src_b;
+  const ValueA* src_a;
+  const uint16_t* src_b;
   auto place = [&] {
-    src_a = A.at(p.A + ((p.sa >> (2 * seg)) & 3) * p.a_plane, m0, kstep * kBK, p.lda);
+    src_a = A.at(reinterpret_cast<const ValueA*>(p.A) + ((p.sa >> (2 * seg)) & 3) * p.a_plane, m0, kstep * kBK, p.lda);
     src_b = B.at(p.B + ((p.sb >> (2 * seg)) & 3) * p.b_plane, n0, kstep * kBK, p.ldb);
   };
   place();
   const int64_t step_a = AK ? (int64_t)kBK * p.lda : kBK, step_b = BK ? (int64_t)kBK * p.ldb : kBK;
   auto load = [&](int buf) {
     uint16_t* la = base + buf * T::kStage;
-    uint16_t* lb = la + TM * kBK;
+    uint16_t* lb = la + T::kStageA;
     const int k0 = kstep * kBK;
     if (k0 <= last) {
       A.load(src_a, p.lda, la, 64 * wave);
       B.load(src_b, p.ldb, lb, 64 * wave);
-    } else if (T::kRing > 2) {
+    } else if constexpr (T::kRing > 2) {
       A.load_short(src_a, p.lda, p.K - k0, la, 64 * wave);
       B.load_short(src_b, p.ldb, p.K - k0, lb, 64 * wave);
     } else {
@@ -267,17 +330,20 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
   for (int i = 0; i < kFM; ++i)
 #pragma unroll
     for (int j = 0; j < kFN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  bf16x8_t af[2][kFM], bf[2][kFN];
+  bf16x8_t af[2][kFM * kTerms], bf[2][kFN];
   auto read = [&](int buf, int kk, int w) {
     const uint16_t* la = base + buf * T::kStage;
-    B.template read<kFN>(la + TM * kBK, (TN / WN) * wn, kk, bf[w]);
-    A.template read<kFM>(la, (TM / WM) * wm, kk, af[w]);
+    B.template read<kFN>(la + T::kStageA, (TN / WN) * wn, kk, bf[w]);
+    A.template read<kFM * kTerms>(la, (TM / WM) * wm, kk, af[w]);
   };
   auto mma = [&](int w) {
 #pragma unroll
     for (int i = 0; i < kFM; ++i)
 #pragma unroll
-      for (int j = 0; j < kFN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[w][j], af[w][i], acc[i][j], 0, 0, 0);
+      for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+        for (int j = 0; j < kFN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[w][j], af[w][i * kTerms + t], acc[i][j], 0, 0, 0);
   };
   constexpr int kReads = kFM * (AK ? 2 : 1) + kFN * (BK ? 2 : 1);
   auto mix = [&] {  // the reads of the next half spread between the products of this one
@@ -298,11 +364,12 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
     asm volatile("" ::: "memory");
   };
   if constexpr (T::kRing > 2) {
-    // Few tiles: the time is the latency of the loads, so kRing - 1 steps of them are kept under way.  A step's own have
+    // The time is the latency of the loads, so kRing - 1 steps of them are kept under way.  A step's own have
     // landed once no more are outstanding than the later steps issued.  The last step of a reduction that is no multiple
     // of 64 is no exception: it loads what it can and masks both operands' fragments.
     constexpr int kPer = decltype(A)::kLoads + decltype(B)::kLoads, kLeft = (T::kRing - 2) * kPer;
-    static_assert(kLeft < 16, "vmcnt's low bits");
+    static_assert(kLeft < 64, "vmcnt's bits");
+    constexpr int kHalves = 2 / T::KG;  // of a step, per wave
     if (lo < hi) {
 #pragma unroll
       for (int i = 0; i < T::kRing - 1; ++i) load(i);
@@ -310,21 +377,21 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
       int now = 0, free = T::kRing - 1;
       auto step = [&](auto masked) {
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0070 | kLeft);  // vmcnt(kLeft) lgkmcnt(0)
+        __builtin_amdgcn_s_waitcnt(0x0070 | (kLeft & 15) | (kLeft >> 4) << 14);  // vmcnt(kLeft) lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         load(free);
-        read(now, 0, 0);
-        read(now, 1, 1);
+#pragma unroll
+        for (int w = 0; w < kHalves; ++w) read(now, T::KG == 2 ? kg : w, w);
         if constexpr (decltype(masked)::value) {
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            mask_k(af[w], 32 * w, rem);
-            mask_k(bf[w], 32 * w, rem);
+          for (int w = 0; w < kHalves; ++w) {
+            mask_k(af[w], 32 * (T::KG == 2 ? kg : w), rem);
+            mask_k(bf[w], 32 * (T::KG == 2 ? kg : w), rem);
           }
         }
-        mma(0);
-        mma(1);
+#pragma unroll
+        for (int w = 0; w < kHalves; ++w) mma(w);
         now = now + 1 == T::kRing ? 0 : now + 1;
         free = free + 1 == T::kRing ? 0 : free + 1;
       };
@@ -368,16 +435,23 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
 #pragma unroll
   for (int pass = 0; pass < T::kPasses; ++pass) {
     hand_over();  // the loads and reads of the loop, or the reads of the pass before, are done
-    if (T::kPasses == 1 || wm == pass) {
+    auto put = [&](auto add) {
 #pragma unroll
       for (int i = 0; i < kFM; ++i)
 #pragma unroll
         for (int j = 0; j < kFN; ++j) {
           const int m = (T::kPasses == 1 ? (TM / WM) * wm : 0) + 16 * i + r16, c = (TN / WN / 4) * wn + 4 * j + q;
-          *reinterpret_cast<f32x4_t*>(tile_c + (m * kPieces + (c ^ (m & 15))) * 4) = acc[i][j];
+          f32x4_t* at = reinterpret_cast<f32x4_t*>(tile_c + (m * kPieces + (c ^ (m & 15))) * 4);
+          *at = decltype(add)::value ? acc[i][j] + *at : acc[i][j];
         }
-    }
+    };
+    static_assert(T::KG == 1 || T::kPasses == 1, "groups of waves are added once");
+    if (T::KG == 2 ? kg == 1 : T::kPasses == 1 || wm == pass) put(std::false_type{});
     hand_over();
+    if constexpr (T::KG == 2) {
+      if (kg == 0) put(std::true_type{});
+      hand_over();
+    }
     // a thread keeps to four columns and walks down the rows
     static_assert(kThreads % kOutPieces == 0, "columns per thread");
     const int o = tid % kOutPieces, n = n0 + 4 * o;
@@ -410,10 +484,10 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
 }
 
 // The forward product.
-template <typename T, bool PAIR>
+template <typename T, bool PAIR, int TERMS>
 __global__ __launch_bounds__(T::kThreads, 2) void linear_product_kernel(Prob p) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[T::kLds];
-  product_tile<T, false, false, PAIR>(p, blockIdx.x, gridDim.x, lds);
+  product_tile<T, false, false, PAIR, TERMS>(p, blockIdx.x, gridDim.x, lds);
 }
 
 // db from its parts: 64 columns a workgroup; four waves take every fourth part, and their sums are added in wave order.
@@ -497,12 +571,14 @@ __global__ __launch_bounds__(256) void join_kernel(Join jn) {
 }
 
 int64_t tiles_of(const Shape& s, int side) { return ceil_div(s.M, side) * ceil_div(s.R, side); }
-int64_t steps_of(const Shape& s) { return ceil_div(s.K, kBK) * s.nseg; }
+int64_t steps_of(const Shape& s, int shape) { return ceil_div(s.K, kBK) * (shape == kDirect ? 1 : s.nseg); }
 
-// Time of a launch in microseconds, from measurements of the tile shapes over 1 to 64 K-steps and 32 to 4,096 tiles:
+// Time of a launch in microseconds, from measurements of the tile shapes over 1 to 192 K-steps and 16 to 4,096 tiles:
 // a workgroup costs a start and an epilogue besides its K-steps, less of each while it has a CU to itself, and a cut
 // reduction costs a second launch and its parts' way through memory.
-//   500 x 2048 x 1024: 64 x 64 tiles 12.1 us, 128 x 128 22.1;  65 x 4096 x 4096: 64 x 64 20.8 us, in four parts 14.6
+//   500 x 2048 x 1024: 64 x 64 tiles 12.1 us, 128 x 128 22.1;  65 x 4096 x 4096: 64 x 64 17.4 us, in four parts 14.6
+//   fp32 A, three terms: 65 x 4096 x 4096 37.3 us, in two parts 24.7, as term planes 45.8;  2048 x 2048 x 512 21.6, as
+//   planes 34.1, in two parts 26.2
 //   8192 x 2048 x 1024: 128 x 128 tiles 37.5 us, 256 x 256 (half the CUs idle) 54, in two parts 41 + 15 for the join
 //   8192 x 1024 x 2048: 43.8 against 38.8;  8192 x 4096 x 4096: 261 against 224
 //   1024 x 8192 x 2048 in parts: one 117, two 57, four 47 us
@@ -511,9 +587,11 @@ struct Rates {
   double start, step;           // with all slots taken
   double start_alone, step_alone;  // up to half of them
 };
-constexpr Rates kRates[3] = {{512, 64, 2.2, 0.40, 1.9, 0.262}, {512, 128, 3.5, 0.99, 2.7, 0.58}, {256, 256, 13.0, 1.50, 10.5, 1.19}};
+constexpr Rates kRates[3] = {{512, 64, 2.2, 0.37, 1.9, 0.205}, {512, 128, 3.5, 0.99, 2.7, 0.58}, {256, 256, 13.0, 1.50, 10.5, 1.19}};
+constexpr Rates kDirectRates[2] = {{512, 64, 2.7, 0.45, 2.5, 0.266}, {512, 64, 2.7, 0.92, 2.5, 0.52}};  // one term, three
 
-double cost_of(const Rates& r, const Shape* s, const int* split, int count) {
+double cost_of(int shape, const Shape* s, const int* split, int count) {
+  const Rates& r = shape == kDirect ? kDirectRates[s[0].nseg > 1] : kRates[shape];
   int64_t blocks = 0;
   double parts = 0;  // bytes of fp32 sums
   for (int i = 0; i < count; ++i) {
@@ -523,7 +601,7 @@ double cost_of(const Rates& r, const Shape* s, const int* split, int count) {
   const bool alone = blocks <= r.slots / 2;
   double sum = 0, longest = 0;
   for (int i = 0; i < count; ++i) {
-    const int64_t steps = ceil_div(steps_of(s[i]), split[i]);
+    const int64_t steps = ceil_div(steps_of(s[i], shape), split[i]);
     const double d = alone ? r.start_alone + r.step_alone * steps : r.start + r.step * steps;
     const int64_t n = tiles_of(s[i], r.side) * split[i];
     sum += d * (count == 1 ? (double)(ceil_div(n, r.slots) * r.slots) : (double)n);
@@ -539,13 +617,15 @@ double cost_of(const Rates& r, const Shape* s, const int* split, int count) {
 Plan plan_products(const Shape* s, int count) {
   Plan best{};
   double least = 0;
-  for (int shape = 0; shape < 3; ++shape)
+  for (int shape = 0; shape < (s[0].f32 ? 4 : 3); ++shape)
     for (int share = 1 << 20; share >= 8; share = share > 128 ? 128 : share / 2) {  // K-steps of a part, about
       Plan p{};
       p.shape = shape;
       for (int i = 0; i < count; ++i)
-        p.split[i] = (int)std::max<int64_t>(1, std::min<int64_t>(16, (steps_of(s[i]) + share / 2) / share));
-      const double c = cost_of(kRates[shape], s, p.split, count);
+        p.split[i] = (int)std::max<int64_t>(1, std::min<int64_t>(16, (steps_of(s[i], shape) + share / 2) / share));
+      double c = cost_of(shape, s, p.split, count);
+      // a launch of its own writes the term planes
+      if (s[0].f32 && shape != kDirect) c += 4.0 + (4.0 + 2.0 * s[0].nseg) * s[0].M * s[0].K / 5.0e6;
       if (least == 0 || c < least) {
         least = c;
         best = p;
@@ -556,7 +636,7 @@ Plan plan_products(const Shape* s, int count) {
 
 moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool grad, bool first_is_dw, const DbSum& db,
                            hipStream_t s, const char* what) {
-  const int side = kRates[plan.shape].side;
+  const int side = plan.shape == kDirect ? Direct::TM : kRates[plan.shape].side;
   const int64_t db_blocks = db.db ? ceil_div(db.n, 64) : 0;
   int64_t blocks[2] = {0, 0};
   Join j{};
@@ -579,17 +659,21 @@ moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool g
   auto go = [&](auto tile) {
     using T = decltype(tile);
     const dim3 threads((unsigned)T::kThreads);
-    if (grad)
+    auto forward = [&](auto kernel) { launch_k(kid, kernel, grid, threads, 0, s, p[0]); };
+    if constexpr (std::is_same_v<T, Direct>) {
+      if (p[0].terms == 1) pair ? forward(linear_product_kernel<T, true, 1>) : forward(linear_product_kernel<T, false, 1>);
+      else pair ? forward(linear_product_kernel<T, true, 3>) : forward(linear_product_kernel<T, false, 3>);
+    } else if (grad) {
       launch_k(kid, grad_products_kernel<T>, grid, threads, 0, s, p[0], p[count - 1], first_is_dw ? (int)blocks[0] : 0,
                first_is_dw ? (int)blocks[1] : (int)blocks[0], db);
-    else if (pair)
-      launch_k(kid, linear_product_kernel<T, true>, grid, threads, 0, s, p[0]);
-    else
-      launch_k(kid, linear_product_kernel<T, false>, grid, threads, 0, s, p[0]);
+    } else {
+      pair ? forward(linear_product_kernel<T, true, 0>) : forward(linear_product_kernel<T, false, 0>);
+    }
   };
   if (plan.shape == 0) go(Tiny{});
   else if (plan.shape == 1) go(Small{});
-  else go(Large{});
+  else if (plan.shape == 2) go(Large{});
+  else go(Direct{});
   if (moe_status st = check_launch(what)) return st;
   if (j.n0 + j.n1 > 0) {
     join_kernel<<<dim3((unsigned)(j.n0 + j.n1)), 256, 0, s>>>(j);

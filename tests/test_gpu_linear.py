@@ -294,3 +294,18 @@ def test_infinities_stay_where_they_are(moe, T, xt):
     dx, dw, _ = moe.linear_backward(dy.cuda(), x.cuda(), w.cuda(), need=("dx", "dw"))
     assert torch.isfinite(dx).all() and torch.isfinite(dw[:, :95]).all() and not torch.isfinite(dw[:, 95]).any()
     assert torch.equal(torch.isinf(dw[:, 95]).cpu(), dy[T - 1] != 0)
+
+
+# fp32 activations split inside the tiles: the reduction cut into parts that end on and off its last, partial step, both
+# halves of a SwiGLU tile, one term and three; and, for the largest, as planes of one term
+@pytest.mark.parametrize("T,K,N,act,yt", [(65, 4128, 201, "gelu", F32), (100, 2080, 515, "swiglu", F32),
+                                          (300, 2080, 1030, "silu", BF16), (66, 8224, 33, "swiglu", BF16),
+                                          (1000, 1056, 999, "none", F32), (4000, 4128, 4094, "none", BF16)])
+def test_fp32_activations_on_tiles(moe, T, K, N, act, yt):
+    x, w, b, r, _ = _big(T, K, N, act, F32, seed=N + T)
+    pre = torch.empty((T, w.shape[0]), dtype=yt, device="cuda")
+    y = moe.linear(x, w, bias=b, act=act, residual=r, y_dtype=yt, pre=pre)
+    ry, rz = linear64(x, w, b, act, r)
+    by, bz = linear_bounds(x, w, b, act, r, yt, yt == BF16)
+    within(y, ry, by.cpu(), "y")
+    within(pre, rz, bz.cpu(), "pre")

@@ -76,7 +76,8 @@ def _linear(x=P, x_t=BF16, w=P, bias=None, act=0, res=None, r_t=0, T=100, K=64, 
     (dict(x_t=2), EINVAL), (dict(y_t=2), EINVAL), (dict(res=P, r_t=3), EINVAL), (dict(x=None), EINVAL),
     (dict(w=None), EINVAL), (dict(y=None), EINVAL), (dict(x=ODD), EINVAL), (dict(w=ODD), EINVAL),
     (dict(ws=ODD), EINVAL), (dict(y=ODD, y_t=F32), EINVAL), (dict(bias=ODD), EINVAL),
-    (dict(x_t=F32, y_t=F32, ws=None), EWS), (dict(x_t=F32, y_t=F32, nb=16), EWS)])
+    (dict(x_t=F32, y_t=F32, T=8192, K=4096, N=4096, ws=None), EWS),
+    (dict(x_t=F32, y_t=F32, T=8192, K=4096, N=4096, nb=16), EWS)])
 def test_linear_refusals(kw, want):
     assert _linear(**kw) == want
     assert b"moe_linear" in L.moe_last_error()
