@@ -36,23 +36,31 @@ __device__ __forceinline__ int col_of(int lane, int i) {
   return VEC ? 256 * (i >> 2) + 4 * lane + (i & 3) : 64 * i + lane;
 }
 
-// A row of logits in registers; columns past E read as -inf.
+// A row of logits to registers.  The loads stand under no condition, as a conditional one is waited for where its branch
+// ends, which made each of a wave's loads a round trip of its own: columns past E read column 0 and are set to -inf by
+// mask_row when the row is worked on.
 template <int N, bool VEC>
 __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int lane, float (&v)[N]) {
   if constexpr (VEC) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
       const int c = col_of<true>(lane, i);
-      const float4 q = c < E ? *reinterpret_cast<const float4*>(row + c) : make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+      const float4 q = *reinterpret_cast<const float4*>(row + (c < E ? c : 0));
       v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = col_of<false>(lane, i);
-      v[i] = c < E ? row[c] : kNegInf;
+      v[i] = row[c < E ? c : 0];
     }
   }
+}
+template <int N, bool VEC>
+__device__ __forceinline__ void mask_row(int E, int lane, float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (col_of<VEC>(lane, i) >= E) v[i] = kNegInf;
 }
 
 // v becomes exp(v - max) (0 where v = -inf).  Returns false when every value is -inf.  `inv` = 1 / sum of those
@@ -153,15 +161,13 @@ __global__ __launch_bounds__(64 * kLossWaves) void balance_rows_kernel(
   auto fetch = [&](int r) {
 #pragma unroll
     for (int u = 0; u < U; ++u, r += step) {
-      next_keep[u] = 0;
-      if (r < T) {
-        load_row<N, VEC>(logits + (size_t)r * E, E, lane, next[u]);
-        next_id[u] = lane < k ? ids[(size_t)r * k + lane] : -1;
-        next_keep[u] = mask ? mask[r] : 1;
-      }
+      const int row = min(r, T - 1);  // (past the end: the last row again, not worked on)
+      load_row<N, VEC>(logits + (size_t)row * E, E, lane, next[u]);
+      next_id[u] = ids[(size_t)row * k + min(lane, k - 1)];
+      next_keep[u] = mask ? mask[row] : 1;
     }
   };
-  fetch(t);
+  if (T > 0) fetch(t);
   for (; t < T; t += U * step) {
     float v[U][N];
     int id[U], keep[U];
@@ -169,10 +175,11 @@ __global__ __launch_bounds__(64 * kLossWaves) void balance_rows_kernel(
     for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (int i = 0; i < N; ++i) v[u][i] = next[u][i];
-      id[u] = next_id[u];
+      mask_row<N, VEC>(E, lane, v[u]);
+      id[u] = lane < k ? next_id[u] : -1;
       keep[u] = next_keep[u];
     }
-    fetch(t + U * step);
+    if (t + U * step < T) fetch(t + U * step);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (t + u * step >= T) continue;
@@ -321,37 +328,43 @@ __global__ __launch_bounds__(64 * kGradWaves) void route_backward_kernel(
   float* gate = s_gate[wave];
   const bool has_gate = w != nullptr, has_loss = lse_in != nullptr;
   const int step = gridDim.x * kGradWaves;
+  // ahead of the rows' loads, which would otherwise all have to land before the first row is worked on
+  float cnt[N];
+  float a = 0.0f, z2 = 0.0f;
+  if (has_loss) {
+#pragma unroll
+    for (int i = 0; i < N; i += VEC ? 4 : 1) {
+      const int c = col_of<VEC>(lane, i);
+      if constexpr (VEC) {
+        const int4 q = *reinterpret_cast<const int4*>(counts + (c < E ? c : 0));  // (of columns past E: times 0)
+        cnt[i] = (float)q.x; cnt[i + 1] = (float)q.y; cnt[i + 2] = (float)q.z; cnt[i + 3] = (float)q.w;
+      } else {
+        cnt[i] = (float)counts[c < E ? c : 0];
+      }
+    }
+    const float n = (float)counts[E];
+    if (n > 0.0f) {
+      a = dloss[0] * (float)E / (n * n * (float)k);
+      z2 = 2.0f * dloss[1] / n;
+    }
+  }
   for (int t0 = blockIdx.x * kGradWaves + wave; t0 < T; t0 += U * step) {
     float v[U][N], wj[U], dwj[U], lse[U];
     int id[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int t = t0 + u * step;
+      const size_t t = min(t0 + u * step, T - 1);  // (past the end: the last row again, not worked on)
       id[u] = -1;
       wj[u] = dwj[u] = lse[u] = 0.0f;
-      if (t >= T) continue;
       if (has_loss) {
-        load_row<N, VEC>(logits + (size_t)t * E, E, lane, v[u]);
+        load_row<N, VEC>(logits + t * E, E, lane, v[u]);
         lse[u] = lse_in[t];
       }
-      if (has_gate && lane < k) {
-        id[u] = ids[(size_t)t * k + lane];
-        wj[u] = w[(size_t)t * k + lane];
-        dwj[u] = dw[(size_t)t * k + lane];
-      }
-    }
-    float cnt[N];
-    float a = 0.0f, z2 = 0.0f;
-    if (has_loss) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int c = col_of<VEC>(lane, i);
-        cnt[i] = c < E ? (float)counts[c] : 0.0f;
-      }
-      const float n = (float)counts[E];
-      if (n > 0.0f) {
-        a = dloss[0] * (float)E / (n * n * (float)k);
-        z2 = 2.0f * dloss[1] / n;
+      if (has_gate) {
+        const size_t at = t * k + min(lane, k - 1);
+        id[u] = ids[at];
+        wj[u] = w[at];
+        dwj[u] = dw[at];
       }
     }
     if (t0 < step) {  // the wave's first rows
@@ -364,6 +377,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void route_backward_kernel(
       if (t >= T) continue;
       const bool takes = !has_loss || !(lse[u] == kNegInf);  // the forward pass wrote -inf for rows that take no part
       float inv = 0.0f, own_lse = 0.0f;
+      if (has_loss) mask_row<N, VEC>(E, lane, v[u]);
       if (has_loss && takes && row_softmax<N>(v[u], inv, own_lse)) {
         float s = 0.0f;
 #pragma unroll
@@ -438,7 +452,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void route_backward_kernel(
   }
 }
 
-constexpr int kGradGrid = 1024;  // workgroups at most: four per CU, which are there at once (2,048: 14.0 us on 8,192 x 512, these 12.0)
+constexpr int kGradGrid = 1024;  // workgroups at most: four per CU, which are there at once
 
 }  // namespace
 
@@ -468,7 +482,7 @@ moe_status launch_balance_loss(const float* logits, const int32_t* ids, const ui
 moe_status launch_route_backward(const float* logits, const int32_t* ids, const float* w, const float* dw,
                                  const float* lse, const int32_t* counts, const float* dloss, int T, int E, int k,
                                  float* dlogits, hipStream_t s) {
-  const bool vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dlogits)) % 16 == 0;
+  const bool vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dlogits) | reinterpret_cast<uintptr_t>(counts)) % 16 == 0;
   const unsigned grid = (unsigned)std::min<int64_t>(kGradGrid, ceil_div(T, kGradWaves));
   auto go = [&](auto kernel) {
     launch_k(MOE_KERNEL_ROUTE_BACKWARD, kernel, dim3(grid), dim3(64 * kGradWaves), 0, s, logits, ids, w, dw, lse, counts,
