@@ -21,7 +21,8 @@ namespace moe {
 namespace {
 
 // Of dy per workgroup: 32 threads of 8 columns by 8 rows at a time, up to 64 rows; fewer where that leaves less than
-// 512 workgroups (8,192 x 512 SwiGLU: 18 us with 64 rows, 12.5 with 32; 333 x 201: 31 us with 64, 6.6 with 8).
+// 512 workgroups (8,192 x 512 SwiGLU: 11.5 us with 32
+// rows, half as long again with 64; 333 x 201: 5.1 us with 8, five times that with 64).
 constexpr int kPrepCols = 256;
 int prep_rows(int T, int N) {
   int rows = 64;
@@ -35,7 +36,7 @@ struct Prep {
   int64_t dz_plane;
   float* db_part;          // [row tiles][R], or null
   int T, N, R, ldz, terms, rows;
-  int act, bf16;           // dy's and pre's type
+  int act;
   int blocks, tiles_n;
   const float* x;          // fp32 activations to `x_terms` planes, or null
   uint16_t* xt;
@@ -43,34 +44,34 @@ struct Prep {
   int x_terms;
 };
 
-// Columns i ... i + 8 of a row, those past `left` as zeros.
-__device__ __forceinline__ void load8(const void* p, int bf16, size_t i, int left, float (&v)[8]) {
-  if (left >= 8) {
-    if (bf16) {
-      const u32x4_at2_t q = *reinterpret_cast<const u32x4_at2_t*>(reinterpret_cast<const uint16_t*>(p) + i);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+// Columns i ... i + 8 of a row; without FULL, those past `left` as zeros.
+template <bool BF16, bool FULL>
+__device__ __forceinline__ void load8(const void* p, size_t i, int left, float (&v)[8]) {
+  if constexpr (!FULL) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        v[2 * r] = __uint_as_float(w[r] << 16);
-        v[2 * r + 1] = __uint_as_float(w[r] & 0xFFFF0000u);
-      }
-    } else {
-      float a[4], b[4];
-      load4(p, 0, i, a);
-      load4(p, 0, i + 4, b);
+    for (int r = 0; r < 8; ++r) v[r] = r < left ? load_any(p, BF16, i + r) : 0.0f;
+  } else if constexpr (BF16) {
+    const u32x4_at2_t q = *reinterpret_cast<const u32x4_at2_t*>(reinterpret_cast<const uint16_t*>(p) + i);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        v[r] = a[r];
-        v[4 + r] = b[r];
-      }
+    for (int r = 0; r < 4; ++r) {
+      v[2 * r] = __uint_as_float(w[r] << 16);
+      v[2 * r + 1] = __uint_as_float(w[r] & 0xFFFF0000u);
     }
   } else {
+    float a[4], b[4];
+    load4(p, 0, i, a);
+    load4(p, 0, i + 4, b);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) v[r] = r < left ? load_any(p, bf16, i + r) : 0.0f;
+    for (int r = 0; r < 4; ++r) {
+      v[r] = a[r];
+      v[4 + r] = b[r];
+    }
   }
 }
 
 // Those 8 values as terms at element `at` of each plane.
+template <bool FULL>
 __device__ __forceinline__ void write8(uint16_t* dst, int64_t plane, int terms, size_t at, int left, const float (&v)[8]) {
   uint16_t t[8][3];
 #pragma unroll
@@ -79,7 +80,7 @@ __device__ __forceinline__ void write8(uint16_t* dst, int64_t plane, int terms, 
   for (int k = 0; k < 3; ++k) {
     if (k >= terms) continue;
     uint16_t* o = dst + k * plane + at;
-    if (left >= 8) {
+    if constexpr (FULL) {
       *reinterpret_cast<u32x4_at2_t*>(o) =
           u32x4_at2_t{t[0][k] | (uint32_t)t[1][k] << 16, t[2][k] | (uint32_t)t[3][k] << 16,
                       t[4][k] | (uint32_t)t[5][k] << 16, t[6][k] | (uint32_t)t[7][k] << 16};
@@ -91,60 +92,69 @@ __device__ __forceinline__ void write8(uint16_t* dst, int64_t plane, int terms, 
   }
 }
 
-template <bool PAIR>
+// What dz is made of: dy alone, dy and one pre-activation, or dy and a SwiGLU pair.
+enum PrepKind { kPlain, kSlope, kPair };
+
+// One row's 8 columns from n on; of rows shorter than that (not FULL) the `left` that are there.  Everything that decides which loads there are is known to the compiler, so that a
+// thread's loads are issued together (decided at run time, each was waited for before the next).
+template <int KIND, bool BF16, bool FULL>
+__device__ __forceinline__ void prep_row(const Prep& p, int t, int n, int left, float (&sa)[8], float (&su)[8]) {
+  float g[8], z[8], zu[8], a[8], u[8];
+  load8<BF16, FULL>(p.dy, (size_t)t * p.N + n, left, g);
+  if constexpr (KIND != kPlain) load8<BF16, FULL>(p.pre, (size_t)t * p.R + n, left, z);
+  if constexpr (KIND == kPair) load8<BF16, FULL>(p.pre, (size_t)t * p.R + p.N + n, left, zu);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (KIND == kPair) {
+      const float h = sigmoid(z[j]);
+      a[j] = g[j] * zu[j] * (h * __builtin_fmaf(z[j], 1.0f - h, 1.0f));
+      u[j] = g[j] * (z[j] * h);
+    } else if constexpr (KIND == kSlope) {
+      a[j] = g[j] * act_slope(p.act, z[j]);
+    } else {
+      a[j] = g[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {  // (what is not there adds zero)
+    sa[j] += a[j];
+    if constexpr (KIND == kPair) su[j] += u[j];
+  }
+  if (!p.dz) return;
+  const size_t at = (size_t)t * p.ldz + n;
+  write8<FULL>(p.dz, p.dz_plane, p.terms, at, left, a);
+  if constexpr (KIND == kPair) write8<FULL>(p.dz, p.dz_plane, p.terms, at + p.N, left, u);
+  if (n + 8 >= p.N)  // the last columns' thread also fills the row's padding
+    for (int c = p.R; c < p.ldz; ++c)
+      for (int k = 0; k < p.terms; ++k) p.dz[k * p.dz_plane + (size_t)t * p.ldz + c] = 0;
+}
+
+template <int KIND, bool BF16>
 __device__ void prep_dz(const Prep& p, int b, float (&sums)[2][8][kPrepCols]) {
+  constexpr bool PAIR = KIND == kPair;
   const int tid = threadIdx.x;
   const int tt = b / p.tiles_n, n0 = (b % p.tiles_n) * kPrepCols;
-  const int ry = tid >> 5, cx = (tid & 31) * 8, n = n0 + cx, left = p.N - n;
+  // The last columns of rows whose length is no multiple of 8 are the row's last 8: those before its own a thread
+  // computes as its neighbour does, writes the same values and leaves out of the sums.  (A path of its own for them took
+  // 7.2 us against 5.9 on 333 x 201, as the wave goes through both.)
+  const int ry = tid >> 5, own = n0 + (tid & 31) * 8, n = p.N < 8 ? own : min(own, p.N - 8);
   const int t_first = tt * p.rows + ry, t_end = min(p.T, (tt + 1) * p.rows);
   float sa[8], su[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sa[j] = su[j] = 0.0f;
-  if (left > 0) {
+  if (own < p.N) {
     for (int t = t_first; t < t_end; t += 8) {
-      float g[8], a[8], u[8];
-      load8(p.dy, p.bf16, (size_t)t * p.N + n, left, g);
-      if constexpr (PAIR) {
-        float zg[8], zu[8];
-        load8(p.pre, p.bf16, (size_t)t * p.R + n, left, zg);
-        load8(p.pre, p.bf16, (size_t)t * p.R + p.N + n, left, zu);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float h = sigmoid(zg[j]);
-          a[j] = g[j] * zu[j] * (h * __builtin_fmaf(zg[j], 1.0f - h, 1.0f));
-          u[j] = g[j] * (zg[j] * h);
-        }
-      } else if (p.act == MOE_ACT_NONE) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = g[j];
-      } else {
-        float z[8];
-        load8(p.pre, p.bf16, (size_t)t * p.N + n, left, z);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = g[j] * act_slope(p.act, z[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j < left) {
-          sa[j] += a[j];
-          if (PAIR) su[j] += u[j];
-        }
-      }
-      if (p.dz) {
-        const size_t at = (size_t)t * p.ldz + n;
-        write8(p.dz, p.dz_plane, p.terms, at, left, a);
-        if constexpr (PAIR) write8(p.dz, p.dz_plane, p.terms, at + p.N, left, u);
-        if (left <= 8)  // the last columns' thread also fills the row's padding
-          for (int c = p.R; c < p.ldz; ++c)
-            for (int k = 0; k < p.terms; ++k) p.dz[k * p.dz_plane + (size_t)t * p.ldz + c] = 0;
-      }
+      if (p.N >= 8) prep_row<KIND, BF16, true>(p, t, n, 8, sa, su);
+      else prep_row<KIND, BF16, false>(p, t, n, p.N, sa, su);
     }
   }
   if (!p.db_part) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    sums[0][ry][cx + j] = sa[j];
-    if (PAIR) sums[1][ry][cx + j] = su[j];
+    if (n + j >= own && n + j < n0 + kPrepCols) {
+      sums[0][ry][n - n0 + j] = sa[j];
+      if (PAIR) sums[1][ry][n - n0 + j] = su[j];
+    }
   }
   __syncthreads();
 #pragma unroll
@@ -156,11 +166,11 @@ __device__ void prep_dz(const Prep& p, int b, float (&sums)[2][8][kPrepCols]) {
   }
 }
 
-template <bool PAIR>
+template <int KIND, bool BF16>
 __global__ __launch_bounds__(256) void linear_prep_kernel(Prep p) {
   __shared__ float sums[2][8][kPrepCols];
   if ((int)blockIdx.x < p.blocks) {
-    prep_dz<PAIR>(p, blockIdx.x, sums);
+    prep_dz<KIND, BF16>(p, blockIdx.x, sums);
     return;
   }
   const int64_t step = (int64_t)(gridDim.x - p.blocks) * 256;
@@ -277,7 +287,6 @@ moe_status launch_linear_backward(const void* dy, moe_dtype dy_t, const void* pr
   p.N = N;
   p.R = pl.R;
   p.act = act;
-  p.bf16 = dy_t == MOE_BF16;
   p.ldz = pl.ldr;
   p.terms = pl.terms;
   p.rows = prep_rows(T, N);
@@ -299,8 +308,11 @@ moe_status launch_linear_backward(const void* dy, moe_dtype dy_t, const void* pr
   p.blocks = (int)blocks;
   if (blocks + x_blocks > 0) {
     const dim3 grid((unsigned)(blocks + x_blocks));
-    if (act == MOE_ACT_SWIGLU) linear_prep_kernel<true><<<grid, 256, 0, s>>>(p);
-    else linear_prep_kernel<false><<<grid, 256, 0, s>>>(p);
+    auto go = [&](auto kernel) { kernel<<<grid, 256, 0, s>>>(p); };
+    const bool bf16 = dy_t == MOE_BF16;
+    if (act == MOE_ACT_SWIGLU) bf16 ? go(linear_prep_kernel<kPair, true>) : go(linear_prep_kernel<kPair, false>);
+    else if (act == MOE_ACT_NONE) bf16 ? go(linear_prep_kernel<kPlain, true>) : go(linear_prep_kernel<kPlain, false>);
+    else bf16 ? go(linear_prep_kernel<kSlope, true>) : go(linear_prep_kernel<kSlope, false>);
     if (moe_status st = check_launch("linear_backward")) return st;
   }
 
