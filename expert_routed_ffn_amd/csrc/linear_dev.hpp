@@ -158,11 +158,18 @@ __device__ __forceinline__ void epi_rows_act(const Epi& e, int m, int n, int row
   size_t i = (size_t)m * e.N + n, ip = (size_t)m * e.R + n;
   const size_t di = (size_t)STEP * e.N, dp = (size_t)STEP * e.R;
   for (int d = 0; d < rows; d += 4 * STEP) {
-    float res[4][4];
+    float res[4][4] = {};
+    if (e.res) {  // (rows past the last read the first of the four: a load under a condition is waited for at its end)
+      size_t at[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      res[k][0] = res[k][1] = res[k][2] = res[k][3] = 0.0f;
-      if (e.res && d + k * STEP < rows) load4(e.res, e.res_bf16, i + k * di, res[k]);
+      for (int k = 0; k < 4; ++k) at[k] = i + (d + k * STEP < rows ? k * di : 0);
+      if (e.res_bf16) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) load4(e.res, 1, at[k], res[k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) load4(e.res, 0, at[k], res[k]);
+      }
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {

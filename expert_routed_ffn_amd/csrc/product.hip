@@ -272,7 +272,7 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
   const int m0 = uniform((band * 8 + in_band % band_rows) * TM), n0 = uniform(in_band / band_rows * cols);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  const int kg = wave / (WM * WN), wm = wave / WN % WM, wn = wave % WN;
+  const int kg = wave / (WM * WN), wm = T::KG == 1 ? wave / WN : wave / WN % WM, wn = wave % WN;
   using LoaderA = std::conditional_t<TERMS != 0, OperandF32<TM, kThreads, std::max(TERMS, 1)>, Operand<TM, kThreads, AK>>;
   using ValueA = std::conditional_t<TERMS != 0, float, uint16_t>;
   constexpr int kTerms = std::max(TERMS, 1);
@@ -446,12 +446,14 @@ __device__ __forceinline__ void product_tile(const Prob& p, int b, int total, ui
         }
     };
     static_assert(T::KG == 1 || T::kPasses == 1, "groups of waves are added once");
-    if (T::KG == 2 ? kg == 1 : T::kPasses == 1 || wm == pass) put(std::false_type{});
-    hand_over();
     if constexpr (T::KG == 2) {
-      if (kg == 0) put(std::true_type{});
+      if (kg == 1) put(std::false_type{});
       hand_over();
+      if (kg == 0) put(std::true_type{});
+    } else {
+      if (T::kPasses == 1 || wm == pass) put(std::false_type{});
     }
+    hand_over();
     // a thread keeps to four columns and walks down the rows
     static_assert(kThreads % kOutPieces == 0, "columns per thread");
     const int o = tid % kOutPieces, n = n0 + 4 * o;
