@@ -62,6 +62,22 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(const void* 
 #pragma unroll
   for (int f = 0; f < TF; ++f) xoff[f] = (size_t)min(16 * f + fr, T - 1) * K + fq * 8;
 
+  // The results this thread will finish, with their bias and residual, which are read here beside the first weights.
+  constexpr int kElems = (TF * 256 + 64 * kFewWaves - 1) / (64 * kFewWaves);
+  struct {
+    int t, n, r;  // t < 0: none
+    EpiIn in;
+  } el[kElems];
+#pragma unroll
+  for (int i = 0; i < kElems; ++i) {
+    const int at = i * 64 * kFewWaves + threadIdx.x;
+    el[i].r = at & 15;
+    el[i].n = blockIdx.x * (pair ? 8 : 16) + el[i].r;
+    const bool has = at < TF * 256 && at >> 4 < T && el[i].n < e.N && !(pair && el[i].r >= 8);
+    el[i].t = has ? at >> 4 : -1;
+    if (has) el[i].in = epi_in(e, el[i].t, el[i].n);
+  }
+
   f32x4_t acc[TF];
 #pragma unroll
   for (int f = 0; f < TF; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -125,17 +141,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(const void* 
     for (int i = 1; i < kFewWaves; ++i) v += red[i][f][l][r & 3];
     return v;
   };
-  for (int i = threadIdx.x; i < TF * 256; i += 64 * kFewWaves) {
-    const int r = i & 15, tk = (i >> 4) & 15, f = i >> 8;
-    const int t = 16 * f + tk;
-    if (t >= T) continue;
-    if (pair) {
-      const int n = blockIdx.x * 8 + r;
-      if (r < 8 && n < e.N) epi_one(e, t, n, total(f, r, tk), total(f, r + 8, tk));
-    } else {
-      const int n = blockIdx.x * 16 + r;
-      if (n < e.N) epi_one(e, t, n, total(f, r, tk), 0.0f);
-    }
+#pragma unroll
+  for (int i = 0; i < kElems; ++i) {
+    if (el[i].t < 0) continue;
+    const int f = el[i].t >> 4, tk = el[i].t & 15;
+    epi_one(e, el[i].t, el[i].n, total(f, el[i].r, tk), pair ? total(f, el[i].r + 8, tk) : 0.0f, el[i].in);
   }
 }
 

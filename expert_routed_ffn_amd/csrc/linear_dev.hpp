@@ -128,20 +128,31 @@ __device__ __forceinline__ void store_any(void* p, int bf16, size_t i, float v) 
   if (bf16) reinterpret_cast<uint16_t*>(p)[i] = f32_to_bf16(v);
   else reinterpret_cast<float*>(p)[i] = v;
 }
-// One element; zu is the up value of a SwiGLU pair.
-__device__ __forceinline__ void epi_one(const Epi& e, int m, int n, float z, float zu) {
-  const bool pair = e.act == MOE_ACT_SWIGLU;
+// What the epilogue of one element reads, so that it can be read before the product is there.
+struct EpiIn {
+  float b = 0.0f, bu = 0.0f, res = 0.0f;
+};
+__device__ __forceinline__ EpiIn epi_in(const Epi& e, int m, int n) {
+  EpiIn in;
   if (e.bias) {
-    z += e.bias[n];
-    if (pair) zu += e.bias[e.N + n];
+    in.b = e.bias[n];
+    if (e.act == MOE_ACT_SWIGLU) in.bu = e.bias[e.N + n];
   }
+  if (e.res) in.res = load_any(e.res, e.res_bf16, (size_t)m * e.N + n);
+  return in;
+}
+// One element; zu is the up value of a SwiGLU pair.
+__device__ __forceinline__ void epi_one(const Epi& e, int m, int n, float z, float zu, const EpiIn& in) {
+  const bool pair = e.act == MOE_ACT_SWIGLU;
+  z += in.b;
+  zu += in.bu;
   if (e.pre) {
     store_any(e.pre, e.y_bf16, (size_t)m * e.R + n, z);
     if (pair) store_any(e.pre, e.y_bf16, (size_t)m * e.R + e.N + n, zu);
   }
   float v = pair ? z * sigmoid(z) * zu : act_value(e.act, z);
   const size_t i = (size_t)m * e.N + n;
-  if (e.res) v += load_any(e.res, e.res_bf16, i);
+  v += in.res;
   store_any(e.y, e.y_bf16, i, v);
 }
 // Columns n .. n + 3 (n < N; those past N are left out) of rows m, m + STEP, ...: `rows` rows from m on, whose products
@@ -206,7 +217,7 @@ __device__ __forceinline__ void epi_rows(const Epi& e, int m, int n, int rows, V
       value(d, z, zu);
 #pragma unroll
       for (int r = 0; r < 3; ++r)
-        if (n + r < e.N) epi_one(e, m + d, n + r, z[r], zu[r]);
+        if (n + r < e.N) epi_one(e, m + d, n + r, z[r], zu[r], epi_in(e, m + d, n + r));
     }
   } else if (PAIR) {
     epi_rows_act<PAIR, STEP, MOE_ACT_SWIGLU>(e, m, n, rows, value);
