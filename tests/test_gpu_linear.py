@@ -309,3 +309,19 @@ def test_fp32_activations_on_tiles(moe, T, K, N, act, yt):
     by, bz = linear_bounds(x, w, b, act, r, yt, yt == BF16)
     within(y, ry, by.cpu(), "y")
     within(pre, rz, bz.cpu(), "pre")
+
+
+@pytest.mark.parametrize("T,K,N,act,xt,gt", [(1, 224, 111, "swiglu", BF16, BF16), (6, 256, 19, "gelu", BF16, F32),
+                                             (2, 96, 40, "none", F32, F32), (1, 64, 8000, "silu", F32, BF16)])
+def test_few_values_of_dz_are_not_rounded(moe, T, K, N, act, xt, gt):
+    """bf16 gradients of few tokens are the rounded exact ones but for fp32's part of the error: half a step of bf16,
+    and what two terms leave of dz (and of fp32 x), 2^-16 of the sums' magnitudes each, counted double."""
+    x, w, _, r = _inputs(T, K, N, act, xt, seed=N, res=gt)
+    pre = torch.randn((T, w.shape[0]), generator=torch.Generator().manual_seed(N + 1)).to(gt)
+    dx, dw, _ = moe.linear_backward(r.cuda(), x.cuda(), w.cuda(), act=act, pre=pre.cuda(), dx_dtype=BF16, dw_dtype=BF16)
+    rx, rw, _, dz = linear_grad64(r, x, w, act, pre)
+    # bounds of the fp32 results, whose dz carries the activation's own error
+    bx, bw, _ = linear_grad_bounds(r, x, w, act, pre, F32, F32)
+    za = dz.abs()
+    within(dx, rx, bx + 2.0 ** -8 * (rx.abs() + bx) + 2 * 2.0 ** -16 * (za @ w.double().abs()), "dx")
+    within(dw, rw, bw + 2.0 ** -8 * (rw.abs() + bw) + 4 * 2.0 ** -16 * (za.t() @ x.double().abs()), "dw")
