@@ -1,0 +1,63 @@
+"""GPU: what the dense product and its gradient round, and what they do not.
+
+The exact tests use whole numbers whose products and sums fp32 holds exactly (below 2^24), with operands of 12 bits that one
+bf16 does not hold: a bf16 result is then the exact sum rounded once, to the nearest and ties to even, bit for bit.  An
+operand that was rounded to bf16 on the way would show in most elements.
+"""
+import pytest
+import torch
+
+from tests._train_ref import linear_grad64, linear_grad_bounds, rows_of, within
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def moe():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import expert_routed_ffn_amd as m
+    return m
+
+
+def _whole(shape, most, seed, dtype):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(-most, most + 1, shape, generator=g, device="cuda").to(dtype)
+
+
+def _rounded(exact):
+    """A float64 tensor of values that fp32 holds, rounded once to bf16."""
+    assert exact.abs().max() < 1 << 24
+    return exact.float().to(BF16)
+
+
+# more than 2^14 values of dz, fewer and more tokens than a part of the reduction, odd columns, each tile shape
+@pytest.mark.parametrize("T,K,N", [(300, 96, 200), (1000, 64, 33), (4000, 512, 520), (3000, 2048, 1001), (1, 64, 8000)])
+@pytest.mark.parametrize("xt", [BF16, F32])
+def test_bf16_gradients_of_fp32_dy_are_rounded_once(moe, T, K, N, xt):
+    dy = _whole((T, N), 2047, T + N, F32)
+    x, w = _whole((T, K), 1, K, xt), _whole((N, K), 2, N, BF16)
+    dx, dw, db = moe.linear_backward(dy, x, w, dx_dtype=BF16, dw_dtype=BF16)
+    rx, rw, rb, _ = linear_grad64(dy, x, w, "none", None)
+    assert torch.equal(dx, _rounded(rx))
+    assert torch.equal(dw, _rounded(rw))
+    assert torch.equal(db.double(), rb)
+
+
+# the same behind an activation, where dz is no whole number.  The bounds of the fp32 results carry dz's own error and that
+# of the sums; beside those a result is off by half a step of bf16 and by what two terms leave of dz, 2^-17 of it.
+@pytest.mark.parametrize("T,K,N,act,gt", [(400, 96, 65, "swiglu", BF16), (300, 224, 201, "gelu", F32),
+                                          (500, 64, 300, "silu", BF16)])
+def test_bf16_gradients_behind_an_activation_are_rounded_once(moe, T, K, N, act, gt):
+    g = torch.Generator().manual_seed(T + K)
+    R = rows_of(act, N)
+    x, dy = torch.randn((T, K), generator=g).to(BF16), torch.randn((T, N), generator=g).to(gt)
+    w = (torch.randn((R, K), generator=g) / K ** 0.5).to(BF16)
+    pre = torch.randn((T, R), generator=g).to(gt)
+    dx, dw, _ = moe.linear_backward(dy.cuda(), x.cuda(), w.cuda(), act=act, pre=pre.cuda(), dx_dtype=BF16, dw_dtype=BF16)
+    rx, rw, _, dz = linear_grad64(dy, x, w, act, pre)
+    bx, bw, _ = linear_grad_bounds(dy, x, w, act, pre, F32, F32)
+    za = dz.abs()
+    within(dx, rx, bx + 2.0 ** -8 * (rx.abs() + bx) + 2.0 ** -17 * (za @ w.double().abs()), "dx")
+    within(dw, rw, bw + 2.0 ** -8 * (rw.abs() + bw) + 2.0 ** -17 * (za.t() @ x.double().abs()), "dw")
