@@ -177,8 +177,7 @@ __global__ __launch_bounds__(256) void linear_prep_kernel(Prep p) {
   }
   const int64_t step = (int64_t)(gridDim.x - p.blocks) * 256;
   for (int64_t i = (int64_t)(blockIdx.x - p.blocks) * 256 + threadIdx.x; i < p.x4; i += step) {
-    if (p.x_terms == 1) write_terms<1>(p.x, i, p.xt, p.x_plane);
-    else if (p.x_terms == 2) write_terms<2>(p.x, i, p.xt, p.x_plane);
+    if (p.x_terms == 2) write_terms<2>(p.x, i, p.xt, p.x_plane);
     else write_terms<3>(p.x, i, p.xt, p.x_plane);
   }
 }
@@ -225,7 +224,7 @@ GradPlan grad_plan(int T, int K, int N, int act, moe_dtype dy_t, moe_dtype x_t, 
   p.dx_terms = one ? 1 : dx_t == MOE_BF16 ? 2 : 3;
   p.dw_terms = one ? 1 : dw_t == MOE_BF16 ? 2 : 3;
   p.terms = std::max(p.dx ? p.dx_terms : 1, p.dw ? p.dw_terms : 1);
-  p.x_terms = x_t == MOE_BF16 ? 1 : dw_t == MOE_F32 ? 3 : one ? 1 : 2;
+  p.x_terms = x_t == MOE_BF16 ? 1 : dw_t == MOE_F32 ? 3 : 2;
   // (the products load 16 bytes of a row at a time)
   p.direct = one && p.R % 8 == 0;
   p.segs_dx = segments(p.dx_terms, 1, p.dx_sa, p.dx_sb);

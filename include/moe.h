@@ -478,8 +478,8 @@ enum { MOE_NEED_DX = 1, MOE_NEED_DW = 2, MOE_NEED_DB = 4 };
  *        the MOE_NEED_* bits of the outputs that are not NULL.
  * dx and dw must be 16-byte aligned; outputs may not overlap the inputs that are
  * read or each other.  Sums in fp32.  An fp32 dx or dw comes from dz (and x) at
- * full precision; a bf16 one from dz to within 2^-17 of each value, then rounded
- * once.
+ * full precision; a bf16 one from dz (and fp32 x) to within 2^-17 of each value,
+ * then rounded once.
  * An infinite or NaN dz or x makes the elements it enters infinite or NaN, where
  * an infinity may become a NaN.
  * Errors: MOE_EINVAL (no output wanted among that), MOE_EUNSUPPORTED, MOE_EWORKSPACE.

@@ -61,3 +61,13 @@ def test_bf16_gradients_behind_an_activation_are_rounded_once(moe, T, K, N, act,
     za = dz.abs()
     within(dx, rx, bx + 2.0 ** -8 * (rx.abs() + bx) + 2.0 ** -17 * (za @ w.double().abs()), "dx")
     within(dw, rw, bw + 2.0 ** -8 * (rw.abs() + bw) + 2.0 ** -17 * (za.t() @ x.double().abs()), "dw")
+
+
+# dy in bf16 without an activation is dz as it stands, and fp32 x is what would be rounded
+@pytest.mark.parametrize("T,K,N", [(1, 64, 40), (3, 96, 8), (6, 2048, 512), (300, 96, 200), (4000, 512, 520), (2000, 1024, 33)])
+def test_bf16_weight_gradient_takes_fp32_activations_unrounded(moe, T, K, N):
+    dy, x, w = _whole((T, N), 2, N, BF16), _whole((T, K), 2047, K, F32), _whole((N, K), 1, T, BF16)
+    dx, dw, db = moe.linear_backward(dy, x, w, dx_dtype=BF16, dw_dtype=BF16)
+    rx, rw, rb, _ = linear_grad64(dy, x, w, "none", None)
+    assert torch.equal(dw, _rounded(rw))
+    assert torch.equal(dx, _rounded(rx)) and torch.equal(db.double(), rb)
