@@ -3,8 +3,10 @@
 //
 // Up to 64 tokens: linear_few_kernel, weights straight from memory into matrix operands, the reduction split over the
 // waves of a workgroup.  More: the tiled product of product.hip.  Sums in fp32.  fp32 activations enter
-// as bf16 terms (bf16_terms in linear_dev.hpp): three, which hold them exactly, when y is fp32; one, a rounding by at
-// most 2^-9 relative that y's own rounding to bf16 matches, when y is bf16 and the product is tiled.
+// as bf16 terms (split_terms in linear_dev.hpp): three, which hold them exactly, when y is fp32 or the tokens are few; two,
+// which leave at most 2^-17 of each value (2^-9 of the half step that y's rounding costs), when y is bf16 and the product is
+// tiled.  (One term there was off by up to 2^-8 of each value, as much again as y's rounding, and gave a token another
+// value in a batch of more than 64.)
 #include <algorithm>
 
 #include "linear_dev.hpp"
@@ -166,6 +168,7 @@ struct LinearPlan {
   int terms;
   bool split_first;  // fp32 x becomes term planes by a launch of its own
   Plan plan;
+  int rows;          // tokens at a time: all, or half of them
   size_t planes, partial, bytes;  // offsets and size of the workspace
   int R, ldp;
 };
@@ -175,15 +178,18 @@ LinearPlan linear_plan(int T, int K, int N, int act, moe_dtype x_t, moe_dtype y_
   p.ldp = (p.R + 3) / 4 * 4;
   p.few = T <= kFewT;
   if (p.few) return p;
-  p.terms = x_t == MOE_BF16 ? 1 : y_t == MOE_F32 ? 3 : 1;
-  const Shape shape{T, p.R, K, p.terms, x_t == MOE_F32};
+  p.terms = x_t == MOE_BF16 ? 1 : y_t == MOE_F32 ? 3 : 2;
+  // Two planes are made and used for half of the tokens at a time, so that they take the memory of x in bf16 beside a bf16 y.
+  const int turns = p.terms == 2 ? 2 : 1;
+  const Shape shape{T, p.R, K, p.terms, x_t == MOE_F32, turns};
   p.plan = plan_products(&shape, 1);
+  p.split_first = x_t == MOE_F32 && p.plan.shape != kDirect;
+  p.rows = p.split_first ? (int)ceil_div(T, turns) : T;
   size_t o = 0;
   p.planes = o;
-  p.split_first = x_t == MOE_F32 && p.plan.shape != kDirect;
-  if (p.split_first) o = up256(o + (size_t)p.terms * T * K * 2);
+  if (p.split_first) o = up256(o + (size_t)p.terms * p.rows * K * 2);
   p.partial = o;
-  if (p.plan.split[0] > 1) o = up256(o + (size_t)p.plan.split[0] * T * p.ldp * 4);
+  if (p.plan.split[0] > 1) o = up256(o + (size_t)p.plan.split[0] * p.rows * p.ldp * 4);
   p.bytes = o;
   return p;
 }
@@ -192,7 +198,7 @@ LinearPlan linear_plan(int T, int K, int N, int act, moe_dtype x_t, moe_dtype y_
 
 static moe_status launch_terms(const float* x, int64_t n, uint16_t* planes, int64_t plane, int terms, hipStream_t s) {
   const dim3 grid((unsigned)std::min<int64_t>(2048, ceil_div(n / 4, 256)));
-  if (terms == 1) terms_kernel<1><<<grid, 256, 0, s>>>(x, n / 4, planes, plane);
+  if (terms == 2) terms_kernel<2><<<grid, 256, 0, s>>>(x, n / 4, planes, plane);
   else terms_kernel<3><<<grid, 256, 0, s>>>(x, n / 4, planes, plane);
   return check_launch("linear");
 }
@@ -216,29 +222,40 @@ moe_status launch_linear(const void* x, moe_dtype x_t, const uint16_t* w, const 
     return check_launch("linear");
   }
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
-  Prob p{};
-  p.A = reinterpret_cast<const uint16_t*>(x);
-  if (pl.split_first) {
-    uint16_t* planes = reinterpret_cast<uint16_t*>(base + pl.planes);
-    p.a_plane = (int64_t)T * K;
-    if (moe_status st = launch_terms(reinterpret_cast<const float*>(x), (int64_t)T * K, planes, p.a_plane, pl.terms, s))
-      return st;
-    p.A = planes;
+  for (int t = 0; t < T; t += pl.rows) {
+    const int n = std::min(pl.rows, T - t);
+    auto from = [&](const void* q, size_t row_bytes) {  // row t of a buffer, or null
+      return q ? reinterpret_cast<const uint8_t*>(q) + (size_t)t * row_bytes : nullptr;
+    };
+    const size_t by = y_t == MOE_F32 ? 4 : 2;
+    Prob p{};
+    p.A = reinterpret_cast<const uint16_t*>(from(x, (size_t)K * (x_t == MOE_F32 ? 4 : 2)));
+    if (pl.split_first) {
+      uint16_t* planes = reinterpret_cast<uint16_t*>(base + pl.planes);
+      p.a_plane = (int64_t)n * K;
+      if (moe_status st = launch_terms(reinterpret_cast<const float*>(p.A), (int64_t)n * K, planes, p.a_plane, pl.terms, s))
+        return st;
+      p.A = planes;
+    }
+    p.B = w;
+    p.lda = p.ldb = K;
+    p.M = n;
+    p.R = pl.R;
+    p.K = K;
+    p.nseg = pl.plan.shape == kDirect ? 1 : pl.terms;
+    p.terms = pl.terms;
+    p.sa = 0 | 1u << 2 | 2u << 4;
+    p.sb = 0;
+    p.split = pl.plan.split[0];
+    p.partial = reinterpret_cast<float*>(base + pl.partial);
+    p.ldp = pl.ldp;
+    p.epi = e;
+    p.epi.res = from(residual, (size_t)N * (r_t == MOE_F32 ? 4 : 2));
+    p.epi.y = const_cast<uint8_t*>(from(y, (size_t)N * by));
+    p.epi.pre = const_cast<uint8_t*>(from(pre, (size_t)pl.R * by));
+    if (moe_status st = launch_products(MOE_KERNEL_LINEAR, pl.plan, &p, 1, false, false, DbSum{}, s, "linear")) return st;
   }
-  p.B = w;
-  p.lda = p.ldb = K;
-  p.M = T;
-  p.R = pl.R;
-  p.K = K;
-  p.nseg = pl.plan.shape == kDirect ? 1 : pl.terms;
-  p.terms = pl.terms;
-  p.sa = 0 | 1u << 2 | 2u << 4;
-  p.sb = 0;
-  p.split = pl.plan.split[0];
-  p.partial = reinterpret_cast<float*>(base + pl.partial);
-  p.ldp = pl.ldp;
-  p.epi = e;
-  return launch_products(MOE_KERNEL_LINEAR, pl.plan, &p, 1, false, false, DbSum{}, s, "linear");
+  return MOE_OK;
 }
 
 }  // namespace moe

@@ -261,6 +261,7 @@ struct Join {  // sums of the parts of up to two products, or db's
 struct Shape {
   int M, R, K, nseg;
   bool f32;      // A is fp32 in memory, its terms the segments: kDirect may split it as it reads it
+  int turns;     // launches that its term planes take otherwise, each with its share of the rows
 };
 constexpr int kDirect = 3;
 struct Plan {

@@ -579,6 +579,7 @@ int64_t steps_of(const Shape& s, int shape) { return ceil_div(s.K, kBK) * (shape
 // a workgroup costs a start and an epilogue besides its K-steps, less of each while it has a CU to itself, and a cut
 // reduction costs a second launch and its parts' way through memory.
 //   500 x 2048 x 1024: 64 x 64 tiles 12.1 us, 128 x 128 22.1;  65 x 4096 x 4096: 64 x 64 17.4 us, in four parts 14.6
+//   fp32 A, two terms: 2048 x 512 x 512 7.9 us, x 4096 x 512 32.0; 4096 x 512 x 512 10.8 us, x 4096 x 512 49.8
 //   fp32 A, three terms: 65 x 4096 x 4096 37.3 us, in two parts 24.7, as term planes 45.8;  2048 x 2048 x 512 21.6, as
 //   planes 34.1, in two parts 26.2
 //   8192 x 2048 x 1024: 128 x 128 tiles 37.5 us, 256 x 256 (half the CUs idle) 54, in two parts 41 + 15 for the join
@@ -590,10 +591,10 @@ struct Rates {
   double start_alone, step_alone;  // up to half of them
 };
 constexpr Rates kRates[3] = {{512, 64, 2.2, 0.37, 1.9, 0.205}, {512, 128, 3.5, 0.99, 2.7, 0.58}, {256, 256, 13.0, 1.50, 10.5, 1.19}};
-constexpr Rates kDirectRates[2] = {{512, 64, 2.7, 0.45, 2.5, 0.266}, {512, 64, 2.7, 0.92, 2.5, 0.52}};  // one term, three
+constexpr Rates kDirectRates[2] = {{512, 64, 2.7, 0.69, 2.5, 0.42}, {512, 64, 2.7, 0.92, 2.5, 0.52}};  // two terms, three
 
 double cost_of(int shape, const Shape* s, const int* split, int count) {
-  const Rates& r = shape == kDirect ? kDirectRates[s[0].nseg > 1] : kRates[shape];
+  const Rates& r = shape == kDirect ? kDirectRates[s[0].nseg > 2] : kRates[shape];
   int64_t blocks = 0;
   double parts = 0;  // bytes of fp32 sums
   for (int i = 0; i < count; ++i) {
@@ -625,9 +626,14 @@ Plan plan_products(const Shape* s, int count) {
       p.shape = shape;
       for (int i = 0; i < count; ++i)
         p.split[i] = (int)std::max<int64_t>(1, std::min<int64_t>(16, (steps_of(s[i], shape) + share / 2) / share));
-      double c = cost_of(shape, s, p.split, count);
-      // a launch of its own writes the term planes
-      if (s[0].f32 && shape != kDirect) c += 4.0 + (4.0 + 2.0 * s[0].nseg) * s[0].M * s[0].K / 5.0e6;
+      double c;
+      if (s[0].f32 && shape != kDirect) {  // a launch of its own writes the term planes
+        Shape turn = s[0];
+        turn.M = (int)ceil_div(s[0].M, s[0].turns);
+        c = s[0].turns * (cost_of(shape, &turn, p.split, 1) + 4.0 + (4.0 + 2.0 * turn.nseg) * turn.M * turn.K / 5.0e6);
+      } else {
+        c = cost_of(shape, s, p.split, count);
+      }
       if (least == 0 || c < least) {
         least = c;
         best = p;
@@ -663,7 +669,7 @@ moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool g
     const dim3 threads((unsigned)T::kThreads);
     auto forward = [&](auto kernel) { launch_k(kid, kernel, grid, threads, 0, s, p[0]); };
     if constexpr (std::is_same_v<T, Direct>) {
-      if (p[0].terms == 1) pair ? forward(linear_product_kernel<T, true, 1>) : forward(linear_product_kernel<T, false, 1>);
+      if (p[0].terms == 2) pair ? forward(linear_product_kernel<T, true, 2>) : forward(linear_product_kernel<T, false, 2>);
       else pair ? forward(linear_product_kernel<T, true, 3>) : forward(linear_product_kernel<T, false, 3>);
     } else if (grad) {
       launch_k(kid, grad_products_kernel<T>, grid, threads, 0, s, p[0], p[count - 1], first_is_dw ? (int)blocks[0] : 0,

@@ -454,7 +454,7 @@ typedef enum moe_act {
  *   ws        moe_linear_workspace_bytes(T, K, N, act, x_t, y_t) bytes, 256-byte aligned
  *             (the query answers 0 for sizes that the call refuses).
  * Sums in fp32.  fp32 x is used to full precision when y is fp32 or T <= 64; a
- * bf16 y of more tokens takes x rounded to bf16.  T <= 2^20.
+ * bf16 y of more tokens takes x to within 2^-17 of each value.  T <= 2^20.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE.
  */
 size_t moe_linear_workspace_bytes(int T, int K, int N, moe_act act, moe_dtype x_t, moe_dtype y_t);

@@ -71,3 +71,28 @@ def test_bf16_weight_gradient_takes_fp32_activations_unrounded(moe, T, K, N):
     rx, rw, rb, _ = linear_grad64(dy, x, w, "none", None)
     assert torch.equal(dw, _rounded(rw))
     assert torch.equal(dx, _rounded(rx)) and torch.equal(db.double(), rb)
+
+
+# fewest tokens that take tiles, reductions cut into parts, rows past the last tile, an odd number of tokens above and below
+# a tile's half, columns off the tile, the largest
+@pytest.mark.parametrize("T,K,N", [(64, 96, 33), (65, 96, 33), (65, 4096, 512), (301, 544, 515), (2000, 64, 9), (1001, 4096, 1024),
+                                   (4001, 2080, 2047), (8192, 4096, 4096)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_bf16_product_of_fp32_activations_is_rounded_once(moe, T, K, N, act):
+    if act == "swiglu" and T == 8192:
+        N = 1024
+    R = rows_of(act, N)
+    x, w = _whole((T, K), 2047, T, F32), _whole((R, K), 1, N, BF16)
+    bias, res = _whole((R,), 1000, K, F32), _whole((T, N), 100, K + 1, BF16)
+    pre = torch.empty((T, R), dtype=BF16, device="cuda")
+    y = moe.linear(x, w, bias=bias, act=act, residual=res, y_dtype=BF16, pre=pre)
+    z = x.double() @ w.double().t() + bias.double()
+    assert torch.equal(pre, _rounded(z))
+    if act == "none":
+        assert torch.equal(y, _rounded(z + res.double()))
+
+
+def test_a_token_keeps_its_value_in_a_larger_batch(moe):
+    x, w = _whole((200, 256), 2047, 1, F32), _whole((70, 256), 2, 2, BF16)
+    few, many = moe.linear(x[:64], w, y_dtype=BF16), moe.linear(x, w, y_dtype=BF16)
+    assert torch.equal(few, many[:64])
