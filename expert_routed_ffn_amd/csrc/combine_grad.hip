@@ -86,9 +86,11 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(const YT* __
   const size_t row0 = t * k + j0;
   float wj[J], dot[J];
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    wj[j] = j < nj ? w[row0 + j] : 0.0f;
-    dot[j] = 0.0f;
+  for (int j = 0; j < J; ++j) wj[j] = dot[j] = 0.0f;
+  if (dy) {  // (w may be null without dy)
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (j < nj) wj[j] = w[row0 + j];
   }
   for (int c = tid * C; c < H; c += kThreads * C) {
     Raw<YT, C> rows[J];

@@ -97,3 +97,22 @@ def test_most_tokens(moe):
     dw, dy = moe.combine_backward(y, w, dout)
     assert torch.equal(dw[:, 0], (y[:, 0].float() * dout.float()).sum(1))
     assert torch.equal(dy[:, 0].float(), w * dout.float())
+
+
+@pytest.mark.parametrize("T,k,H", [(3, 2, 64), (300, 9, 96), (300, 4, 36)])
+@pytest.mark.parametrize("yt,gt", [(F32, BF16), (BF16, F32)])
+def test_what_an_output_does_not_need_may_be_null(moe, T, k, H, yt, gt):
+    """Through the C interface: dw alone without w, dy alone without y."""
+    import ctypes
+
+    from expert_routed_ffn_amd import _lib
+
+    y, w, dout = (t.cuda() for t in _inputs(T, k, H, yt, gt, seed=T + H))
+    want = moe.combine_backward(y, w, dout)
+    dw, dy = torch.empty_like(w), torch.empty_like(y)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    for a_y, a_w, a_dw, a_dy in [(y.data_ptr(), None, dw.data_ptr(), None), (None, w.data_ptr(), None, dy.data_ptr())]:
+        assert int(_lib.lib.moe_combine_backward(a_y, _lib._dtype_code(y), a_w, dout.data_ptr(), _lib._dtype_code(dout), T, k, H,
+                                                 a_dw, a_dy, stream)) == _lib.MOE_OK
+    torch.cuda.synchronize()
+    assert torch.equal(dw, want[0]) and torch.equal(dy, want[1])
