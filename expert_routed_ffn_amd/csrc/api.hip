@@ -443,21 +443,24 @@ namespace {
 
 constexpr int kLinearMaxT = 1 << 20, kLinearMaxK = 16384, kLinearMaxN = 16384;
 
+bool is_act(moe_act a) {
+  return a == MOE_ACT_NONE || a == MOE_ACT_GELU || a == MOE_ACT_SILU || a == MOE_ACT_SWIGLU;
+}
+bool linear_k(int K) { return K >= 32 && K <= kLinearMaxK && K % 32 == 0; }
+bool linear_n(int N) { return N >= 1 && N <= kLinearMaxN; }
+
 moe_status check_linear(const char* fn, int T, int K, int N, moe_act act) {
   if (T < 0) return fail(MOE_EINVAL, std::string(fn) + ": T < 0");
-  if (act != MOE_ACT_NONE && act != MOE_ACT_GELU && act != MOE_ACT_SILU && act != MOE_ACT_SWIGLU)
-    return fail(MOE_EINVAL, std::string(fn) + ": activation");
+  if (!is_act(act)) return fail(MOE_EINVAL, std::string(fn) + ": activation");
   if (T > kLinearMaxT) return fail(MOE_EUNSUPPORTED, std::string(fn) + fmt(": T=%lld above 2^20", T));
-  if (K < 32 || K > kLinearMaxK || K % 32)
-    return fail(MOE_EUNSUPPORTED, std::string(fn) + fmt(": K=%lld (multiple of 32 in [32, 16384])", K));
-  if (N < 1 || N > kLinearMaxN)
-    return fail(MOE_EUNSUPPORTED, std::string(fn) + fmt(": N=%lld outside [1, 16384]", N));
+  if (!linear_k(K)) return fail(MOE_EUNSUPPORTED, std::string(fn) + fmt(": K=%lld (multiple of 32 in [32, 16384])", K));
+  if (!linear_n(N)) return fail(MOE_EUNSUPPORTED, std::string(fn) + fmt(": N=%lld outside [1, 16384]", N));
   return MOE_OK;
 }
 
-// Sizes that a workspace is asked for: others, which the calls refuse or which have no rows, need none.
-bool sizes_in_range(int T, int K, int N) {
-  return T >= 1 && T <= kLinearMaxT && K >= 1 && K <= kLinearMaxK && N >= 1 && N <= kLinearMaxN;
+// What a workspace is asked for: other calls, which are refused or have no rows, need none.
+bool linear_has_work(int T, int K, int N, moe_act act) {
+  return T >= 1 && T <= kLinearMaxT && linear_k(K) && linear_n(N) && is_act(act);
 }
 bool is_dtype(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16; }
 uintptr_t elem(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }
@@ -467,7 +470,7 @@ uintptr_t elem(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }
 extern "C" {
 
 size_t moe_linear_workspace_bytes(int T, int K, int N, moe_act act, moe_dtype x_t, moe_dtype y_t) {
-  if (!sizes_in_range(T, K, N)) return 0;
+  if (!linear_has_work(T, K, N, act) || !is_dtype(x_t) || !is_dtype(y_t)) return 0;
   return linear_ws_bytes(T, K, N, act, x_t, y_t);
 }
 
@@ -502,7 +505,7 @@ moe_status moe_linear(const void* x, moe_dtype x_t, const void* w, const float* 
 
 size_t moe_linear_backward_workspace_bytes(int T, int K, int N, moe_act act, moe_dtype dy_t, moe_dtype x_t,
                                            moe_dtype dx_t, moe_dtype dw_t, int need) {
-  if (!sizes_in_range(T, K, N)) return 0;
+  if (!linear_has_work(T, K, N, act) || !is_dtype(dy_t) || !is_dtype(x_t) || !is_dtype(dx_t) || !is_dtype(dw_t)) return 0;
   return linear_backward_ws_bytes(T, K, N, act, dy_t, x_t, dx_t, dw_t, need);
 }
 

@@ -452,7 +452,7 @@ typedef enum moe_act {
  *   pre       NULL or [T x R] out, dtype y_t: z, which moe_linear_backward needs
  *             for every activation but MOE_ACT_NONE.
  *   ws        moe_linear_workspace_bytes(T, K, N, act, x_t, y_t) bytes, 256-byte aligned
- *             (the query answers 0 for sizes that the call refuses).
+ *             (the query answers 0 for sizes and types that the call refuses).
  * Sums in fp32.  fp32 x is used to full precision when y is fp32 or T <= 64; a
  * bf16 y of more tokens takes x to within 2^-17 of each value.  T <= 2^20.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE.
@@ -475,7 +475,8 @@ enum { MOE_NEED_DX = 1, MOE_NEED_DW = 2, MOE_NEED_DB = 4 };
  *   dx   NULL or [T x K] out, dtype dx_t.   dw NULL or [R x K] out, dtype dw_t.
  *   db   NULL or [R] fp32 out.  With T == 0, dw and db are set to zero.
  *   ws   moe_linear_backward_workspace_bytes(...) bytes, 256-byte aligned, `need`
- *        the MOE_NEED_* bits of the outputs that are not NULL.
+ *        the MOE_NEED_* bits of the outputs that are not NULL (0 for sizes and
+ *        types that the call refuses).
  * dx and dw must be 16-byte aligned; outputs may not overlap the inputs that are
  * read or each other.  Sums in fp32.  An fp32 dx or dw comes from dz (and x) at
  * full precision; a bf16 one from dz (and fp32 x) to within 2^-17 of each value,

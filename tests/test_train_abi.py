@@ -218,3 +218,20 @@ def test_rows_past_32_bits_are_refused(name, call):
     big = torch.empty(((1 << 32) + 1, 1), device="meta")
     with pytest.raises(ValueError, match=name + r".*2\^31"):
         call(big)
+
+
+@pytest.mark.parametrize("T,K,N", [(100, 16, 64), (100, 33, 64), (100, 48, 64), (65, 4104, 512), (8192, 4112, 4096),
+                                   (8192, 0, 4096), (8192, 4096, 0), (-1, 64, 64), (0, 64, 64)])
+def test_workspaces_of_unsupported_shapes_are_zero(T, K, N):
+    """What the calls refuse (K that is no multiple of 32 among it) or have no rows for needs no workspace."""
+    for act in ("none", "swiglu"):
+        assert m.linear_workspace_bytes(T, K, N, act, torch.float32, torch.float32) == 0
+        assert m.linear_backward_workspace_bytes(T, K, N, act, torch.float32, torch.float32) == 0
+
+
+@pytest.mark.parametrize("act,x_t,y_t", [(4, F32, F32), (-1, F32, F32), (0, 2, F32), (0, F32, 2), (0, -1, F32)])
+def test_workspaces_of_unknown_types_are_zero(act, x_t, y_t):
+    assert int(L.moe_linear_workspace_bytes(8192, 4096, 4096, 0, F32, F32)) > 0
+    assert int(L.moe_linear_workspace_bytes(8192, 4096, 4096, act, x_t, y_t)) == 0
+    for types in [(x_t, y_t, F32, F32), (F32, F32, x_t, y_t)]:
+        assert int(L.moe_linear_backward_workspace_bytes(8192, 4096, 4096, act, *types, 7)) == 0
