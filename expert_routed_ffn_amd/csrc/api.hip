@@ -90,6 +90,21 @@ bool overlap(const void* p, uint64_t n, const void* q, uint64_t m) {
   const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
   return a < b + m && b < a + n;
 }
+struct Span {
+  const void* p;
+  uint64_t n;
+};
+// Whether a buffer that is written shares a byte with one that is read or with another that is written.
+template <size_t O, size_t I>
+bool any_overlap(const Span (&out)[O], const Span (&in)[I]) {
+  for (size_t i = 0; i < O; ++i) {
+    for (const Span& s : in)
+      if (overlap(out[i].p, out[i].n, s.p, s.n)) return true;
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+  }
+  return false;
+}
 
 }  // namespace
 
@@ -376,18 +391,9 @@ moe_status moe_balance_loss(const float* logits, const int32_t* ids, const uint8
     return fail(MOE_EWORKSPACE, fmt("moe_balance_loss: workspace %lld bytes, needs %lld", (long long)ws_bytes,
                                     (long long)need));
   const uint64_t n_t = (uint64_t)T * 4;
-  struct Span {
-    const void* p;
-    uint64_t n;
-  };
-  const Span out[4] = {{loss, 8}, {counts, (uint64_t)E * 4 + 4}, {lse, n_t}, {ws, need}};
-  const Span in[3] = {{logits, n_t * E}, {ids, n_t * k}, {mask, (uint64_t)T}};
-  for (int i = 0; i < 4; ++i) {
-    bool bad = false;
-    for (const Span& s : in) bad = bad || overlap(out[i].p, out[i].n, s.p, s.n);
-    for (int j = 0; j < i; ++j) bad = bad || overlap(out[i].p, out[i].n, out[j].p, out[j].n);
-    if (bad) return fail(MOE_EINVAL, "moe_balance_loss: an output or ws overlaps another buffer");
-  }
+  const Span out[] = {{loss, 8}, {counts, (uint64_t)E * 4 + 4}, {lse, n_t}, {ws, need}};
+  const Span in[] = {{logits, n_t * E}, {ids, n_t * k}, {mask, (uint64_t)T}};
+  if (any_overlap(out, in)) return fail(MOE_EINVAL, "moe_balance_loss: an output or ws overlaps another buffer");
   return launch_balance_loss(logits, ids, mask, T, E, k, loss, counts, lse, ws, stream);
 }
 
@@ -493,12 +499,12 @@ moe_status moe_linear(const void* x, moe_dtype x_t, const void* w, const float* 
   const uint64_t R = act == MOE_ACT_SWIGLU ? 2 * (uint64_t)N : N;
   const uint64_t nx = (uint64_t)T * K * elem(x_t), nw = R * K * 2, ny = (uint64_t)T * N * elem(y_t),
                  np = (uint64_t)T * R * elem(y_t), nr = (uint64_t)T * N * elem(r_t);
+  // y may be the residual itself, which nothing else may touch
   const bool in_place = residual == y && r_t == y_t;
-  const void* const r = in_place ? nullptr : residual;
-  if (overlap(y, ny, x, nx) || overlap(y, ny, w, nw) || overlap(y, ny, bias, R * 4) || overlap(y, ny, r, nr) ||
-      overlap(y, ny, pre, np) || overlap(pre, np, x, nx) || overlap(pre, np, w, nw) || overlap(pre, np, bias, R * 4) ||
-      overlap(pre, np, residual, nr))
-    return fail(MOE_EINVAL, "moe_linear: an output overlaps another buffer (y may only be the residual itself)");
+  const Span out[] = {{y, ny}, {pre, np}, {ws, need}};
+  const Span in[] = {{x, nx}, {w, nw}, {bias, R * 4}, {in_place ? nullptr : residual, nr}};
+  if (any_overlap(out, in))
+    return fail(MOE_EINVAL, "moe_linear: an output or ws overlaps another buffer (y may only be the residual itself)");
   return launch_linear(x, x_t, reinterpret_cast<const uint16_t*>(w), bias, act, residual, r_t, T, K, N, y, y_t, pre, ws,
                        stream);
 }
@@ -528,21 +534,12 @@ moe_status moe_linear_backward(const void* dy, moe_dtype dy_t, const void* pre, 
     return fail(MOE_EWORKSPACE, fmt("moe_linear_backward: workspace %lld bytes, needs %lld", (long long)ws_bytes,
                                     (long long)need));
   const uint64_t R = act == MOE_ACT_SWIGLU ? 2 * (uint64_t)N : N;
-  struct Span {
-    const void* p;
-    uint64_t n;
-  };
-  const Span out[3] = {{dx, (uint64_t)T * K * elem(dx_t)}, {dw, R * K * elem(dw_t)}, {db, R * 4}};
-  const Span in[4] = {{dy, (uint64_t)T * N * elem(dy_t)},
-                      {act == MOE_ACT_NONE ? nullptr : pre, (uint64_t)T * R * elem(dy_t)},
-                      {dw ? x : nullptr, (uint64_t)T * K * elem(x_t)},
-                      {dx ? w : nullptr, R * K * 2}};
-  for (int i = 0; i < 3; ++i) {
-    bool bad = false;
-    for (const Span& s : in) bad = bad || overlap(out[i].p, out[i].n, s.p, s.n);
-    for (int j = 0; j < i; ++j) bad = bad || overlap(out[i].p, out[i].n, out[j].p, out[j].n);
-    if (bad) return fail(MOE_EINVAL, "moe_linear_backward: an output overlaps another buffer");
-  }
+  const Span out[] = {{dx, (uint64_t)T * K * elem(dx_t)}, {dw, R * K * elem(dw_t)}, {db, R * 4}, {ws, need}};
+  const Span in[] = {{dy, (uint64_t)T * N * elem(dy_t)},
+                     {act == MOE_ACT_NONE ? nullptr : pre, (uint64_t)T * R * elem(dy_t)},
+                     {dw ? x : nullptr, (uint64_t)T * K * elem(x_t)},
+                     {dx ? w : nullptr, R * K * 2}};
+  if (any_overlap(out, in)) return fail(MOE_EINVAL, "moe_linear_backward: an output or ws overlaps another buffer");
   return launch_linear_backward(dy, dy_t, pre, x, x_t, reinterpret_cast<const uint16_t*>(w), act, T, K, N, dx, dx_t, dw,
                                 dw_t, db, ws, stream);
 }

@@ -452,7 +452,8 @@ typedef enum moe_act {
  *   pre       NULL or [T x R] out, dtype y_t: z, which moe_linear_backward needs
  *             for every activation but MOE_ACT_NONE.
  *   ws        moe_linear_workspace_bytes(T, K, N, act, x_t, y_t) bytes, 256-byte aligned
- *             (the query answers 0 for sizes and types that the call refuses).
+ *             (the query answers 0 for sizes and types that the call refuses); it may
+ *             not overlap any other buffer.
  * Sums in fp32.  fp32 x is used to full precision when y is fp32 or T <= 64; a
  * bf16 y of more tokens takes x to within 2^-17 of each value.  T <= 2^20.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE.
@@ -477,10 +478,10 @@ enum { MOE_NEED_DX = 1, MOE_NEED_DW = 2, MOE_NEED_DB = 4 };
  *   ws   moe_linear_backward_workspace_bytes(...) bytes, 256-byte aligned, `need`
  *        the MOE_NEED_* bits of the outputs that are not NULL (0 for sizes and
  *        types that the call refuses).
- * dx and dw must be 16-byte aligned; outputs may not overlap the inputs that are
- * read or each other.  Sums in fp32.  An fp32 dx or dw comes from dz (and x) at
- * full precision; a bf16 one from dz (and fp32 x) to within 2^-17 of each value,
- * then rounded once.
+ * dx and dw must be 16-byte aligned; outputs and ws may not overlap the inputs
+ * that are read or each other.  Sums in fp32.  An fp32 dx or dw comes from dz
+ * (and x) at full precision; a bf16 one from dz (and fp32 x) to within 2^-17 of
+ * each value, then rounded once.
  * An infinite or NaN dz or x makes the elements it enters infinite or NaN, where
  * an infinity may become a NaN.
  * Errors: MOE_EINVAL (no output wanted among that), MOE_EUNSUPPORTED, MOE_EWORKSPACE.

@@ -235,3 +235,29 @@ def test_workspaces_of_unknown_types_are_zero(act, x_t, y_t):
     assert int(L.moe_linear_workspace_bytes(8192, 4096, 4096, act, x_t, y_t)) == 0
     for types in [(x_t, y_t, F32, F32), (F32, F32, x_t, y_t)]:
         assert int(L.moe_linear_backward_workspace_bytes(8192, 4096, 4096, act, *types, 7)) == 0
+
+
+def test_dense_workspaces_that_overlap_are_refused():
+    # x, w, bias, residual, y, pre = a .. f, ws = g; places 64 MB apart
+    nb = m.linear_workspace_bytes(500, 2048, 1024, "silu", torch.float32, torch.float32)
+    assert 0 < nb < 32 << 20
+
+    def linear(p):
+        return int(L.moe_linear(p["a"], F32, p["b"], p["c"], 2, p["d"], F32, 500, 2048, 1024, p["e"], F32, p["f"], p["g"], nb,
+                                None))
+
+    # dy, pre, x, w, dx, dw, db = a .. f and h, ws = g
+    nb_back = m.linear_backward_workspace_bytes(333, 544, 201, "gelu", dx_dtype=BF)
+    assert 0 < nb_back < 32 << 20
+
+    def backward(p):
+        return int(L.moe_linear_backward(p["a"], BF16, p["b"], p["c"], BF16, p["d"], 1, 333, 544, 201, p["e"], BF16, p["f"], F32,
+                                         p["h"], p["g"], nb_back, None))
+
+    for call, others in [(linear, "abcdef"), (backward, "abcdefh")]:
+        for other in others:
+            for by in (0, 256):
+                places = {n: _at(64 + 64 * i) for i, n in enumerate("abcdefgh")}
+                places["g"] = ctypes.c_void_p(places[other].value + by)
+                assert call(places) == EINVAL, (call, other)
+                assert b"overlap" in L.moe_last_error(), (call, other)
