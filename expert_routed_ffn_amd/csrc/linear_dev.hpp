@@ -73,8 +73,10 @@ __device__ __forceinline__ float act_value(int act, float z) {
 }
 __device__ __forceinline__ float act_slope(int act, float z) {
   if (act == MOE_ACT_GELU) {
-    const float h = gelu_gate(z);
-    return __builtin_fmaf(z * h * (1.0f - h), kGeluA2 * __builtin_fmaf(3.0f * kGeluB * z, z, 1.0f), h);
+    // From |z| = 32 on h is 0 or 1 and the slope is h; z^2 is kept from growing past fp32's range there, as 0 times an
+    // infinity is NaN (a NaN z stays one through h).
+    const float h = gelu_gate(z), c = __builtin_amdgcn_fmed3f(z, -32.0f, 32.0f);
+    return __builtin_fmaf(c * h * (1.0f - h), kGeluA2 * __builtin_fmaf(3.0f * kGeluB * c, c, 1.0f), h);
   }
   if (act == MOE_ACT_SILU) {
     const float h = sigmoid(z);

@@ -96,3 +96,20 @@ def test_a_token_keeps_its_value_in_a_larger_batch(moe):
     x, w = _whole((200, 256), 2047, 1, F32), _whole((70, 256), 2, 2, BF16)
     few, many = moe.linear(x[:64], w, y_dtype=BF16), moe.linear(x, w, y_dtype=BF16)
     assert torch.equal(few, many[:64])
+
+
+@pytest.mark.parametrize("gt", [F32, BF16])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_slopes_far_out(moe, act, gt):
+    """The activation's slope is 1 far above zero and 0 far below it, up to the type's largest value: dz is dy or zero there,
+    and the products with the unit matrix give it back."""
+    far = torch.tensor([1e3, 1e6, 1e12, 4e19, 6e19, 1e25, 1e37, torch.finfo(gt).max], dtype=torch.float64)
+    pre = torch.cat([far, -far]).repeat(70, 2).to(gt).cuda()
+    dy = _whole((70, 32), 9, 3, gt)
+    eye = torch.eye(32, dtype=BF16, device="cuda")
+    x = _whole((70, 32), 2, 4, BF16)
+    dx, dw, db = moe.linear_backward(dy, x, eye, act=act, pre=pre, dx_dtype=F32)
+    dz = torch.where(pre > 0, dy, torch.zeros_like(dy)).double()
+    assert torch.equal(dx.double(), dz)
+    assert torch.equal(dw.double(), dz.t() @ x.double())
+    assert torch.equal(db.double(), dz.sum(0))
