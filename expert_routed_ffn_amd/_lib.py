@@ -122,6 +122,10 @@ def _load():
     L.moe_linear_backward_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32]
     L.moe_linear_backward.restype = st
     L.moe_linear_backward.argtypes = [vp, i32, vp, vp, i32, vp, i32, i32, i32, i32, vp, i32, vp, i32, vp, vp, sz, vp]
+    L.moe_linear_form.restype = st
+    L.moe_linear_form.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.POINTER(i32)]
+    L.moe_linear_backward_form.restype = st
+    L.moe_linear_backward_form.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32, ctypes.POINTER(i32)]
     L.moe_profile_next_launch.restype = st
     L.moe_profile_next_launch.argtypes = [i32, vp, vp]
     return L
@@ -699,6 +703,24 @@ def linear_backward_workspace_bytes(T: int, K: int, N: int, act: str = "none", d
     code, t = _size_codes(act, dy_dtype, x_dtype, dx_dtype, dw_dtype)
     _needs(need, ("dx", "dw", "db"))
     return int(lib.moe_linear_backward_workspace_bytes(T, K, N, code, *t, sum(_NEED[n] for n in set(need))))
+
+
+def linear_form(T: int, K: int, N: int, act: str = "none", x_dtype=torch.bfloat16, y_dtype=torch.bfloat16) -> dict:
+    """How linear cuts its work at these sizes, for tests and measurements (moe_linear_form)."""
+    code, t = _size_codes(act, x_dtype, y_dtype)
+    form = (ctypes.c_int32 * 4)()
+    _check(lib.moe_linear_form(T, K, N, code, *t, form))
+    return dict(zip(("tile", "parts", "terms", "planes"), form))
+
+
+def linear_backward_form(T: int, K: int, N: int, act: str = "none", dy_dtype=torch.bfloat16, x_dtype=torch.bfloat16,
+                         dx_dtype=torch.bfloat16, dw_dtype=torch.float32, need=("dx", "dw", "db")) -> dict:
+    """How linear_backward cuts its work at these sizes, for tests and measurements (moe_linear_backward_form)."""
+    code, t = _size_codes(act, dy_dtype, x_dtype, dx_dtype, dw_dtype)
+    _needs(need, ("dx", "dw", "db"))
+    form = (ctypes.c_int32 * 4)()
+    _check(lib.moe_linear_backward_form(T, K, N, code, *t, sum(_NEED[n] for n in set(need)), form))
+    return dict(zip(("tile", "dw_parts", "dx_parts", "terms"), form))
 
 
 # ---- slot table -------------------------------------------------------------------------

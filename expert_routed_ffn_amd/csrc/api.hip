@@ -544,6 +544,24 @@ moe_status moe_linear_backward(const void* dy, moe_dtype dy_t, const void* pre, 
                                 dw_t, db, ws, stream);
 }
 
+moe_status moe_linear_form(int T, int K, int N, moe_act act, moe_dtype x_t, moe_dtype y_t, int32_t form[4]) {
+  if (moe_status st = check_linear("moe_linear_form", T, K, N, act)) return st;
+  if (T == 0 || !form) return fail(MOE_EINVAL, "moe_linear_form: no rows, or a null pointer");
+  if (!is_dtype(x_t) || !is_dtype(y_t)) return fail(MOE_EINVAL, "moe_linear_form: dtype");
+  linear_form(T, K, N, act, x_t, y_t, form);
+  return MOE_OK;
+}
+
+moe_status moe_linear_backward_form(int T, int K, int N, moe_act act, moe_dtype dy_t, moe_dtype x_t, moe_dtype dx_t,
+                                    moe_dtype dw_t, int need, int32_t form[4]) {
+  if (moe_status st = check_linear("moe_linear_backward_form", T, K, N, act)) return st;
+  if (T == 0 || !form) return fail(MOE_EINVAL, "moe_linear_backward_form: no rows, or a null pointer");
+  if (!is_dtype(dy_t) || !is_dtype(x_t) || !is_dtype(dx_t) || !is_dtype(dw_t))
+    return fail(MOE_EINVAL, "moe_linear_backward_form: dtype");
+  linear_backward_form(T, K, N, act, dy_t, x_t, dx_t, dw_t, need, form);
+  return MOE_OK;
+}
+
 moe_status moe_profile_next_launch(moe_kernel kernel, hipEvent_t start, hipEvent_t stop) {
   if ((int)kernel < 0 || (int)kernel > (int)MOE_KERNEL_LINEAR_BACKWARD) return fail(MOE_EINVAL, "moe_profile_next_launch: kernel");
   if (!start || !stop) return fail(MOE_EINVAL, "moe_profile_next_launch: null event");

@@ -166,8 +166,11 @@ size_t linear_ws_bytes(int T, int K, int N, int act, moe_dtype x_t, moe_dtype y_
 moe_status launch_linear(const void* x, moe_dtype x_t, const uint16_t* w, const float* bias, int act,
                          const void* residual, moe_dtype r_t, int T, int K, int N, void* y, moe_dtype y_t, void* pre,
                          void* ws, hipStream_t s);
+void linear_form(int T, int K, int N, int act, moe_dtype x_t, moe_dtype y_t, int32_t form[4]);
 size_t linear_backward_ws_bytes(int T, int K, int N, int act, moe_dtype dy_t, moe_dtype x_t, moe_dtype dx_t,
                                 moe_dtype dw_t, int need);
+void linear_backward_form(int T, int K, int N, int act, moe_dtype dy_t, moe_dtype x_t, moe_dtype dx_t, moe_dtype dw_t,
+                          int need, int32_t form[4]);
 moe_status launch_linear_backward(const void* dy, moe_dtype dy_t, const void* pre, const void* x, moe_dtype x_t,
                                   const uint16_t* w, int act, int T, int K, int N, void* dx, moe_dtype dx_t, void* dw,
                                   moe_dtype dw_t, float* db, void* ws, hipStream_t s);

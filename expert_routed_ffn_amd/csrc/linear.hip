@@ -207,6 +207,14 @@ size_t linear_ws_bytes(int T, int K, int N, int act, moe_dtype x_t, moe_dtype y_
   return linear_plan(T, K, N, act, x_t, y_t).bytes;
 }
 
+void linear_form(int T, int K, int N, int act, moe_dtype x_t, moe_dtype y_t, int32_t form[4]) {
+  const LinearPlan p = linear_plan(T, K, N, act, x_t, y_t);
+  form[0] = p.few ? 0 : tile_side(p.plan);
+  form[1] = p.few ? 1 : p.plan.split[0];
+  form[2] = !p.few ? p.terms : x_t == MOE_F32 ? 3 : 1;
+  form[3] = p.split_first ? (int)ceil_div(T, p.rows) : 0;
+}
+
 moe_status launch_linear(const void* x, moe_dtype x_t, const uint16_t* w, const float* bias, int act,
                          const void* residual, moe_dtype r_t, int T, int K, int N, void* y, moe_dtype y_t, void* pre,
                          void* ws, hipStream_t s) {

@@ -271,6 +271,7 @@ struct Plan {
   int split[2];
 };
 Plan plan_products(const Shape* s, int count);
+int tile_side(const Plan& plan);
 // Launches a forward product (`grad` false, count = 1) or the gradient's (dW first where both are there) with db's sum,
 // then what joins the products' parts.
 moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool grad, bool first_is_dw, const DbSum& db,

@@ -265,6 +265,15 @@ size_t linear_backward_ws_bytes(int T, int K, int N, int act, moe_dtype dy_t, mo
   return grad_plan(T, K, N, act, dy_t, x_t, dx_t, dw_t, need).bytes;
 }
 
+void linear_backward_form(int T, int K, int N, int act, moe_dtype dy_t, moe_dtype x_t, moe_dtype dx_t, moe_dtype dw_t,
+                          int need, int32_t form[4]) {
+  const GradPlan p = grad_plan(T, K, N, act, dy_t, x_t, dx_t, dw_t, need);
+  form[0] = p.dx || p.dw ? tile_side(p.plan) : 0;
+  form[1] = p.dw ? p.split_dw : 0;
+  form[2] = p.dx ? p.split_dx : 0;
+  form[3] = p.terms;
+}
+
 moe_status launch_linear_backward(const void* dy, moe_dtype dy_t, const void* pre, const void* x, moe_dtype x_t,
                                   const uint16_t* w, int act, int T, int K, int N, void* dx, moe_dtype dx_t, void* dw,
                                   moe_dtype dw_t, float* db, void* ws, hipStream_t s) {

@@ -642,9 +642,11 @@ Plan plan_products(const Shape* s, int count) {
   return best;
 }
 
+int tile_side(const Plan& plan) { return plan.shape == kDirect ? Direct::TM : kRates[plan.shape].side; }
+
 moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool grad, bool first_is_dw, const DbSum& db,
                            hipStream_t s, const char* what) {
-  const int side = plan.shape == kDirect ? Direct::TM : kRates[plan.shape].side;
+  const int side = tile_side(plan);
   const int64_t db_blocks = db.db ? ceil_div(db.n, 64) : 0;
   int64_t blocks[2] = {0, 0};
   Join j{};

@@ -493,6 +493,22 @@ moe_status moe_linear_backward(const void* dy, moe_dtype dy_t, const void* pre, 
                                moe_dtype dw_t, float* db, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /*
+ * How a dense call cuts its work, for tests and measurement tools: the answer
+ * follows measured rates and may change from one version to the next.  Errors
+ * as the calls' own for these sizes and types; nothing is enqueued.
+ *   moe_linear_form           form[0] side of the square tiles (0: no tiles, up
+ *                             to 64 tokens); form[1] parts of the reduction;
+ *                             form[2] bf16 terms of x; form[3] launches that take
+ *                             them from planes (0: x is read as it is).
+ *   moe_linear_backward_form  form[0] side (0: no product); form[1], form[2]
+ *                             parts of dw's and of dx's reduction (0: not
+ *                             wanted); form[3] bf16 terms of dz.
+ */
+moe_status moe_linear_form(int T, int K, int N, moe_act act, moe_dtype x_t, moe_dtype y_t, int32_t form[4]);
+moe_status moe_linear_backward_form(int T, int K, int N, moe_act act, moe_dtype dy_t, moe_dtype x_t, moe_dtype dx_t,
+                                    moe_dtype dw_t, int need, int32_t form[4]);
+
+/*
  * Kernel timing hook (for measurement tools; not part of the layer).  The
  * next launch of `kernel` issued by this host thread is made with
  * hipExtLaunchKernel so that `start` and `stop` (created by the caller with

@@ -261,3 +261,21 @@ def test_dense_workspaces_that_overlap_are_refused():
                 places["g"] = ctypes.c_void_p(places[other].value + by)
                 assert call(places) == EINVAL, (call, other)
                 assert b"overlap" in L.moe_last_error(), (call, other)
+
+
+def test_forms():
+    for T, K, N in [(0, 64, 64), (-1, 64, 64), (100, 48, 64), (100, 64, 0)]:
+        with pytest.raises(m.MoeError):
+            m.linear_form(T, K, N)
+        with pytest.raises(m.MoeError):
+            m.linear_backward_form(T, K, N)
+    form = (ctypes.c_int32 * 4)()
+    assert int(L.moe_linear_form(100, 64, 64, 0, F32, 2, form)) == EINVAL
+    assert int(L.moe_linear_form(100, 64, 64, 0, F32, F32, None)) == EINVAL
+    assert int(L.moe_linear_backward_form(100, 64, 64, 0, F32, F32, 5, F32, 7, form)) == EINVAL
+    assert int(L.moe_linear_backward_form(100, 64, 64, 4, F32, F32, F32, F32, 7, form)) == EINVAL
+    assert m.linear_form(64, 64, 64) == {"tile": 0, "parts": 1, "terms": 1, "planes": 0}
+    assert m.linear_form(64, 64, 64, x_dtype=torch.float32)["terms"] == 3
+    assert m.linear_backward_form(100, 64, 64, need=("db",)) == {"tile": 0, "dw_parts": 0, "dx_parts": 0, "terms": 1}
+    only = m.linear_backward_form(100, 64, 64, dy_dtype=torch.float32, need=("dx",))
+    assert only["dw_parts"] == 0 and only["dx_parts"] >= 1 and only["terms"] == 2
