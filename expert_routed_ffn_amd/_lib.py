@@ -437,6 +437,9 @@ def decode_workspace_bytes(layer: ExpertLayer, T: int, k: int) -> int:
 
 
 # ---- training the router and the dense parts beside the experts ------------------------
+#
+# There is no autograd here: what these calls return is detached, whatever their inputs require, and each has its gradient
+# as a call of its own.
 
 _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
 
@@ -507,7 +510,8 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, mask: torch.Tensor | N
                  lse: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
     """moe_balance_loss: (loss [2] fp32, counts [E + 1] int32, lse [T] fp32) of logits [T, E] fp32 routed to ids
     [T, k]; loss[0] is the balance loss, loss[1] the mean squared log-sum-exp, counts[E] the number of tokens that
-    take part.  mask [T] (bool or uint8) leaves padding out."""
+    take part.  mask [T] (bool or uint8) leaves padding out.  The losses are detached; their gradient is
+    route_backward."""
     T, E = _rows(logits, "logits", 2)
     k = _rows(ids, "ids", 2)[1]
     a_logits = _arg(logits, "logits", (T, E), (_F32,))
@@ -610,7 +614,8 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, a
 
     w is bf16, x and residual fp32 or bf16, bias fp32, y of y_dtype (x's by default).  act is "none", "gelu" (tanh
     form), "silu" or "swiglu", whose w holds N gate rows, then N up rows (R = 2 N; else R = N).  `pre` [T, R], of y's
-    type, receives the values before the activation, which linear_backward needs.  y may be the residual itself."""
+    type, receives the values before the activation, which linear_backward needs.  y may be the residual itself.
+    y is detached; its gradient is linear_backward."""
     T, K = _rows(x, "x", 2)
     R = _rows(w, "w", 2)[0]
     code, N = _act_rows(w, act)

@@ -22,9 +22,9 @@
 namespace moe {
 namespace {
 
-// Of dy per workgroup: 32 threads of 8 columns by 8 rows at a time, up to 64 rows; fewer where that leaves less than
-// 512 workgroups (8,192 x 512 SwiGLU: 11.5 us with 32
-// rows, half as long again with 64; 333 x 201: 5.1 us with 8, five times that with 64).
+// Of dy per workgroup: 32 threads of 8 columns by 8 rows at a time, up to 64 rows; fewer where that leaves less than 512
+// workgroups (8,192 x 512 SwiGLU in one plane: 11.5 us with 32 rows, half as long again with 64, 14.6 in the two planes of
+// a bf16 result; 333 x 201: 5.1 us with 8, five times that with 64).
 constexpr int kPrepCols = 256;
 int prep_rows(int T, int N) {
   int rows = 64;
@@ -97,8 +97,9 @@ __device__ __forceinline__ void write8(uint16_t* dst, int64_t plane, int terms, 
 // What dz is made of: dy alone, dy and one pre-activation, or dy and a SwiGLU pair.
 enum PrepKind { kPlain, kSlope, kPair };
 
-// One row's 8 columns from n on; of rows shorter than that (not FULL) the `left` that are there.  Everything that decides which loads there are is known to the compiler, so that a
-// thread's loads are issued together (decided at run time, each was waited for before the next).
+// One row's 8 columns from n on; of rows shorter than that (not FULL) the `left` that are there.  Everything that decides
+// which loads there are is known to the compiler, so that a thread's loads are issued together (decided at run time, each
+// was waited for before the next).
 template <int KIND, bool BF16, bool FULL>
 __device__ __forceinline__ void prep_row(const Prep& p, int t, int n, int left, float (&sa)[8], float (&su)[8]) {
   float g[8], z[8], zu[8], a[8], u[8];

@@ -370,6 +370,11 @@ void moe_slot_table_destroy(moe_slot_table* t);
  * moe_route_topk, the experts, moe_combine and moe_balance_loss, then
  * moe_combine_backward (the gate weights' gradient), moe_route_backward (the
  * logits') and moe_linear_backward (the router's and the dense weights').
+ * The gradient through the quantised experts to their input is not here: the
+ * layer's input gets the router's and the dense parts' share of its gradient
+ * only, so parameters below one such layer cannot be trained through it with
+ * these calls alone.  A caller with a gradient of its own for the experts
+ * starts it from moe_combine_backward's dy.
  * Each call gives the same bits for the same inputs every time.
  */
 
