@@ -157,3 +157,23 @@ def test_backward_holds_all_of_fp32(moe, T, K, N, types, tile, dw_cut, dx_cut):
         dy, t_of, sign = _ones(T, N, g, F32)
         _, dw, _ = moe.linear_backward(dy, x, w, need=("dw",), dw_dtype=dwt)
         assert torch.equal(dw, x[t_of] * sign[:, None])
+
+
+def test_largest_rows_and_columns(moe):
+    """K and N at their largest, SwiGLU's 32,768 rows of w among them: no row, column or piece is left out or taken twice."""
+    K = N = 16384
+    g = _gen(5)
+    for T in (64, 66):
+        x = torch.randn((T, K), generator=g, device="cuda")
+        wt, at, sign = _ones(K, 2 * N, g, BF16)
+        pre = torch.empty((T, 2 * N), device="cuda")
+        moe.linear(x, wt.t().contiguous(), act="swiglu", pre=pre)
+        assert torch.equal(pre, x[:, at] * sign)
+        dy = torch.randn((T, N), generator=g, device="cuda")
+        w, r_of, w_sign = _ones(N, K, g, BF16)
+        ones, t_of, x_sign = _ones(T, K, g, F32)
+        dx, dw, db = moe.linear_backward(dy, ones, w, dx_dtype=F32)
+        assert torch.equal(dx, dy[:, r_of] * w_sign)
+        assert torch.equal(dw, dy[t_of].t() * x_sign)
+        bound = (T + 8) * U * dy.double().abs().sum(0)
+        within(db, dy.double().sum(0), bound.cpu(), "db")
