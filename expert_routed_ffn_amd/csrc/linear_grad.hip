@@ -110,7 +110,7 @@ __device__ __forceinline__ void prep_row(const Prep& p, int t, int n, int left, 
   for (int j = 0; j < 8; ++j) {
     if constexpr (KIND == kPair) {
       const float h = sigmoid(z[j]);
-      a[j] = g[j] * zu[j] * (h * __builtin_fmaf(z[j], 1.0f - h, 1.0f));
+      a[j] = g[j] * (zu[j] * (h * __builtin_fmaf(z[j], 1.0f - h, 1.0f)));  // (dy times up may pass fp32's range)
       u[j] = g[j] * (z[j] * h);
     } else if constexpr (KIND == kSlope) {
       a[j] = g[j] * act_slope(p.act, z[j]);

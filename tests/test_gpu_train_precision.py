@@ -113,3 +113,13 @@ def test_slopes_far_out(moe, act, gt):
     assert torch.equal(dx.double(), dz)
     assert torch.equal(dw.double(), dz.t() @ x.double())
     assert torch.equal(db.double(), dz.sum(0))
+
+
+def test_swiglu_slope_of_a_closed_gate_is_zero(moe):
+    """Where the gate's slope is 0 its dz is 0, however large dy times the up value (here past fp32's range)."""
+    T, N = 70, 32
+    pre = torch.cat([torch.full((T, N), -300.0), torch.full((T, N), 1e30)], 1).cuda()
+    dy = torch.full((T, N), 1e30, device="cuda")
+    x, w = _whole((T, 64), 2, 1, BF16), _whole((2 * N, 64), 2, 2, BF16)
+    dx, dw, db = moe.linear_backward(dy, x, w, act="swiglu", pre=pre, dx_dtype=F32)
+    assert not dx.any() and not dw.any() and not db.any()
