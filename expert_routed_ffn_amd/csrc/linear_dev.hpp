@@ -234,7 +234,7 @@ __device__ __forceinline__ void epi_rows(const Epi& e, int m, int n, int rows, V
 // One product C[m][n] = sum over segments and k of A(m, k) B(n, k); which operand lies [index][k] and which [k][index]
 // is the kernel's.  A segment names one term plane of each operand (see bf16_terms): planes are `a_plane` / `b_plane`
 // elements apart.
-struct Prob {
+struct Mats {
   const uint16_t *A, *B;
   int64_t a_plane, b_plane;
   int lda, ldb;            // elements per stored row, multiples of 8
@@ -242,6 +242,8 @@ struct Prob {
   int nseg;                // of a plan of kDirect 1
   int terms;               // kDirect: A is fp32 and enters as so many bf16 terms
   uint32_t sa, sb;         // two bits per segment: its plane of A and of B
+};
+struct Prob : Mats {
   int split;               // parts of the reduction, each a workgroup
   float* partial;          // [split][M][ldp] when split > 1
   int ldp;                 // elements per row of a part
