@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(_PKG, "libmoe.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "moe.h")
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP, MOE_ENOTPINNED, MOE_ECAPACITY = range(7)
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_I8 = 0, 1, 2
 PATHS = {"auto": 0, "gemv": 1, "mfma": 2}
 
 
@@ -126,6 +126,14 @@ def _load():
     L.moe_linear_form.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.POINTER(i32)]
     L.moe_linear_backward_form.restype = st
     L.moe_linear_backward_form.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32, ctypes.POINTER(i32)]
+    L.moe_quantize_rows.restype = st
+    L.moe_quantize_rows.argtypes = [vp, i32, i32, i32, vp, vp, vp]
+    L.moe_linear_q8_workspace_bytes.restype = sz
+    L.moe_linear_q8_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    L.moe_linear_q8.restype = st
+    L.moe_linear_q8.argtypes = [vp, i32, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, vp, i32, vp, sz, vp]
+    L.moe_linear_q8_form.restype = st
+    L.moe_linear_q8_form.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(i32)]
     L.moe_profile_next_launch.restype = st
     L.moe_profile_next_launch.argtypes = [i32, vp, vp]
     return L
@@ -186,7 +194,7 @@ def _need(t: torch.Tensor, name: str):
 
 KERNELS = {"route": 0, "dispatch": 1, "gemv_gateup": 2, "gemv_down": 3, "mfma_gateup": 4, "mfma_down": 5,
            "combine": 6, "decode_prep": 7, "router": 8, "balance": 9, "route_backward": 10, "combine_backward": 11,
-           "linear": 12, "linear_backward": 13}
+           "linear": 12, "linear_backward": 13, "quantize": 14, "linear_q8": 15}
 ACTS = {"none": 0, "gelu": 1, "silu": 2, "swiglu": 3}
 
 
@@ -726,6 +734,81 @@ def linear_backward_form(T: int, K: int, N: int, act: str = "none", dy_dtype=tor
     form = (ctypes.c_int32 * 4)()
     _check(lib.moe_linear_backward_form(T, K, N, code, *t, sum(_NEED[n] for n in set(need)), form))
     return dict(zip(("tile", "dw_parts", "dx_parts", "terms"), form))
+
+
+# ---- the dense parts in 8 bits ----------------------------------------------------------
+
+_I8 = torch.int8
+
+
+def quantize_rows(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
+    """moe_quantize_rows: (q [T, K] int8, scale [T] fp32) of x [T, K] (fp32 or bf16): x is about q * scale[:, None], with
+    scale a 127th of the row's largest magnitude.  Rows are a weight's output channels or tokens."""
+    T, K = _rows(x, "x", 2)
+    a_x = _arg(x, "x", (T, K), (_F32, _BF16))
+    at = x.get_device()
+    if q is None:
+        q = _new(x, (T, K), _I8, stream)
+    if scale is None:
+        scale = _new(x, T, _F32, stream)
+    _launch(lib.moe_quantize_rows, at, stream, a_x, _dtype_code(x), T, K, _arg(q, "q", (T, K), (_I8,), at),
+            _arg(scale, "scale", (T,), (_F32,), at))
+    return q, scale
+
+
+_Q8_CODE = {_F32: MOE_F32, _BF16: MOE_BF16, _I8: MOE_I8}
+
+
+def linear_q8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, x_scale: torch.Tensor | None = None,
+              bias: torch.Tensor | None = None, act: str = "none", residual: torch.Tensor | None = None,
+              y: torch.Tensor | None = None, y_dtype=None, ws: torch.Tensor | None = None, stream=None):
+    """moe_linear_q8: y [T, N] = act((x [T, K] . w [R, K]^T) * scales + bias [R]) + residual [T, N] in 8-bit integers.
+
+    w int8 and w_scale [R] fp32 come from quantize_rows.  x is int8 with x_scale [T] fp32 (quantize_rows of the
+    activations), or fp32 or bf16, which the call codes the same way.  bias is fp32, residual fp32 or bf16, y of y_dtype
+    (x's by default, bf16 for int8 x).  act as for linear: "swiglu" takes N gate rows, then N up rows.  y may be the
+    residual itself."""
+    T, K = _rows(x, "x", 2)
+    R = _rows(w, "w", 2)[0]
+    code, N = _act_rows(w, act)
+    a_x = _arg(x, "x", (T, K), (_F32, _BF16, _I8))
+    at = x.get_device()
+    x_t = _Q8_CODE[x.dtype]
+    if (x_scale is None) != (x_t != MOE_I8):
+        raise ValueError("x_scale goes with int8 x")
+    a_xs = None if x_scale is None else _arg(x_scale, "x_scale", (T,), (_F32,), at)
+    a_w, a_ws_ = _arg(w, "w", (R, K), (_I8,), at), _arg(w_scale, "w_scale", (R,), (_F32,), at)
+    a_bias = None if bias is None else _arg(bias, "bias", (R,), (_F32,), at)
+    a_res, r_t = None, MOE_F32
+    if residual is not None:
+        a_res, r_t = _arg(residual, "residual", (T, N), (_F32, _BF16), at), _dtype_code(residual)
+    if y is None:
+        y = _new(x, (T, N), y_dtype or (_BF16 if x_t == MOE_I8 else x.dtype), stream)
+    a_y, y_t = _arg(y, "y", (T, N), (_F32, _BF16), at), _dtype_code(y)
+    ws, a_ws, n_ws = _ws(ws, lib.moe_linear_q8_workspace_bytes(T, K, N, code, x_t), x, at, stream)
+    _launch(lib.moe_linear_q8, at, stream, a_x, x_t, a_xs, a_w, a_ws_, a_bias, code, a_res, r_t, T, K, N, a_y, y_t, a_ws,
+            n_ws)
+    return y
+
+
+def _q8_codes(act: str, x_dtype):
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, got {act!r}")
+    if x_dtype not in _Q8_CODE:
+        raise TypeError(f"unsupported dtype {x_dtype} (float32, bfloat16 or int8)")
+    return ACTS[act], _Q8_CODE[x_dtype]
+
+
+def linear_q8_workspace_bytes(T: int, K: int, N: int, act: str = "none", x_dtype=torch.bfloat16) -> int:
+    """Bytes of linear_q8's workspace for N output columns."""
+    return int(lib.moe_linear_q8_workspace_bytes(T, K, N, *_q8_codes(act, x_dtype)))
+
+
+def linear_q8_form(T: int, K: int, N: int, act: str = "none", x_dtype=torch.bfloat16) -> dict:
+    """How linear_q8 cuts its work at these sizes, for tests and measurements (moe_linear_q8_form)."""
+    form = (ctypes.c_int32 * 3)()
+    _check(lib.moe_linear_q8_form(T, K, N, *_q8_codes(act, x_dtype), form))
+    return dict(zip(("tile", "parts", "coded_before"), form))
 
 
 # ---- slot table -------------------------------------------------------------------------

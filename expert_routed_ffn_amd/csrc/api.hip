@@ -562,8 +562,66 @@ moe_status moe_linear_backward_form(int T, int K, int N, moe_act act, moe_dtype 
   return MOE_OK;
 }
 
+moe_status moe_quantize_rows(const void* x, moe_dtype x_t, int T, int K, int8_t* q, float* scale, hipStream_t stream) {
+  if (T < 0) return fail(MOE_EINVAL, "moe_quantize_rows: T < 0");
+  if (T > kLinearMaxT) return fail(MOE_EUNSUPPORTED, fmt("moe_quantize_rows: T=%lld above 2^20", T));
+  if (!linear_k(K)) return fail(MOE_EUNSUPPORTED, fmt("moe_quantize_rows: K=%lld (multiple of 32 in [32, 16384])", K));
+  if (!is_dtype(x_t)) return fail(MOE_EINVAL, "moe_quantize_rows: x dtype");
+  if (T == 0) return MOE_OK;
+  if (!x || !q || !scale) return fail(MOE_EINVAL, "moe_quantize_rows: null pointer");
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4))
+    return fail(MOE_EINVAL, "moe_quantize_rows: misaligned buffer (x and q need 16 bytes)");
+  const uint64_t n = (uint64_t)T * K;
+  const Span out[] = {{q, n}, {scale, (uint64_t)T * 4}};
+  const Span in[] = {{x, n * elem(x_t)}};
+  if (any_overlap(out, in)) return fail(MOE_EINVAL, "moe_quantize_rows: an output overlaps another buffer");
+  return launch_quantize_rows(x, x_t, T, K, q, scale, stream);
+}
+
+size_t moe_linear_q8_workspace_bytes(int T, int K, int N, moe_act act, moe_dtype x_t) {
+  if (!linear_has_work(T, K, N, act) || !(is_dtype(x_t) || x_t == MOE_I8)) return 0;
+  return linear_q8_ws_bytes(T, K, N, act, x_t);
+}
+
+moe_status moe_linear_q8(const void* x, moe_dtype x_t, const float* x_scale, const int8_t* w, const float* w_scale,
+                         const float* bias, moe_act act, const void* residual, moe_dtype r_t, int T, int K, int N,
+                         void* y, moe_dtype y_t, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (moe_status st = check_linear("moe_linear_q8", T, K, N, act)) return st;
+  if (!is_dtype(x_t) && x_t != MOE_I8) return fail(MOE_EINVAL, "moe_linear_q8: x dtype");
+  if (!is_dtype(y_t)) return fail(MOE_EINVAL, "moe_linear_q8: y dtype");
+  if (residual && !is_dtype(r_t)) return fail(MOE_EINVAL, "moe_linear_q8: residual dtype");
+  if (x_t != MOE_I8 && x_scale) return fail(MOE_EINVAL, "moe_linear_q8: x_scale goes with 8-bit x");
+  if (T == 0) return MOE_OK;
+  if (!x || !w || !w_scale || !y || (x_t == MOE_I8 && !x_scale)) return fail(MOE_EINVAL, "moe_linear_q8: null pointer");
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(ws, 256) || !aligned(x_scale, 4) || !aligned(w_scale, 4) ||
+      !aligned(bias, 4) || !aligned(y, elem(y_t)) || (residual && !aligned(residual, elem(r_t))))
+    return fail(MOE_EINVAL, "moe_linear_q8: misaligned buffer (x and w need 16 bytes, ws 256)");
+  const size_t need = linear_q8_ws_bytes(T, K, N, act, x_t);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(MOE_EWORKSPACE, fmt("moe_linear_q8: workspace %lld bytes, needs %lld", (long long)ws_bytes,
+                                    (long long)need));
+  const uint64_t R = act == MOE_ACT_SWIGLU ? 2 * (uint64_t)N : N;
+  // y may be the residual itself, which nothing else may touch
+  const bool in_place = residual == y && r_t == y_t;
+  const Span out[] = {{y, (uint64_t)T * N * elem(y_t)}, {ws, need}};
+  const Span in[] = {{x, (uint64_t)T * K * (x_t == MOE_I8 ? 1 : elem(x_t))}, {x_scale, (uint64_t)T * 4}, {w, R * K},
+                     {w_scale, R * 4}, {bias, R * 4},
+                     {in_place ? nullptr : residual, residual ? (uint64_t)T * N * elem(r_t) : 0}};
+  if (any_overlap(out, in))
+    return fail(MOE_EINVAL, "moe_linear_q8: an output or ws overlaps another buffer (y may only be the residual itself)");
+  return launch_linear_q8(x, x_t, x_scale, w, w_scale, bias, act, residual, r_t, T, K, N, y, y_t, ws, stream);
+}
+
+moe_status moe_linear_q8_form(int T, int K, int N, moe_act act, moe_dtype x_t, int32_t form[3]) {
+  if (moe_status st = check_linear("moe_linear_q8_form", T, K, N, act)) return st;
+  if (T == 0 || !form) return fail(MOE_EINVAL, "moe_linear_q8_form: no rows, or a null pointer");
+  if (!is_dtype(x_t) && x_t != MOE_I8) return fail(MOE_EINVAL, "moe_linear_q8_form: dtype");
+  linear_q8_form(T, K, N, act, x_t, form);
+  return MOE_OK;
+}
+
 moe_status moe_profile_next_launch(moe_kernel kernel, hipEvent_t start, hipEvent_t stop) {
-  if ((int)kernel < 0 || (int)kernel > (int)MOE_KERNEL_LINEAR_BACKWARD) return fail(MOE_EINVAL, "moe_profile_next_launch: kernel");
+  if ((int)kernel < 0 || (int)kernel > (int)MOE_KERNEL_LINEAR_Q8) return fail(MOE_EINVAL, "moe_profile_next_launch: kernel");
   if (!start || !stop) return fail(MOE_EINVAL, "moe_profile_next_launch: null event");
   ProfileReq& p = profile_req();
   p.kernel = (int)kernel;

@@ -175,6 +175,15 @@ moe_status launch_linear_backward(const void* dy, moe_dtype dy_t, const void* pr
                                   const uint16_t* w, int act, int T, int K, int N, void* dx, moe_dtype dx_t, void* dw,
                                   moe_dtype dw_t, float* db, void* ws, hipStream_t s);
 
+// ---- the dense parts in 8 bits --------------------------------------------------------------
+
+moe_status launch_quantize_rows(const void* x, moe_dtype x_t, int T, int K, int8_t* q, float* scale, hipStream_t s);
+size_t linear_q8_ws_bytes(int T, int K, int N, int act, moe_dtype x_t);
+void linear_q8_form(int T, int K, int N, int act, moe_dtype x_t, int32_t form[3]);
+moe_status launch_linear_q8(const void* x, moe_dtype x_t, const float* x_scale, const int8_t* w, const float* w_scale,
+                            const float* bias, int act, const void* residual, moe_dtype r_t, int T, int K, int N, void* y,
+                            moe_dtype y_t, void* ws, hipStream_t s);
+
 moe_status launch_fill_i32(int32_t* p, int64_t n, int32_t v, hipStream_t s);
 
 // Pending timing request of moe_profile_next_launch (per host thread).

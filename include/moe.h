@@ -76,7 +76,11 @@ typedef enum moe_status {
   MOE_ECAPACITY = 6     /* the slot table cannot hold the active set */
 } moe_status;
 
-typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
+typedef enum moe_dtype {
+  MOE_F32 = 0,
+  MOE_BF16 = 1,
+  MOE_I8 = 2 /* 8-bit codes of moe_quantize_rows; only where a call says so */
+} moe_dtype;
 
 /* Which expert-FFN kernels to run.  AUTO picks GEMV for T * k <= 128 routed rows
  * and MFMA above (the measured crossover on the 512-expert, top-10 decode layer);
@@ -514,6 +518,54 @@ moe_status moe_linear_backward_form(int T, int K, int N, moe_act act, moe_dtype 
                                     moe_dtype dw_t, int need, int32_t form[4]);
 
 /*
+ * Serving the dense parts in 8 bits.
+ *
+ * moe_quantize_rows gives a matrix one scale per row: rows are output channels when the matrix is a weight, tokens when
+ * it is activations.  moe_linear_q8 is moe_linear on such weights.
+ */
+
+/*
+ * moe_quantize_rows -- rows to 8-bit codes with a scale each: x[t][c] is about q[t][c] * scale[t].
+ * scale[t] = max(amax / 127, 2^-126) in fp32, amax the largest magnitude of row t;
+ * q[t][c] = x[t][c] / scale[t] rounded to the nearest integer, ties to even (the real quotient: no
+ * rounding before), which lies in [-127, 127].
+ * A row that holds an infinity or a NaN gets scale NaN and codes 0.
+ *   x      [T x K], dtype x_t (MOE_F32 or MOE_BF16), 16-byte aligned; K % 32 == 0, 32 <= K <= 16384; T <= 2^20.
+ *   q      [T x K] int8 out, 16-byte aligned.   scale [T] fp32 out.
+ * Outputs may not overlap x or each other.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED.
+ */
+moe_status moe_quantize_rows(const void* x, moe_dtype x_t, int T, int K, int8_t* q, float* scale, hipStream_t stream);
+
+/*
+ * moe_linear_q8 -- dense product of 8-bit integers with bias, activation and residual.
+ * z[t][r] = (sum_c qx[t][c] * w[r][c]) * sx[t] * w_scale[r] + bias[r];  y[t][n] = act(z[t])[n] + residual[t][n].
+ *   x         [T x K], 16-byte aligned; K % 32 == 0, 32 <= K <= 16384.
+ *             MOE_I8: qx is x and sx is x_scale.  MOE_F32, MOE_BF16: qx and sx are what moe_quantize_rows
+ *             makes of x, so that a token's row gives the same result in every batch.
+ *   x_scale   [T] fp32 with MOE_I8, else NULL.
+ *   w         [R x K] int8, 16-byte aligned; R = 2 N for SwiGLU (gate rows first), else N; 1 <= N <= 16384.
+ *   w_scale   [R] fp32.
+ *   bias      NULL or [R] fp32.     residual  NULL or [T x N], dtype r_t.
+ *   y         [T x N] out, dtype y_t; may not overlap the inputs, except that y
+ *             may be the residual itself when r_t == y_t.
+ *   ws        moe_linear_q8_workspace_bytes(T, K, N, act, x_t) bytes, 256-byte aligned
+ *             (the query answers 0 for sizes and types that the call refuses); it may
+ *             not overlap any other buffer.
+ * The integer sums are exact; scales, bias, activation and residual are fp32.  A row of x with an
+ * infinity or a NaN, and a NaN scale, give NaN (before the residual).  T <= 2^20.  Scales below 2^-126 may be taken as 0.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE.
+ */
+size_t moe_linear_q8_workspace_bytes(int T, int K, int N, moe_act act, moe_dtype x_t);
+moe_status moe_linear_q8(const void* x, moe_dtype x_t, const float* x_scale, const int8_t* w, const float* w_scale,
+                         const float* bias, moe_act act, const void* residual, moe_dtype r_t, int T, int K, int N,
+                         void* y, moe_dtype y_t, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* How moe_linear_q8 cuts its work, as moe_linear_form: form[0] side of the square tiles (0: no tiles), form[1] parts
+ * of the reduction, form[2] 1 where a launch of its own codes the activations. */
+moe_status moe_linear_q8_form(int T, int K, int N, moe_act act, moe_dtype x_t, int32_t form[3]);
+
+/*
  * Kernel timing hook (for measurement tools; not part of the layer).  The
  * next launch of `kernel` issued by this host thread is made with
  * hipExtLaunchKernel so that `start` and `stop` (created by the caller with
@@ -534,7 +586,9 @@ typedef enum moe_kernel {
   MOE_KERNEL_ROUTE_BACKWARD = 10,   /* gradient of the logits */
   MOE_KERNEL_COMBINE_BACKWARD = 11,
   MOE_KERNEL_LINEAR = 12,           /* dense product (few tokens, or tiled) */
-  MOE_KERNEL_LINEAR_BACKWARD = 13   /* the two products of its gradient */
+  MOE_KERNEL_LINEAR_BACKWARD = 13,  /* the two products of its gradient */
+  MOE_KERNEL_QUANTIZE = 14,         /* rows to 8-bit codes */
+  MOE_KERNEL_LINEAR_Q8 = 15         /* dense product of 8-bit integers */
 } moe_kernel;
 moe_status moe_profile_next_launch(moe_kernel kernel, hipEvent_t start, hipEvent_t stop);
 
