@@ -126,6 +126,13 @@ def _load():
     L.moe_linear_form.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.POINTER(i32)]
     L.moe_linear_backward_form.restype = st
     L.moe_linear_backward_form.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32, ctypes.POINTER(i32)]
+    f64 = ctypes.c_double
+    L.moe_orthogonalize_workspace_bytes.restype = sz
+    L.moe_orthogonalize_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.moe_orthogonalize.restype = st
+    L.moe_orthogonalize.argtypes = [vp, i32, vp, f64, i32, i32, i32, i32, i32, vp, f64, vp, i32, vp, sz, vp]
+    L.moe_orthogonalize_form.restype = st
+    L.moe_orthogonalize_form.argtypes = [i32, i32, i32, i32, ctypes.POINTER(i32)]
     L.moe_quantize_rows.restype = st
     L.moe_quantize_rows.argtypes = [vp, i32, i32, i32, vp, vp, vp]
     L.moe_linear_q8_workspace_bytes.restype = sz
@@ -194,7 +201,8 @@ def _need(t: torch.Tensor, name: str):
 
 KERNELS = {"route": 0, "dispatch": 1, "gemv_gateup": 2, "gemv_down": 3, "mfma_gateup": 4, "mfma_down": 5,
            "combine": 6, "decode_prep": 7, "router": 8, "balance": 9, "route_backward": 10, "combine_backward": 11,
-           "linear": 12, "linear_backward": 13, "quantize": 14, "linear_q8": 15}
+           "linear": 12, "linear_backward": 13, "quantize": 14, "linear_q8": 15,
+           "orthogonalize": 16}
 ACTS = {"none": 0, "gelu": 1, "silu": 2, "swiglu": 3}
 
 
@@ -734,6 +742,49 @@ def linear_backward_form(T: int, K: int, N: int, act: str = "none", dy_dtype=tor
     form = (ctypes.c_int32 * 4)()
     _check(lib.moe_linear_backward_form(T, K, N, code, *t, sum(_NEED[n] for n in set(need)), form))
     return dict(zip(("tile", "dw_parts", "dx_parts", "terms"), form))
+
+
+def orthogonalize(g: torch.Tensor, momentum: torch.Tensor | None = None, beta: float = 0.95, nesterov: bool = True,
+                  steps: int = 5, coef=None, eps: float = 1e-7, o: torch.Tensor | None = None, o_dtype=None,
+                  ws: torch.Tensor | None = None, stream=None):
+    """moe_orthogonalize: o, the gradient g [R, K] or [B, R, K] (fp32 or bf16; linear_backward's dw) with every singular
+    value brought near 1, as the Muon optimiser applies it: w -= lr * scale * o.
+
+    momentum (fp32, g's shape) is updated in place to beta * momentum + (1 - beta) * g and used instead of g, with
+    `nesterov` mixed with g once more.  coef: (a, b, c) of every step, or one triple per step; None takes the usual
+    quintic.  o is bf16 by default, fp32 with o_dtype (three times the work).  The matrices of a batch share every launch."""
+    if g.dim() not in (2, 3):
+        raise ValueError(f"g must have 2 or 3 dimensions, got {g.dim()}")
+    shape = _rows(g, "g", g.dim())
+    B, R, K = shape if len(shape) == 3 else (1, *shape)
+    a_g = _arg(g, "g", shape, (_F32, _BF16))
+    at = g.get_device()
+    a_m = None if momentum is None else _arg(momentum, "momentum", shape, (_F32,), at)
+    a_coef = None
+    if coef is not None:
+        flat = [float(v) for c in coef for v in c] if hasattr(coef[0], "__len__") else [float(v) for v in coef] * steps
+        if len(flat) != 3 * steps:
+            raise ValueError(f"coef holds one (a, b, c), or one for each of {steps} steps")
+        a_coef = (ctypes.c_float * len(flat))(*flat)
+    if o is None:
+        o = _new(g, shape, o_dtype or _BF16, stream)
+    a_o, o_t = _arg(o, "o", shape, (_F32, _BF16), at), _dtype_code(o)
+    ws, a_ws, n_ws = _ws(ws, lib.moe_orthogonalize_workspace_bytes(B, R, K, o_t), g, at, stream)
+    _launch(lib.moe_orthogonalize, at, stream, a_g, _dtype_code(g), a_m, beta, bool(nesterov), B, R, K, steps, a_coef, eps, a_o,
+            o_t, a_ws, n_ws)
+    return o
+
+
+def orthogonalize_workspace_bytes(B: int, R: int, K: int, o_dtype=torch.bfloat16) -> int:
+    """Bytes of orthogonalize's workspace for B matrices."""
+    return int(lib.moe_orthogonalize_workspace_bytes(B, R, K, *_size_codes("none", o_dtype)[1]))
+
+
+def orthogonalize_form(B: int, R: int, K: int, o_dtype=torch.bfloat16) -> dict:
+    """How orthogonalize cuts its work at these sizes, for tests and measurements (moe_orthogonalize_form)."""
+    form = (ctypes.c_int32 * 2)()
+    _check(lib.moe_orthogonalize_form(B, R, K, *_size_codes("none", o_dtype)[1], form))
+    return dict(zip(("gram", "apply"), form))
 
 
 # ---- the dense parts in 8 bits ----------------------------------------------------------

@@ -471,6 +471,22 @@ bool linear_has_work(int T, int K, int N, moe_act act) {
 bool is_dtype(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16; }
 uintptr_t elem(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }
 
+constexpr int kNewtonMaxSide = 16384, kNewtonMaxSteps = 16;
+constexpr float kNewtonCoef[3] = {3.4445f, -4.7750f, 2.0315f};
+
+bool newton_size(int B, int R, int K) {  // of work there is
+  if (B < 1 || R < 1 || K < 1 || R > kNewtonMaxSide || K > kNewtonMaxSide) return false;
+  const int64_t per = ceil_div(R, 64) * ceil_div(K, 64) * 4096;
+  return B <= ((int64_t)1 << 33) / per;
+}
+moe_status check_newton(const char* fn, int B, int R, int K) {
+  if (B < 0) return fail(MOE_EINVAL, std::string(fn) + ": B < 0");
+  if (!newton_size(B < 1 ? 1 : B, R, K))
+    return fail(MOE_EUNSUPPORTED, std::string(fn) + fmt(": B=%lld, R=%lld, K=%lld (R and K in [1, 16384], padded values up to 2^33)",
+                                                        B, R, K));
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -562,6 +578,44 @@ moe_status moe_linear_backward_form(int T, int K, int N, moe_act act, moe_dtype 
   return MOE_OK;
 }
 
+size_t moe_orthogonalize_workspace_bytes(int B, int R, int K, moe_dtype o_t) {
+  if (!newton_size(B, R, K) || !is_dtype(o_t)) return 0;
+  return orthogonalize_ws_bytes(B, R, K, o_t);
+}
+
+moe_status moe_orthogonalize(const void* g, moe_dtype g_t, float* momentum, double beta, int nesterov, int B, int R, int K,
+                             int steps, const float* coef, double eps, void* o, moe_dtype o_t, void* ws, size_t ws_bytes,
+                             hipStream_t stream) {
+  if (moe_status st = check_newton("moe_orthogonalize", B, R, K)) return st;
+  if (!is_dtype(g_t) || !is_dtype(o_t)) return fail(MOE_EINVAL, "moe_orthogonalize: g or o dtype");
+  if (!(beta >= 0.0 && beta < 1.0)) return fail(MOE_EINVAL, "moe_orthogonalize: beta outside [0, 1)");
+  if (!(eps >= 0.0 && eps < __builtin_huge_val())) return fail(MOE_EINVAL, "moe_orthogonalize: eps");
+  if (steps < 1 || steps > kNewtonMaxSteps) return fail(MOE_EUNSUPPORTED, fmt("moe_orthogonalize: steps=%lld outside [1, 16]", steps));
+  if (B == 0) return MOE_OK;
+  if (!g || !o) return fail(MOE_EINVAL, "moe_orthogonalize: null pointer");
+  if (!aligned(g, elem(g_t)) || !aligned(o, elem(o_t)) || !aligned(momentum, 4) || !aligned(ws, 256))
+    return fail(MOE_EINVAL, "moe_orthogonalize: misaligned buffer (ws needs 256 bytes)");
+  const size_t need = orthogonalize_ws_bytes(B, R, K, o_t);
+  if (!ws || ws_bytes < need)
+    return fail(MOE_EWORKSPACE, fmt("moe_orthogonalize: workspace %lld bytes, needs %lld", (long long)ws_bytes,
+                                    (long long)need));
+  const uint64_t n = (uint64_t)B * R * K;
+  const Span out[] = {{momentum, n * 4}, {o, n * elem(o_t)}, {ws, need}};
+  const Span in[] = {{g, n * elem(g_t)}};
+  if (any_overlap(out, in)) return fail(MOE_EINVAL, "moe_orthogonalize: an output or ws overlaps another buffer");
+  float every[3 * kNewtonMaxSteps];
+  for (int i = 0; i < 3 * steps; ++i) every[i] = coef ? coef[i] : kNewtonCoef[i % 3];
+  return launch_orthogonalize(g, g_t, momentum, beta, nesterov, B, R, K, steps, every, eps, o, o_t, ws, stream);
+}
+
+moe_status moe_orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[2]) {
+  if (moe_status st = check_newton("moe_orthogonalize_form", B, R, K)) return st;
+  if (B == 0 || !form) return fail(MOE_EINVAL, "moe_orthogonalize_form: no matrices, or a null pointer");
+  if (!is_dtype(o_t)) return fail(MOE_EINVAL, "moe_orthogonalize_form: dtype");
+  orthogonalize_form(B, R, K, o_t, form);
+  return MOE_OK;
+}
+
 moe_status moe_quantize_rows(const void* x, moe_dtype x_t, int T, int K, int8_t* q, float* scale, hipStream_t stream) {
   if (T < 0) return fail(MOE_EINVAL, "moe_quantize_rows: T < 0");
   if (T > kLinearMaxT) return fail(MOE_EUNSUPPORTED, fmt("moe_quantize_rows: T=%lld above 2^20", T));
@@ -621,7 +675,7 @@ moe_status moe_linear_q8_form(int T, int K, int N, moe_act act, moe_dtype x_t, i
 }
 
 moe_status moe_profile_next_launch(moe_kernel kernel, hipEvent_t start, hipEvent_t stop) {
-  if ((int)kernel < 0 || (int)kernel > (int)MOE_KERNEL_LINEAR_Q8) return fail(MOE_EINVAL, "moe_profile_next_launch: kernel");
+  if ((int)kernel < 0 || (int)kernel > (int)MOE_KERNEL_ORTHOGONALIZE) return fail(MOE_EINVAL, "moe_profile_next_launch: kernel");
   if (!start || !stop) return fail(MOE_EINVAL, "moe_profile_next_launch: null event");
   ProfileReq& p = profile_req();
   p.kernel = (int)kernel;

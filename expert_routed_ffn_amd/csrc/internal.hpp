@@ -175,6 +175,11 @@ moe_status launch_linear_backward(const void* dy, moe_dtype dy_t, const void* pr
                                   const uint16_t* w, int act, int T, int K, int N, void* dx, moe_dtype dx_t, void* dw,
                                   moe_dtype dw_t, float* db, void* ws, hipStream_t s);
 
+size_t orthogonalize_ws_bytes(int B, int R, int K, moe_dtype o_t);
+void orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[2]);
+moe_status launch_orthogonalize(const void* g, moe_dtype g_t, float* momentum, double beta, int nesterov, int B, int R, int K,
+                                int steps, const float* coef, double eps, void* o, moe_dtype o_t, void* ws, hipStream_t s);
+
 // ---- the dense parts in 8 bits --------------------------------------------------------------
 
 moe_status launch_quantize_rows(const void* x, moe_dtype x_t, int T, int K, int8_t* q, float* scale, hipStream_t s);

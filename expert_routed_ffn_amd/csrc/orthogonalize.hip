@@ -1,0 +1,494 @@
+// orthogonalize.hip -- an update made orthogonal by Newton-Schulz steps:
+//   X = u / (|u|_F + eps);  each step: A = X X^T, P = b A + c A^2, X = a X + P X  (on the shorter side m x n, m <= n)
+// which takes each singular value s of X to a s + b s^3 + c s^5 and leaves the singular vectors as they are.
+//
+// Products run on v_mfma_f32_16x16x32_f16.  fp16 holds 11 bits where bf16 holds 8, and its range is enough: X, A and P of a
+// normalised matrix stay within a few units, and are stored times 2^13, 2^12 and 2^12, so that what lies below fp16's
+// normal range is below 2^-26 of the largest value.
+//
+// What the roundings do: a step multiplies a small singular value by a = 3.44, five of them by 485, and noise beside
+// it as much, so X rounded to 11 bits before each step leaves results of low-rank gradients 1 to 7% off, and bf16 20%
+// or more.  X is therefore kept as two fp16 terms (22 bits): the sum a X takes both, and only the product P X, whose P is
+// nearly 0 on the weak directions, takes the first alone.  P's diagonal, the largest of its values on matrices of
+// even spectrum, stays in fp32 beside it and enters as diag P X.  On random and on low-rank matrices of 60 to 1,024 rows
+// the result is 0.05 to 1.4e-3 of its norm off, a bf16 result's own rounding 1.66e-3.  An fp32 result takes two
+// terms of X, A and P in every product (three passes of the matrix units), and is as near as an fp32 computation.
+//
+// A and P are symmetric: only tiles on and above the diagonal are computed, and stored twice.  All matrices of a
+// call share each launch.  m and n are padded to multiples of 64 with zeros, which stay zeros.
+#include "product_dev.hpp"
+
+namespace moe {
+namespace {
+
+constexpr float kXScale = 8192.0f, kGScale = 4096.0f;  // of X; of A and P
+
+__device__ __forceinline__ uint16_t f32_to_f16(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
+__device__ __forceinline__ float f16_to_f32(uint32_t h) { return (float)__builtin_bit_cast(_Float16, (uint16_t)h); }
+
+// Four values as 8 bytes of fp16 and what they leave, rounded again.
+__device__ __forceinline__ void terms4(const float (&v)[4], uint2& hi, uint2& lo) {
+  uint16_t h[4], l[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    h[r] = f32_to_f16(v[r]);
+    l[r] = f32_to_f16(v[r] - f16_to_f32(h[r]));
+  }
+  hi = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+  lo = make_uint2(l[0] | (uint32_t)l[1] << 16, l[2] | (uint32_t)l[3] << 16);
+}
+__device__ __forceinline__ void unpack4(uint2 q, float (&v)[4]) {
+  v[0] = f16_to_f32(q.x & 0xFFFF); v[1] = f16_to_f32(q.x >> 16);
+  v[2] = f16_to_f32(q.y & 0xFFFF); v[3] = f16_to_f32(q.y >> 16);
+}
+
+// ---- the update and its norm -----------------------------------------------------------
+
+struct Update {
+  const void* g;
+  float* moment;  // null: the update is g
+  int g_bf16, nesterov;
+  float beta, rest;  // rest = 1 - beta
+  int R, K;
+};
+
+// u from g and the moment after this step.
+__device__ __forceinline__ float update_of(const Update& u, float g, float m) {
+  return !u.moment ? g : u.nesterov ? __builtin_fmaf(u.beta, m, u.rest * g) : m;
+}
+
+// The moment m = beta m + (1 - beta) g, and per workgroup the sum of u^2.  In 64 bits: squares of fp32 values neither
+// overflow nor vanish there.
+__global__ __launch_bounds__(256) void newton_moment_kernel(Update u, int blocks, double* __restrict__ parts) {
+  __shared__ double red[4];
+  const int matrix = blockIdx.x / blocks, block = blockIdx.x - matrix * blocks;
+  const int64_t n = (int64_t)u.R * u.K, base = matrix * n;
+  double sum = 0.0;
+  for (int64_t i = ((int64_t)block * 256 + threadIdx.x) * 4; i < n; i += (int64_t)blocks * 1024) {
+    float g[4], m[4] = {0.f, 0.f, 0.f, 0.f};
+    if (i + 4 <= n) {
+      load4(u.g, u.g_bf16, base + i, g);
+      if (u.moment) {
+        load4(u.moment, 0, base + i, m);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[r] = __builtin_fmaf(u.beta, m[r], u.rest * g[r]);
+        store4(u.moment, 0, base + i, m);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const double v = update_of(u, g[r], m[r]);
+        sum += v * v;
+      }
+    } else {
+      for (int r = 0; r < (int)(n - i); ++r) {
+        const float gv = load_any(u.g, u.g_bf16, base + i + r);
+        float mv = 0.0f;
+        if (u.moment) {
+          mv = __builtin_fmaf(u.beta, u.moment[base + i + r], u.rest * gv);
+          u.moment[base + i + r] = mv;
+        }
+        const double v = update_of(u, gv, mv);
+        sum += v * v;
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) parts[blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+struct Planes {  // of fp16 terms, `plane` words apart, matrices `step` words apart
+  uint16_t* p;
+  int64_t plane, step;
+};
+
+// X in two terms, padded with zeros, transposed where R > K: a workgroup brings 64 x 64 values of u through LDS.
+__global__ __launch_bounds__(256) void newton_start_kernel(Update u, int blocks, const double* __restrict__ parts, double eps,
+                                                           int tr, int tk, Planes x, int ld) {
+  __shared__ float tile[64][65];
+  __shared__ double red[4];
+  const int per = tr * tk, matrix = blockIdx.x / per, t = blockIdx.x - matrix * per;
+  const int r0 = t / tk * 64, k0 = t % tk * 64;
+  const int64_t base = (int64_t)matrix * u.R * u.K;
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < blocks; i += 256) sum += parts[(int64_t)matrix * blocks + i];
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+  const int c = (threadIdx.x & 15) * 4, k = k0 + c;
+  float v[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 16 * i + (threadIdx.x >> 4);
+    float g[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
+    if (r < u.R && k + 4 <= u.K) {
+      load4(u.g, u.g_bf16, base + (int64_t)r * u.K + k, g);
+      if (u.moment) load4(u.moment, 0, base + (int64_t)r * u.K + k, m);
+    } else if (r < u.R) {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (k + e < u.K) {
+          g[e] = load_any(u.g, u.g_bf16, base + (int64_t)r * u.K + k + e);
+          if (u.moment) m[e] = u.moment[base + (int64_t)r * u.K + k + e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[i][e] = update_of(u, g[e], m[e]);
+  }
+  __syncthreads();
+  const double total = sqrt((red[0] + red[1]) + (red[2] + red[3])) + eps;
+  // (a zero matrix stays zero; one with an infinity or a NaN becomes NaN throughout)
+  const double inv = total == 0.0 ? 0.0 : total < __builtin_huge_val() ? kXScale / total : __builtin_nan("");
+  const bool turned = u.R > u.K;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 16 * i + (threadIdx.x >> 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[i][e] = (float)(v[i][e] * inv);
+    if (turned) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tile[c + e][r] = v[i][e];
+    }
+  }
+  if (turned) __syncthreads();
+  uint16_t* to = x.p + matrix * x.step + (turned ? (int64_t)k0 * ld + r0 : (int64_t)r0 * ld + k0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 16 * i + (threadIdx.x >> 4);
+    if (turned) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] = tile[r][c + e];
+    }
+    uint2 hi, lo;
+    terms4(v[i], hi, lo);
+    uint16_t* at = to + (int64_t)r * ld + c;
+    *reinterpret_cast<uint2*>(at) = hi;
+    *reinterpret_cast<uint2*>(at + x.plane) = lo;
+  }
+}
+
+// ---- the steps' products ------------------------------------------------------------------
+
+enum Stage { kGram, kPoly, kApply, kLast };
+
+struct Step {
+  Mats mats;                // of the first matrix
+  int64_t a_step, b_step;   // words from one matrix to the next
+  int tiles;                // per matrix
+  Planes in, out;           // kPoly: A -> P;  kApply: X -> X;  kGram: -> A;  kLast: X
+  float* diag;              // [matrix][M] P's diagonal: written by kPoly, read by kApply and kLast
+  float a, b, c;
+  void* o;                  // kLast: [matrix][rows][cols], where X is [cols][rows] if `turned`
+  int o_bf16, turned, rows, cols;
+};
+
+// One tile of one matrix.  SYM stages compute the tiles on and above the diagonal.
+template <typename T, int STAGE, int TERMS>
+__global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st) {
+  constexpr bool SYM = STAGE == kGram || STAGE == kPoly;
+  constexpr int TM = T::TM, TN = T::TN, WM = T::WM, WN = T::WN, kFM = T::kFM, kFN = T::kFN, kThreads = T::kThreads;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[T::kLds];
+  const int item = die_item(blockIdx.x, gridDim.x);
+  const int matrix = uniform(item / st.tiles), t = uniform(item - matrix * st.tiles);
+  Mats p = st.mats;
+  p.A += matrix * st.a_step;
+  p.B += matrix * st.b_step;
+  int m0, n0;
+  if constexpr (SYM) {  // column j of tiles holds j + 1 of them
+    static_assert(TM == TN, "square tiles");
+    int j = (int)((__builtin_sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
+    while ((j + 1) * (j + 2) / 2 <= t) ++j;
+    while (j * (j + 1) / 2 > t) --j;
+    n0 = uniform(j * TN);
+    m0 = uniform((t - j * (j + 1) / 2) * TM);
+  } else {  // bands of 8 row tiles, walked column by column
+    const int tm = (p.M + TM - 1) / TM, tn = (p.R + TN - 1) / TN;
+    const int band = t / (8 * tn), in_band = t - band * 8 * tn, band_rows = min(8, tm - band * 8);
+    m0 = uniform((band * 8 + in_band % band_rows) * TM);
+    n0 = uniform(in_band / band_rows * TN);
+  }
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int kg = wave / (WM * WN), wm = T::KG == 1 ? wave / WN : wave / WN % WM, wn = wave % WN;
+  const int steps = p.K / kBK * p.nseg;
+  f32x4_t acc[kFM][kFN];
+  // rows past the end read the last one and are not stored
+  product_loop<T, false, !SYM, 0, KindF16>(
+      p, m0, n0, 0, steps, [&](int r) { return min(m0 + r, p.M - 1) - m0; },
+      [&](int r) { return min(n0 + r, p.R - 1) - n0; }, lds, acc);
+
+  // Through LDS, so that loads and stores run along rows: 16-byte pieces, piece c of row m at c ^ (m % 16).
+  float* tile_c = reinterpret_cast<float*>(lds);
+  constexpr int kPieces = TN / 4, kPassRows = TM / T::kPasses, kStep = kThreads / kPieces;
+  constexpr int kAhead = std::min(4, kPassRows / kStep);  // rows whose loads are under way together
+  static_assert(kThreads % kPieces == 0 && 64 % (kAhead * kStep) == 0, "a thread keeps to four columns, rows come by 64");
+  const int r16 = lane & 15, q = lane >> 4;
+  const int ld = p.R;
+  const uint16_t* in = st.in.p + matrix * st.in.step;
+  uint16_t* out = st.out.p + matrix * st.out.step;
+  float* diag = st.diag + (int64_t)matrix * p.M;
+#pragma unroll
+  for (int pass = 0; pass < T::kPasses; ++pass) {
+    hand_over();
+    auto put = [&](auto add) {
+#pragma unroll
+      for (int i = 0; i < kFM; ++i)
+#pragma unroll
+        for (int j = 0; j < kFN; ++j) {
+          const int m = (T::kPasses == 1 ? (TM / WM) * wm : 0) + 16 * i + r16, c = (TN / WN / 4) * wn + 4 * j + q;
+          f32x4_t* at = reinterpret_cast<f32x4_t*>(tile_c + (m * kPieces + (c ^ (m & 15))) * 4);
+          *at = decltype(add)::value ? acc[i][j] + *at : acc[i][j];
+        }
+    };
+    static_assert(T::KG == 1 || T::kPasses == 1, "groups of waves are added once");
+    if constexpr (T::KG == 2) {
+      if (kg == 1) put(std::false_type{});
+      hand_over();
+      if (kg == 0) put(std::true_type{});
+    } else {
+      if (T::kPasses == 1 || wm == pass) put(std::false_type{});
+    }
+    hand_over();
+    const int o = tid % kPieces, n = n0 + 4 * o, r0 = tid / kPieces;
+    const int mp = m0 + pass * kPassRows;               // the pass's first row
+    const int rows = min(kPassRows, p.M - mp);          // (a multiple of 64, or below 1)
+    const bool cols_in = n < p.R;
+    const bool mirrored = (SYM && m0 != n0) || (STAGE == kLast && st.turned);
+    for (int d = r0; d < rows; d += kAhead * kStep) {
+      uint2 hi[kAhead], lo[kAhead];
+      float dg[kAhead];
+      // (columns past the end read the row's first values and are not stored)
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int m = mp + d + k * kStep;
+        const uint16_t* at = in + (int64_t)m * ld + (cols_in ? n : 0);
+        if constexpr (STAGE != kGram) hi[k] = *reinterpret_cast<const uint2*>(at);
+        if constexpr (STAGE == kApply || STAGE == kLast || (STAGE == kPoly && TERMS == 2))
+          lo[k] = *reinterpret_cast<const uint2*>(at + st.in.plane);
+        if constexpr (STAGE == kApply || STAGE == kLast) dg[k] = diag[m];
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int r = d + k * kStep, m = mp + r;
+        float4* at = reinterpret_cast<float4*>(tile_c + (r * kPieces + (o ^ (r & 15))) * 4);
+        const float4 s = *at;
+        const float z[4] = {s.x, s.y, s.z, s.w};
+        float h[4], l[4], v[4];
+        if constexpr (STAGE != kGram) unpack4(hi[k], h);
+        if constexpr (STAGE == kApply || STAGE == kLast || (STAGE == kPoly && TERMS == 2)) unpack4(lo[k], l);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (STAGE == kGram) {
+            v[e] = z[e] * (kGScale / (kXScale * kXScale));
+          } else if constexpr (STAGE == kPoly) {
+            const float g = TERMS == 2 ? h[e] + l[e] : h[e];
+            v[e] = __builtin_fmaf(st.b, g, st.c * (z[e] * (1.0f / kGScale)));
+            if (m == n + e) {
+              diag[m] = v[e] * (1.0f / kGScale);
+              v[e] = 0.0f;
+            }
+          } else {
+            const float x = h[e] + l[e], by = TERMS == 2 ? x : h[e];
+            v[e] = __builtin_fmaf(st.a, x, __builtin_fmaf(dg[k], by, z[e] * (1.0f / kGScale)));
+          }
+        }
+        if constexpr (STAGE == kLast) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] *= 1.0f / kXScale;
+        }
+        if (mirrored) *at = make_float4(v[0], v[1], v[2], v[3]);
+        if constexpr (STAGE == kLast) {
+          if (!st.turned && m < st.rows) {
+            const size_t i = ((size_t)matrix * st.rows + m) * st.cols + n;
+            if (n + 4 <= st.cols) {
+              store4(st.o, st.o_bf16, i, v);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 3; ++e)
+                if (n + e < st.cols) store_any(st.o, st.o_bf16, i + e, v[e]);
+            }
+          }
+        } else if (cols_in) {
+          uint2 a, b;
+          terms4(v, a, b);
+          uint16_t* to = out + (int64_t)m * ld + n;
+          *reinterpret_cast<uint2*>(to) = a;
+          if constexpr (STAGE == kApply || TERMS == 2) *reinterpret_cast<uint2*>(to + st.out.plane) = b;
+        }
+      }
+    }
+    if constexpr (STAGE != kApply) {
+      if (mirrored) {  // the tile's transpose: a thread takes four rows of a column
+        hand_over();
+        constexpr int kRowPieces = kPassRows / 4;
+        static_assert(kThreads % kRowPieces == 0, "rows per thread");
+        const int rq = tid % kRowPieces * 4, m = mp + rq;
+        for (int c = tid / kRowPieces; c < TN; c += kThreads / kRowPieces) {
+          if (rq >= rows || n0 + c >= p.R) continue;
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = tile_c[((rq + e) * kPieces + ((c >> 2) ^ ((rq + e) & 15))) * 4 + (c & 3)];
+          if constexpr (STAGE == kLast) {
+            if (n0 + c < st.rows) {
+              const size_t i = ((size_t)matrix * st.rows + n0 + c) * st.cols + m;
+              if (m + 4 <= st.cols) {
+                store4(st.o, st.o_bf16, i, v);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                  if (m + e < st.cols) store_any(st.o, st.o_bf16, i + e, v[e]);
+              }
+            }
+          } else {
+            uint2 a, b;
+            terms4(v, a, b);
+            uint16_t* to = out + (int64_t)(n0 + c) * ld + m;
+            *reinterpret_cast<uint2*>(to) = a;
+            if constexpr (TERMS == 2) *reinterpret_cast<uint2*>(to + st.out.plane) = b;
+          }
+        }
+      }
+    }
+  }
+}
+
+// ---- sizes ------------------------------------------------------------------------------------
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+int up64(int v) { return (v + 63) / 64 * 64; }
+
+int64_t triangle(int64_t t) { return t * (t + 1) / 2; }
+
+struct NewtonPlan {
+  int m, n;           // padded
+  int terms, blocks;  // fp16 terms of products; workgroups of the norm per matrix
+  int shape[2];       // tile shapes of the symmetric products (A and P alike) and of P X
+  size_t xa, xb, gram, poly, diag, parts, bytes;
+};
+int64_t newton_tiles(const NewtonPlan& p, bool sym, int side) {
+  const int64_t tm = ceil_div(p.m, side);
+  return sym ? triangle(tm) : tm * ceil_div(p.n, side);
+}
+NewtonPlan newton_plan(int64_t B, int R, int K, moe_dtype o_t) {
+  NewtonPlan p{};
+  p.m = up64(std::min(R, K));
+  p.n = up64(std::max(R, K));
+  p.terms = o_t == MOE_F32 ? 2 : 1;
+  p.blocks = (int)std::min<int64_t>(512, ceil_div((int64_t)R * K, 8192));
+  const int passes = p.terms == 2 ? 3 : 1;
+  for (int i = 0; i < 2; ++i) {
+    double least = 0;
+    for (int shape = 0; shape < 3; ++shape) {
+      const int64_t tiles = B * newton_tiles(p, i == 0, shape_side(shape));
+      // A's and P's products share a choice: their reductions added
+      const int64_t steps = i == 0 ? (int64_t)passes * (p.n + p.m) / kBK : (int64_t)passes * p.m / kBK;
+      const double c = tile_cost(shape, tiles, steps);
+      if (least == 0 || c < least) {
+        least = c;
+        p.shape[i] = shape;
+      }
+    }
+  }
+  size_t o = 0;
+  const size_t x = (size_t)B * p.m * p.n * 2, s = (size_t)B * p.m * p.m * 2;
+  p.xa = o; o = up256(o + 2 * x);
+  p.xb = o; o = up256(o + 2 * x);
+  p.gram = o; o = up256(o + p.terms * s);
+  p.poly = o; o = up256(o + p.terms * s);
+  p.diag = o; o = up256(o + (size_t)B * p.m * 4);
+  p.parts = o; o = up256(o + (size_t)B * p.blocks * 8);
+  p.bytes = o;
+  return p;
+}
+
+template <int STAGE>
+moe_status launch_stage(const NewtonPlan& pl, int64_t B, Step st, hipStream_t s) {
+  const int shape = pl.shape[STAGE == kGram || STAGE == kPoly ? 0 : 1];
+  st.tiles = (int)newton_tiles(pl, STAGE == kGram || STAGE == kPoly, shape_side(shape));
+  const dim3 grid((unsigned)(B * st.tiles));
+  auto go = [&](auto tile) {
+    using T = decltype(tile);
+    const dim3 threads((unsigned)T::kThreads);
+    if (pl.terms == 2) launch_k(MOE_KERNEL_ORTHOGONALIZE, newton_product_kernel<T, STAGE, 2>, grid, threads, 0, s, st);
+    else launch_k(MOE_KERNEL_ORTHOGONALIZE, newton_product_kernel<T, STAGE, 1>, grid, threads, 0, s, st);
+  };
+  if (shape == 0) go(Tiny{});
+  else if (shape == 1) go(Small{});
+  else go(Large{});
+  return check_launch("orthogonalize");
+}
+
+}  // namespace
+
+size_t orthogonalize_ws_bytes(int B, int R, int K, moe_dtype o_t) { return newton_plan(B, R, K, o_t).bytes; }
+
+void orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[2]) {
+  const NewtonPlan p = newton_plan(B, R, K, o_t);
+  form[0] = shape_side(p.shape[0]);
+  form[1] = shape_side(p.shape[1]);
+}
+
+moe_status launch_orthogonalize(const void* g, moe_dtype g_t, float* momentum, double beta, int nesterov, int B, int R, int K,
+                                int steps, const float* coef, double eps, void* o, moe_dtype o_t, void* ws, hipStream_t s) {
+  const NewtonPlan pl = newton_plan(B, R, K, o_t);
+  uint8_t* base = reinterpret_cast<uint8_t*>(ws);
+  const int64_t xs = (int64_t)pl.m * pl.n, gs = (int64_t)pl.m * pl.m;
+  auto planes = [&](size_t at, int64_t step) { return Planes{reinterpret_cast<uint16_t*>(base + at), B * step, step}; };
+  Planes x = planes(pl.xa, xs), next = planes(pl.xb, xs);
+  const Planes gram = planes(pl.gram, gs), poly = planes(pl.poly, gs);
+  double* parts = reinterpret_cast<double*>(base + pl.parts);
+  const Update u{g, momentum, g_t == MOE_BF16, nesterov, (float)beta, (float)(1.0 - beta), R, K};
+  newton_moment_kernel<<<dim3((unsigned)((int64_t)B * pl.blocks)), 256, 0, s>>>(u, pl.blocks, parts);
+  if (moe_status st = check_launch("orthogonalize")) return st;
+  const int tr = (int)ceil_div(R, 64), tk = (int)ceil_div(K, 64);
+  newton_start_kernel<<<dim3((unsigned)((int64_t)B * tr * tk)), 256, 0, s>>>(u, pl.blocks, parts, eps, tr, tk, x, pl.n);
+  if (moe_status st = check_launch("orthogonalize")) return st;
+
+  Step st{};
+  // the passes of two terms: first x first, first x second, second x first
+  st.mats.nseg = pl.terms == 2 ? 3 : 1;
+  st.mats.sa = 1u << 4;
+  st.mats.sb = 1u << 2;
+  st.mats.M = pl.m;
+  st.diag = reinterpret_cast<float*>(base + pl.diag);
+  st.o = o;
+  st.o_bf16 = o_t == MOE_BF16;
+  st.turned = R > K;
+  st.rows = R;
+  st.cols = K;
+  auto operands = [&](const Planes& a, int lda, const Planes& b, int ldb, int cols, int k) {
+    st.mats.A = a.p;
+    st.mats.B = b.p;
+    st.mats.a_plane = a.plane;
+    st.mats.b_plane = b.plane;
+    st.mats.lda = lda;
+    st.mats.ldb = ldb;
+    st.mats.R = cols;
+    st.mats.K = k;
+    st.a_step = a.step;
+    st.b_step = b.step;
+  };
+  for (int i = 0; i < steps; ++i) {
+    st.a = coef[3 * i];
+    st.b = coef[3 * i + 1];
+    st.c = coef[3 * i + 2];
+    operands(x, pl.n, x, pl.n, pl.m, pl.n);
+    st.in = gram;  // (not read)
+    st.out = gram;
+    if (moe_status e = launch_stage<kGram>(pl, B, st, s)) return e;
+    operands(gram, pl.m, gram, pl.m, pl.m, pl.m);
+    st.in = gram;
+    st.out = poly;
+    if (moe_status e = launch_stage<kPoly>(pl, B, st, s)) return e;
+    operands(poly, pl.m, x, pl.n, pl.n, pl.m);
+    st.in = x;
+    st.out = next;
+    if (moe_status e = i + 1 < steps ? launch_stage<kApply>(pl, B, st, s) : launch_stage<kLast>(pl, B, st, s)) return e;
+    std::swap(x, next);
+  }
+  return MOE_OK;
+}
+
+}  // namespace moe

@@ -518,6 +518,38 @@ moe_status moe_linear_backward_form(int T, int K, int N, moe_act act, moe_dtype 
                                     moe_dtype dw_t, int need, int32_t form[4]);
 
 /*
+ * moe_orthogonalize -- the update of a weight matrix made orthogonal (nearly) by Newton-Schulz steps, for B matrices at once.
+ * For each [R x K] matrix:
+ *   momentum given:  momentum = beta * momentum + (1 - beta) * g, in place, and
+ *                    u = beta * momentum + (1 - beta) * g with nesterov, else u = momentum;
+ *   without:         u = g;
+ *   X = u / (|u|_F + eps);  then `steps` times, with that step's (a, b, c):
+ *   X = a X + (b A + c A A) X,  A = X X^T;   o = X.
+ * Each step takes a singular value s to a s + b s^3 + c s^5 and leaves the singular vectors as they are.
+ *   g         [B x R x K], dtype g_t; 1 <= R, K <= 16384.
+ *   momentum  NULL or [B x R x K] fp32, in and out.     0 <= beta < 1; eps >= 0, finite.
+ *   steps     1 ... 16.   coef  host: [steps x 3], NULL: (3.4445, -4.7750, 2.0315) in every step; read before the
+ *             call returns.  Singular values may not pass 8 on the way (values past that become infinite or NaN).
+ *   o         [B x R x K] out, dtype o_t.
+ *   ws        moe_orthogonalize_workspace_bytes(B, R, K, o_t) bytes, 256-byte aligned (0 for sizes and types that the call
+ *             refuses, and for B == 0).
+ * momentum, o and ws may not overlap g or each other.  With R and K rounded up to multiples of 64, B * R * K <= 2^33.
+ * The norm's sum is 64-bit, all others are fp32.  A bf16 o comes from products of fp16 terms with 11 bits, X held
+ * with 22 (result to 2e-3 of its norm before its rounding, with the usual coefficients); an fp32 o from products of 22-bit terms, as near as fp32 arithmetic.
+ * A matrix of zeros gives zeros when eps == 0, too; one whose u has an infinity or a NaN gives NaN throughout; neither touches the
+ * batch's other matrices.  The same bits for the same inputs every time.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE.
+ */
+size_t moe_orthogonalize_workspace_bytes(int B, int R, int K, moe_dtype o_t);
+moe_status moe_orthogonalize(const void* g, moe_dtype g_t, float* momentum, double beta, int nesterov, int B, int R, int K,
+                             int steps, const float* coef, double eps, void* o, moe_dtype o_t, void* ws, size_t ws_bytes,
+                             hipStream_t stream);
+
+/* How moe_orthogonalize cuts its work, as moe_linear_form: sides of the square tiles of A and A A, and of the product
+ * with X. */
+moe_status moe_orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[2]);
+
+/*
  * Serving the dense parts in 8 bits.
  *
  * moe_quantize_rows gives a matrix one scale per row: rows are output channels when the matrix is a weight, tokens when
@@ -588,7 +620,8 @@ typedef enum moe_kernel {
   MOE_KERNEL_LINEAR = 12,           /* dense product (few tokens, or tiled) */
   MOE_KERNEL_LINEAR_BACKWARD = 13,  /* the two products of its gradient */
   MOE_KERNEL_QUANTIZE = 14,         /* rows to 8-bit codes */
-  MOE_KERNEL_LINEAR_Q8 = 15         /* dense product of 8-bit integers */
+  MOE_KERNEL_LINEAR_Q8 = 15,        /* dense product of 8-bit integers */
+  MOE_KERNEL_ORTHOGONALIZE = 16     /* one product of its steps */
 } moe_kernel;
 moe_status moe_profile_next_launch(moe_kernel kernel, hipEvent_t start, hipEvent_t stop);
 
