@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["api.hip", "route_topk.hip", "dispatch.hip", "ffn_gemv.hip", "ffn_mfma.hip", "combine.hip",
            "slot_table.hip", "router.hip", "noalloc.hip", "balance.hip", "combine_grad.hip", "linear.hip",
            "linear_grad.hip", "product.hip", "quantize.hip", "linear_q8.hip",
-           "orthogonalize.hip"]
+           "orthogonalize.hip", "orthogonalize_small.hip"]
 
 ARCH = "gfx950"
 # Packed fp32 VALU ops are disabled for all device code.  Floating-point

@@ -16,10 +16,15 @@
 //
 // A and P are symmetric: only tiles on and above the diagonal are computed, and stored twice.  All matrices of a
 // call share each launch.  m and n are padded to multiples of 64 with zeros, which stay zeros.
+#include "newton_dev.hpp"
 #include "product_dev.hpp"
 
 namespace moe {
 namespace {
+
+// A tile shape besides those of product_dev.hpp: 192 x 192 (12 waves, 64 x 48 each), for symmetric products whose 256 x 256
+// tiles leave half of the CUs without one.
+using Mid = Tile<192, 192, 3, 4>;
 
 constexpr float kXScale = 8192.0f, kGScale = 4096.0f;  // of X; of A and P
 
@@ -43,19 +48,6 @@ __device__ __forceinline__ void unpack4(uint2 q, float (&v)[4]) {
 }
 
 // ---- the update and its norm -----------------------------------------------------------
-
-struct Update {
-  const void* g;
-  float* moment;  // null: the update is g
-  int g_bf16, nesterov;
-  float beta, rest;  // rest = 1 - beta
-  int R, K;
-};
-
-// u from g and the moment after this step.
-__device__ __forceinline__ float update_of(const Update& u, float g, float m) {
-  return !u.moment ? g : u.nesterov ? __builtin_fmaf(u.beta, m, u.rest * g) : m;
-}
 
 // The moment m = beta m + (1 - beta) g, and per workgroup the sum of u^2.  In 64 bits: squares of fp32 values neither
 // overflow nor vanish there.
@@ -122,25 +114,10 @@ __global__ __launch_bounds__(256) void newton_start_kernel(Update u, int blocks,
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = r0 + 16 * i + (threadIdx.x >> 4);
-    float g[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
-    if (r < u.R && k + 4 <= u.K) {
-      load4(u.g, u.g_bf16, base + (int64_t)r * u.K + k, g);
-      if (u.moment) load4(u.moment, 0, base + (int64_t)r * u.K + k, m);
-    } else if (r < u.R) {
-#pragma unroll
-      for (int e = 0; e < 3; ++e)
-        if (k + e < u.K) {
-          g[e] = load_any(u.g, u.g_bf16, base + (int64_t)r * u.K + k + e);
-          if (u.moment) m[e] = u.moment[base + (int64_t)r * u.K + k + e];
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[i][e] = update_of(u, g[e], m[e]);
+    load_update<false>(u, base, r, k, v[i]);
   }
   __syncthreads();
-  const double total = sqrt((red[0] + red[1]) + (red[2] + red[3])) + eps;
-  // (a zero matrix stays zero; one with an infinity or a NaN becomes NaN throughout)
-  const double inv = total == 0.0 ? 0.0 : total < __builtin_huge_val() ? kXScale / total : __builtin_nan("");
+  const double inv = kXScale * inverse_norm((red[0] + red[1]) + (red[2] + red[3]), eps);
   const bool turned = u.R > u.K;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -211,6 +188,34 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
   }
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int kg = wave / (WM * WN), wm = T::KG == 1 ? wave / WN : wave / WN % WM, wn = wave % WN;
+  // Through LDS, so that loads and stores run along rows: 16-byte pieces, piece c of row m at c ^ (m % 16).
+  float* tile_c = reinterpret_cast<float*>(lds);
+  constexpr int kPieces = TN / 4, kPassRows = TM / T::kPasses, kStep = kThreads / kPieces;
+  // What the epilogue reads is loaded before the products where the registers hold it, else four rows ahead.
+  constexpr bool kEarly = STAGE != kGram && TM <= 128;
+  constexpr int kAhead = kEarly ? kPassRows / kStep : std::min(4, kPassRows / kStep);
+  static_assert(kThreads % kPieces == 0 && kPassRows % 64 == 0 && 64 % (std::min(4, kAhead) * kStep) == 0, "rows come by 64");
+  const int r16 = lane & 15, q = lane >> 4;
+  const int ld = p.R;
+  const uint16_t* in = st.in.p + matrix * st.in.step;
+  uint16_t* out = st.out.p + matrix * st.out.step;
+  float* diag = st.diag + (int64_t)matrix * p.M;
+  const int o = tid % kPieces, n = n0 + 4 * o, r0 = tid / kPieces;
+  const bool cols_in = n < p.R;
+  uint2 hi[kAhead], lo[kAhead];
+  float dg[kAhead];
+  auto ahead = [&](int first) {  // of rows first + k kStep; those past the end read the first row, columns the first ones
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int m = first + k * kStep;
+      const uint16_t* at = in + (int64_t)(m < p.M ? m : m0) * ld + (cols_in ? n : 0);
+      if constexpr (STAGE != kGram) hi[k] = *reinterpret_cast<const uint2*>(at);
+      if constexpr (STAGE == kApply || STAGE == kLast || (STAGE == kPoly && TERMS == 2))
+        lo[k] = *reinterpret_cast<const uint2*>(at + st.in.plane);
+      if constexpr (STAGE == kApply || STAGE == kLast) dg[k] = diag[m < p.M ? m : m0];
+    }
+  };
+  if constexpr (kEarly) ahead(m0 + r0);
   const int steps = p.K / kBK * p.nseg;
   f32x4_t acc[kFM][kFN];
   // rows past the end read the last one and are not stored
@@ -218,16 +223,6 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
       p, m0, n0, 0, steps, [&](int r) { return min(m0 + r, p.M - 1) - m0; },
       [&](int r) { return min(n0 + r, p.R - 1) - n0; }, lds, acc);
 
-  // Through LDS, so that loads and stores run along rows: 16-byte pieces, piece c of row m at c ^ (m % 16).
-  float* tile_c = reinterpret_cast<float*>(lds);
-  constexpr int kPieces = TN / 4, kPassRows = TM / T::kPasses, kStep = kThreads / kPieces;
-  constexpr int kAhead = std::min(4, kPassRows / kStep);  // rows whose loads are under way together
-  static_assert(kThreads % kPieces == 0 && 64 % (kAhead * kStep) == 0, "a thread keeps to four columns, rows come by 64");
-  const int r16 = lane & 15, q = lane >> 4;
-  const int ld = p.R;
-  const uint16_t* in = st.in.p + matrix * st.in.step;
-  uint16_t* out = st.out.p + matrix * st.out.step;
-  float* diag = st.diag + (int64_t)matrix * p.M;
 #pragma unroll
   for (int pass = 0; pass < T::kPasses; ++pass) {
     hand_over();
@@ -250,27 +245,15 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
       if (T::kPasses == 1 || wm == pass) put(std::false_type{});
     }
     hand_over();
-    const int o = tid % kPieces, n = n0 + 4 * o, r0 = tid / kPieces;
-    const int mp = m0 + pass * kPassRows;               // the pass's first row
-    const int rows = min(kPassRows, p.M - mp);          // (a multiple of 64, or below 1)
-    const bool cols_in = n < p.R;
+    const int mp = m0 + pass * kPassRows;       // the pass's first row
+    const int rows = min(kPassRows, p.M - mp);  // (a multiple of 64, or below 1)
     const bool mirrored = (SYM && m0 != n0) || (STAGE == kLast && st.turned);
     for (int d = r0; d < rows; d += kAhead * kStep) {
-      uint2 hi[kAhead], lo[kAhead];
-      float dg[kAhead];
-      // (columns past the end read the row's first values and are not stored)
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int m = mp + d + k * kStep;
-        const uint16_t* at = in + (int64_t)m * ld + (cols_in ? n : 0);
-        if constexpr (STAGE != kGram) hi[k] = *reinterpret_cast<const uint2*>(at);
-        if constexpr (STAGE == kApply || STAGE == kLast || (STAGE == kPoly && TERMS == 2))
-          lo[k] = *reinterpret_cast<const uint2*>(at + st.in.plane);
-        if constexpr (STAGE == kApply || STAGE == kLast) dg[k] = diag[m];
-      }
+      if constexpr (!kEarly) ahead(mp + d);
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int r = d + k * kStep, m = mp + r;
+        if (kEarly && r >= rows) break;
         float4* at = reinterpret_cast<float4*>(tile_c + (r * kPieces + (o ^ (r & 15))) * 4);
         const float4 s = *at;
         const float z[4] = {s.x, s.y, s.z, s.w};
@@ -359,6 +342,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 int up64(int v) { return (v + 63) / 64 * 64; }
 
+constexpr int kSides[4] = {64, 128, 256, 192};
 int64_t triangle(int64_t t) { return t * (t + 1) / 2; }
 
 struct NewtonPlan {
@@ -381,7 +365,7 @@ NewtonPlan newton_plan(int64_t B, int R, int K, moe_dtype o_t) {
   for (int i = 0; i < 2; ++i) {
     double least = 0;
     for (int shape = 0; shape < 3; ++shape) {
-      const int64_t tiles = B * newton_tiles(p, i == 0, shape_side(shape));
+      const int64_t tiles = B * newton_tiles(p, i == 0, kSides[shape]);
       // A's and P's products share a choice: their reductions added
       const int64_t steps = i == 0 ? (int64_t)passes * (p.n + p.m) / kBK : (int64_t)passes * p.m / kBK;
       const double c = tile_cost(shape, tiles, steps);
@@ -406,7 +390,7 @@ NewtonPlan newton_plan(int64_t B, int R, int K, moe_dtype o_t) {
 template <int STAGE>
 moe_status launch_stage(const NewtonPlan& pl, int64_t B, Step st, hipStream_t s) {
   const int shape = pl.shape[STAGE == kGram || STAGE == kPoly ? 0 : 1];
-  st.tiles = (int)newton_tiles(pl, STAGE == kGram || STAGE == kPoly, shape_side(shape));
+  st.tiles = (int)newton_tiles(pl, STAGE == kGram || STAGE == kPoly, kSides[shape]);
   const dim3 grid((unsigned)(B * st.tiles));
   auto go = [&](auto tile) {
     using T = decltype(tile);
@@ -416,22 +400,32 @@ moe_status launch_stage(const NewtonPlan& pl, int64_t B, Step st, hipStream_t s)
   };
   if (shape == 0) go(Tiny{});
   else if (shape == 1) go(Small{});
-  else go(Large{});
+  else if (shape == 2) go(Large{});
+  else if constexpr (STAGE == kGram || STAGE == kPoly) go(Mid{});
   return check_launch("orthogonalize");
 }
 
 }  // namespace
 
-size_t orthogonalize_ws_bytes(int B, int R, int K, moe_dtype o_t) { return newton_plan(B, R, K, o_t).bytes; }
+// (which way a call takes depends on its coefficients, which the query does not know)
+size_t orthogonalize_ws_bytes(int B, int R, int K, moe_dtype o_t) {
+  return std::max(newton_plan(B, R, K, o_t).bytes, newton_small_ws_bytes(B, R, K));
+}
 
 void orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[2]) {
+  if (newton_is_small(B, R, K, 5, nullptr)) {
+    form[0] = form[1] = 0;
+    return;
+  }
   const NewtonPlan p = newton_plan(B, R, K, o_t);
-  form[0] = shape_side(p.shape[0]);
-  form[1] = shape_side(p.shape[1]);
+  form[0] = kSides[p.shape[0]];
+  form[1] = kSides[p.shape[1]];
 }
 
 moe_status launch_orthogonalize(const void* g, moe_dtype g_t, float* momentum, double beta, int nesterov, int B, int R, int K,
                                 int steps, const float* coef, double eps, void* o, moe_dtype o_t, void* ws, hipStream_t s) {
+  const Update u{g, momentum, g_t == MOE_BF16, nesterov, (float)beta, (float)(1.0 - beta), R, K};
+  if (newton_is_small(B, R, K, steps, coef)) return launch_newton_small(u, B, steps, coef, eps, o, o_t, ws, s);
   const NewtonPlan pl = newton_plan(B, R, K, o_t);
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
   const int64_t xs = (int64_t)pl.m * pl.n, gs = (int64_t)pl.m * pl.m;
@@ -439,7 +433,6 @@ moe_status launch_orthogonalize(const void* g, moe_dtype g_t, float* momentum, d
   Planes x = planes(pl.xa, xs), next = planes(pl.xb, xs);
   const Planes gram = planes(pl.gram, gs), poly = planes(pl.poly, gs);
   double* parts = reinterpret_cast<double*>(base + pl.parts);
-  const Update u{g, momentum, g_t == MOE_BF16, nesterov, (float)beta, (float)(1.0 - beta), R, K};
   newton_moment_kernel<<<dim3((unsigned)((int64_t)B * pl.blocks)), 256, 0, s>>>(u, pl.blocks, parts);
   if (moe_status st = check_launch("orthogonalize")) return st;
   const int tr = (int)ceil_div(R, 64), tk = (int)ceil_div(K, 64);

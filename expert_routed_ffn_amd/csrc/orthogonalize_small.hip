@@ -1,0 +1,328 @@
+// orthogonalize_small.hip -- Newton-Schulz steps of matrices whose shorter side m is at most 64 (routers of few experts),
+// in three launches instead of two and three for each step.
+//
+// Every step multiplies X by a polynomial of its Gram matrix, all of them are polynomials of the first one and commute, so
+// they can be gathered on the shorter side: with A = X X^T,
+//   S = b A + c A^2,  P = a I + S,  Q' = P Q = a Q + S Q,  A' = P A P = a^2 A + 2 a S A + S (S A),
+// and o = Q X in the end.  X (m x n) is read twice whatever the number of steps, and one workgroup holds A, S, S A and Q of
+// a matrix in LDS through all of them.
+//
+// What is near 0 in A grows by a^2 a step, 19,800 over the four that matter of five, where X's own steps have 3.44 each, so
+// fp16 terms would not do: A is summed in 64 bits, and the steps run in fp32 for a bf16 result and in 64 bits for an
+// fp32 one.  Random, low-rank and steeply falling matrices are then off by 1e-6 to 7e-4 of their norm (bf16; its rounding is
+// 1.66e-3) and by 1e-12 before an fp32 result's rounding.  Coefficients that grow more than that take 64 bits, or the way
+// of orthogonalize.hip.
+//
+// v_mfma_f32_16x16x4_f32 and v_mfma_f64_16x16x4_f64: lane l holds row l % 16 and k = l / 16 of an operand; of the result
+// column l % 16, rows 4 (l / 16) + i in fp32 and 4 i + l / 16 in 64 bits.
+#include <algorithm>
+#include <cmath>
+
+#include "newton_dev.hpp"
+
+namespace moe {
+namespace {
+
+typedef double f64x4_t __attribute__((ext_vector_type(4)));
+constexpr int kSide = 64, kTiles = 10;  // 16 x 16 tiles on and above the diagonal of a 64 x 64 matrix
+constexpr int kMaxParts = 16;           // workgroups that share a matrix's Gram matrix
+constexpr int kMaxSteps = 16;
+
+template <typename F>
+struct Mat;
+template <>
+struct Mat<float> {
+  typedef f32x4_t Acc;
+  static constexpr int kStride = 68, kLong = 80;  // values per row in LDS: the lanes of a read fall on different banks
+  static __device__ __forceinline__ Acc mma(float a, float b, Acc c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+  static __device__ __forceinline__ int row(int i, int q) { return 4 * q + i; }
+};
+template <>
+struct Mat<double> {
+  typedef f64x4_t Acc;
+  static constexpr int kStride = 66, kLong = 80;
+  static __device__ __forceinline__ Acc mma(double a, double b, Acc c) { return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0); }
+  static __device__ __forceinline__ int row(int i, int q) { return 4 * i + q; }
+};
+
+// Tile number to its place, column by column of the upper triangle.
+__device__ __forceinline__ void tile_at(int t, int& i, int& j) {
+  j = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0;
+  i = t - j * (j + 1) / 2;
+}
+
+// 64 x 64 values of u (rows from r0, columns from k0 on) to v: thread t holds columns 4 (t % 16) of rows t / 16 + 16 i.
+template <bool MOMENT>
+__device__ __forceinline__ void load_tile(const Update& u, int64_t base, int r0, int k0, float (&v)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) load_update<MOMENT>(u, base, r0 + 16 * i + (threadIdx.x >> 4), k0 + (threadIdx.x & 15) * 4, v[i]);
+}
+
+// Parts of the Gram matrices: a workgroup takes `subs` stretches of 64 along the longer side, brings the moment up to
+// date there, and leaves the ten tiles of its sum as its lanes hold them.
+__global__ __launch_bounds__(256) void small_gram_kernel(Update u, int parts, int subs, double* __restrict__ out) {
+  __shared__ float xs[kSide * 80];
+  const int matrix = blockIdx.x / parts, part = blockIdx.x - matrix * parts;
+  const int64_t base = (int64_t)matrix * u.R * u.K;
+  const bool turned = u.R > u.K;
+  const int n = max(u.R, u.K), tiles = (min(u.R, u.K) + 15) / 16;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
+  const int count = tiles * (tiles + 1) / 2;
+  // u lies in LDS as in memory: [short][long] at a stride of 68, or [long][short] at 80
+  const int along_m = turned ? 1 : 68, along_n = turned ? 80 : 1, stride = turned ? 80 : 68;
+  f64x4_t acc[3] = {};
+  float v[4][4];
+  const int first = part * subs, last = min(first + subs, (n + kSide - 1) / kSide);
+  for (int c = first; c < last; ++c) {
+    load_tile<true>(u, base, turned ? c * kSide : 0, turned ? 0 : c * kSide, v);
+    if (c > first) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4*>(xs + (16 * i + (threadIdx.x >> 4)) * stride + (threadIdx.x & 15) * 4) =
+          make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      const int t = wave + 4 * s;
+      if (t >= count) break;
+      int ti, tj;
+      tile_at(t, ti, tj);
+      const float* a = xs + (16 * ti + r) * along_m + q * along_n;
+      const float* b = xs + (16 * tj + r) * along_m + q * along_n;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[s] = Mat<double>::mma(a[4 * k * along_n], b[4 * k * along_n], acc[s]);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    const int t = wave + 4 * s;
+    if (t < count) *reinterpret_cast<f64x4_t*>(out + (((int64_t)blockIdx.x * kTiles + t) * 64 + lane) * 4) = acc[s];
+  }
+}
+
+struct Coefs {
+  float v[3 * kMaxSteps];
+};
+
+// All steps of one matrix: wave t has tile t of the upper triangle of every matrix, and stores it on both sides.  Leaves
+// Q [64][64] (of which the tiles in use are written) and 1 / (norm + eps).
+template <typename F>
+__global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* __restrict__ parts, int count, int tiles,
+                                                                  int steps, Coefs coef, double eps, F* __restrict__ q_out,
+                                                                  double* __restrict__ inv_out) {
+  typedef Mat<F> M;
+  typedef typename M::Acc Acc;
+  constexpr int kS = M::kStride;
+  __shared__ F as[kSide * kS], ss[kSide * kS], ts[kSide * kS], qs[kSide * kS];
+  __shared__ double red[kTiles];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
+  const bool in = wave < tiles * (tiles + 1) / 2;
+  int ti, tj;
+  tile_at(wave, ti, tj);
+  f64x4_t g = {};
+  if (in) {
+    const double* p = parts + (((int64_t)blockIdx.x * count * kTiles + wave) * 64 + lane) * 4;
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) g += *reinterpret_cast<const f64x4_t*>(p + (int64_t)i * kTiles * 256);
+  }
+  double trace = 0.0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (ti == tj && 4 * i + q == r) trace += g[i];
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) trace += __shfl_xor(trace, d);
+  if (lane == 0) red[wave] = trace;
+  __syncthreads();
+  const double inv = inverse_norm((red[0] + red[2]) + (red[5] + red[9]), eps);  // (the tiles on the diagonal)
+  if (threadIdx.x == 0) inv_out[blockIdx.x] = inv;
+
+  auto store = [&](F* to, const Acc& v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * ti + M::row(i, q), col = 16 * tj + r;
+      to[row * kS + col] = v[i];
+      to[col * kS + row] = v[i];
+    }
+  };
+  auto product = [&](const F* x, const F* y) {  // the tile of x y, both symmetric
+    const F* a = x + (16 * ti + r) * kS + q;
+    const F* b = y + (16 * tj + r) * kS + q;
+    Acc acc = {};
+    for (int k = 0; k < 4 * tiles; k += 4) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc = M::mma(a[4 * (k + e)], b[4 * (k + e)], acc);
+    }
+    return acc;
+  };
+  if (in) {  // (the sums are laid out as 64-bit results)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * ti + 4 * i + q, col = 16 * tj + r;
+      const F v = (F)(g[i] * inv * inv);
+      as[row * kS + col] = v;
+      as[col * kS + row] = v;
+    }
+  }
+  __syncthreads();
+  Acc A = {}, Q = {};
+  if (in) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) A[i] = as[(16 * ti + M::row(i, q)) * kS + 16 * tj + r];
+  }
+  for (int k = 0; k < steps; ++k) {
+    const F a = coef.v[3 * k], b = coef.v[3 * k + 1], c = coef.v[3 * k + 2];
+    Acc S = {}, T = {};
+    if (in) {
+      S = product(as, as);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[i] = b * A[i] + c * S[i];
+      store(ss, S);
+    }
+    __syncthreads();
+    if (in) {
+      if (k == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Q[i] = ti == tj && M::row(i, q) == r ? S[i] + a : S[i];
+      } else {
+        const Acc z = product(ss, qs);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Q[i] = a * Q[i] + z[i];
+      }
+    }
+    if (k + 1 == steps) break;
+    if (in) T = product(ss, as);
+    __syncthreads();  // Q's old values have been read
+    if (in) {
+      store(qs, Q);
+      store(ts, T);
+    }
+    __syncthreads();
+    if (in) {
+      const Acc z = product(ss, ts);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) A[i] = a * (a * A[i] + (F)2 * T[i]) + z[i];
+      store(as, A);
+    }
+    __syncthreads();
+  }
+  if (in) {
+    F* to = q_out + (int64_t)blockIdx.x * kSide * kSide;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * ti + M::row(i, q), col = 16 * tj + r;
+      to[row * kSide + col] = Q[i];
+      if (ti != tj) to[col * kSide + row] = Q[i];
+    }
+  }
+}
+
+// o = Q u / (norm + eps), 64 values along the longer side per workgroup; wave w has rows 16 w ... of Q.
+template <typename F>
+__global__ __launch_bounds__(256) void small_apply_kernel(Update u, int chunks, const F* __restrict__ q_in,
+                                                          const double* __restrict__ inv_in, void* o, int o_bf16) {
+  typedef Mat<F> M;
+  constexpr int kS = M::kStride, kL = M::kLong;
+  __shared__ F qs[kSide * kS], xs[kSide * kL];
+  const int matrix = blockIdx.x / chunks, chunk = blockIdx.x - matrix * chunks;
+  const int64_t base = (int64_t)matrix * u.R * u.K;
+  const bool turned = u.R > u.K;
+  const int m = min(u.R, u.K), n = max(u.R, u.K), tiles = (m + 15) / 16;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
+  float v[4][4];
+  load_tile<false>(u, base, turned ? chunk * kSide : 0, turned ? 0 : chunk * kSide, v);
+  const F* from = q_in + (int64_t)matrix * kSide * kSide;
+  for (int i = threadIdx.x; i < 16 * tiles * kSide; i += 256) {
+    const int row = i >> 6, col = i & 63;
+    if (col < 16 * tiles) qs[row * kS + col] = from[i];
+  }
+  const double inv = inv_in[matrix];
+  const int stride = turned ? kS : kL;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      xs[(16 * i + (threadIdx.x >> 4)) * stride + (threadIdx.x & 15) * 4 + e] = (F)((double)v[i][e] * inv);
+  __syncthreads();
+  if (wave >= tiles) return;
+  const int along_m = turned ? 1 : kL, along_n = turned ? kS : 1;
+  typename M::Acc acc[4] = {};
+  const F* a = qs + (16 * wave + r) * kS + q;
+  const F* b = xs + q * along_m + r * along_n;
+  for (int k = 0; k < 4 * tiles; ++k) {
+    const F x = a[4 * k];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = M::mma(x, b[4 * k * along_m + 16 * j * along_n], acc[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * wave + M::row(i, q), col = chunk * kSide + 16 * j + r;
+      if (row < m && col < n)
+        store_any(o, o_bf16, base + (turned ? (int64_t)col * u.K + row : (int64_t)row * u.K + col), (float)acc[j][i]);
+    }
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+struct SmallPlan {
+  int chunks, parts, subs;  // stretches of 64; workgroups that share a Gram matrix, and the stretches of each
+  size_t gram, q, inv, bytes;
+};
+SmallPlan small_plan(int64_t B, int R, int K) {
+  SmallPlan p{};
+  p.chunks = (int)ceil_div(std::max(R, K), kSide);
+  p.subs = (int)ceil_div(p.chunks, kMaxParts);
+  p.parts = (int)ceil_div(p.chunks, p.subs);
+  size_t o = 0;
+  p.gram = o; o = up256(o + (size_t)B * p.parts * kTiles * 256 * 8);
+  p.q = o; o = up256(o + (size_t)B * kSide * kSide * 8);
+  p.inv = o; o = up256(o + (size_t)B * 8);
+  p.bytes = o;
+  return p;
+}
+
+// What the smallest eigenvalues of A may grow by before the last step uses them.
+double growth(int steps, const float* coef) {
+  double g = 1.0;
+  for (int i = 0; i + 1 < steps; ++i) g *= std::max(1.0, (double)coef[3 * i] * coef[3 * i]);
+  return g;
+}
+constexpr double kGrowth32 = 32768.0, kGrowth64 = 268435456.0;  // times 2^-24 and 2^-53: 2e-3 and 3e-8
+constexpr int kSmallMost = 1024;  // matrices, one workgroup each
+
+}  // namespace
+
+bool newton_is_small(int B, int R, int K, int steps, const float* coef) {
+  return std::min(R, K) <= kSide && B <= kSmallMost && (!coef || growth(steps, coef) <= kGrowth64);
+}
+
+size_t newton_small_ws_bytes(int B, int R, int K) {
+  return std::min(R, K) <= kSide && B <= kSmallMost ? small_plan(B, R, K).bytes : 0;
+}
+
+moe_status launch_newton_small(const Update& u, int B, int steps, const float* coef, double eps, void* o, moe_dtype o_t,
+                               void* ws, hipStream_t s) {
+  const SmallPlan p = small_plan(B, u.R, u.K);
+  uint8_t* base = reinterpret_cast<uint8_t*>(ws);
+  double* gram = reinterpret_cast<double*>(base + p.gram);
+  double* inv = reinterpret_cast<double*>(base + p.inv);
+  const int tiles = (std::min(u.R, u.K) + 15) / 16;
+  Coefs c{};
+  std::copy(coef, coef + 3 * steps, c.v);
+  small_gram_kernel<<<dim3((unsigned)(B * p.parts)), 256, 0, s>>>(u, p.parts, p.subs, gram);
+  if (moe_status st = check_launch("orthogonalize")) return st;
+  const dim3 all((unsigned)((int64_t)B * p.chunks));
+  auto go = [&](auto zero) {
+    using F = decltype(zero);
+    F* q = reinterpret_cast<F*>(base + p.q);
+    launch_k(MOE_KERNEL_ORTHOGONALIZE, small_steps_kernel<F>, dim3((unsigned)B), dim3(64 * kTiles), 0, s, gram, p.parts, tiles, steps,
+             c, eps, q, inv);
+    small_apply_kernel<F><<<all, 256, 0, s>>>(u, p.chunks, q, inv, o, o_t == MOE_BF16);
+  };
+  if (o_t == MOE_BF16 && growth(steps, coef) <= kGrowth32) go(0.0f);
+  else go(0.0);
+  return check_launch("orthogonalize");
+}
+
+}  // namespace moe

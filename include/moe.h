@@ -546,7 +546,7 @@ moe_status moe_orthogonalize(const void* g, moe_dtype g_t, float* momentum, doub
                              hipStream_t stream);
 
 /* How moe_orthogonalize cuts its work, as moe_linear_form: sides of the square tiles of A and A A, and of the product
- * with X. */
+ * with X (0: the steps run on the shorter side, one workgroup a matrix); with the coefficients of coef == NULL and 5 steps. */
 moe_status moe_orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[2]);
 
 /*

@@ -44,7 +44,9 @@ def _dense(R, K, kind, seed):
     return low / r ** 0.5 + (0.1 * n if kind == "strong" else 0)
 
 
-SIZES = [(1, 1), (1, 50), (50, 1), (3, 5), (16, 16), (60, 137), (64, 64), (65, 63), (129, 40), (100, 300), (257, 200), (200, 321)]
+# the shorter side around 16, 32, 48 and 64 (sums on the shorter side up to there), the longer one around stretches of 64 and
+# the 16 workgroups that share them
+SIZES = [(15, 17), (17, 100), (33, 49), (48, 1025), (49, 64), (64, 1024), (2000, 60), (1, 1), (1, 50), (50, 1), (3, 5), (16, 16), (60, 137), (64, 64), (65, 63), (129, 40), (100, 300), (257, 200), (200, 321)]
 
 
 @pytest.mark.parametrize("R,K", SIZES)
@@ -78,7 +80,7 @@ def test_low_rank_gradients_stay_clean(moe):
 
 
 # (B, R, K, o): tiles of A and P, tiles of P X
-FORMS = [(1, 64, 128, BF16, 64, 64), (2, 190, 130, F32, 64, 64), (24, 515, 130, BF16, 64, 128), (24, 130, 515, F32, 64, 128),
+FORMS = [(1, 64, 128, BF16, 0, 0), (7, 500, 33, F32, 0, 0), (2, 70, 5000, BF16, 64, 64), (2, 190, 130, F32, 64, 64), (24, 515, 130, BF16, 64, 128), (24, 130, 515, F32, 64, 128),
          (2, 4097, 1025, BF16, 64, 256), (2, 1025, 4097, F32, 64, 256), (24, 515, 513, BF16, 128, 64), (24, 513, 515, F32, 128, 64),
          (3, 1100, 1100, BF16, 128, 128), (3, 1101, 1100, F32, 128, 128), (8, 1100, 1100, BF16, 128, 256),
          (24, 700, 512, F32, 128, 256), (8, 1700, 1500, BF16, 256, 128), (8, 1500, 1700, F32, 256, 128),
@@ -184,17 +186,22 @@ def test_coefficients_and_steps(moe):
     _near(moe.orthogonalize(u.cuda(), coef=one, steps=12, o_dtype=F32), u, F32, coef=one, steps=12)
     _near(moe.orthogonalize(u.cuda(), coef=many, steps=3, o_dtype=F32), u, F32, coef=many, steps=3)
     _near(moe.orthogonalize(u.cuda(), coef=many, steps=3), u, BF16, coef=many, steps=3)
+    # more steps of the usual quintic than the sums on the shorter side hold in 32 bits, and than they hold in 64
+    for steps in (6, 7, 9):
+        _near(moe.orthogonalize(u.cuda(), steps=steps, o_dtype=F32), u, F32, steps=steps)
+        _near(moe.orthogonalize(u.cuda(), steps=steps), u, BF16, steps=steps)
     # twelve cubic steps end near an orthogonal matrix
     o = moe.orthogonalize(u.cuda(), coef=one, steps=16, o_dtype=F32).double().cpu()
     assert (o @ o.t() - torch.eye(48, dtype=torch.float64)).abs().max() < 1e-3
 
 
-def test_zero_and_nonfinite_matrices_stay_alone(moe):
-    u = torch.stack([_dense(40, 70, "strong", s) for s in range(6)])
+@pytest.mark.parametrize("R,K", [(40, 70), (70, 90)])
+def test_zero_and_nonfinite_matrices_stay_alone(moe, R, K):
+    u = torch.stack([_dense(R, K, "strong", s) for s in range(6)])
     clean = moe.orthogonalize(u.cuda())
     u[1] = 0.0
     u[2, 3, 5] = float("nan")
-    u[4, 39, 69] = float("inf")
+    u[4, R - 1, K - 1] = float("inf")
     for eps in (1e-7, 0.0):
         o = moe.orthogonalize(u.cuda(), eps=eps)
         assert not o[1].any()
@@ -214,8 +221,8 @@ def test_same_bits_every_time_and_in_a_workspace_of_garbage(moe):
         assert torch.equal(o[1:-1], want) and (o[0] == 7).all() and (o[-1] == 7).all()
 
 
-def test_views_off_alignment(moe):
-    R, K = 37, 51
+@pytest.mark.parametrize("R,K", [(37, 51), (81, 67)])
+def test_views_off_alignment(moe, R, K):
     u = _dense(R, K, "strong", 4)
     big = torch.full((R * K + 2,), 7.0, device="cuda")
     big[1:-1] = u.reshape(-1).cuda()
@@ -237,7 +244,7 @@ def test_no_matrices(moe):
 
 def test_streams_and_graph(moe):
     g = torch.Generator(device="cuda").manual_seed(1)
-    for B, R, K in [(1, 60, 137), (3, 200, 64)]:
+    for B, R, K in [(1, 60, 137), (3, 200, 70)]:
         u = torch.randn((B, R, K), generator=g, device="cuda")
         m0 = torch.randn((B, R, K), generator=g, device="cuda")
         m = m0.clone()

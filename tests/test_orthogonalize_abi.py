@@ -64,7 +64,8 @@ def test_forms():
     form = (ctypes.c_int32 * 2)()
     assert int(L.moe_orthogonalize_form(1, 64, 64, I8, form)) == EINVAL
     assert int(L.moe_orthogonalize_form(1, 64, 64, BF16, None)) == EINVAL
-    assert m.orthogonalize_form(1, 60, 544) == {"gram": 64, "apply": 64}
+    assert m.orthogonalize_form(1, 60, 544) == {"gram": 0, "apply": 0}
+    assert m.orthogonalize_form(1, 544, 65) == {"gram": 64, "apply": 64}
 
 
 def _t(*shape, dtype=torch.float32):
