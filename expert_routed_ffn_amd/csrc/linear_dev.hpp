@@ -272,9 +272,6 @@ struct Plan {
   int split[2];
 };
 Plan plan_products(const Shape* s, int count);
-// Side of a shape's tiles, and the time in microseconds of a launch of `tiles` whole ones of `steps` K-steps each.
-int shape_side(int shape);
-double tile_cost(int shape, int64_t tiles, int64_t steps);
 int tile_side(const Plan& plan);
 // Launches a forward product (`grad` false, count = 1) or the gradient's (dW first where both are there) with db's sum,
 // then what joins the products' parts.

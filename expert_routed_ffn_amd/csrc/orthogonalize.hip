@@ -343,6 +343,26 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 int up64(int v) { return (v + 63) / 64 * 64; }
 
 constexpr int kSides[4] = {64, 128, 256, 192};
+
+// Time of a launch in microseconds, from traces of 1 to 4,096 tiles of 4 to 64 K-steps: a workgroup costs a start and an
+// epilogue (most of a short reduction's time) and its K-steps, less of each while it has a CU to itself.
+//   P X, 8 K-steps (48 matrices of 512 x 2,048): 128 x 128 tiles 124 us, 256 x 256 114; of 8 matrices 21 and 26, 64 x 64 27
+//   A, 64 K-steps of 4,096 x 4,096: 64 x 64 168 us, 128 x 128 110, 192 x 192 77, 256 x 256 108
+//   A, 32 K-steps of 512 x 2,048: 11.4, 25.8, 33, 58
+struct Rates {
+  int slots;                       // workgroups at once
+  double start, step;              // with the slots taken
+  double start_alone, step_alone;  // up to half of them
+};
+constexpr Rates kSymRates[4] = {{512, 5.0, 0.42, 4.5, 0.19}, {512, 18.0, 1.12, 12.0, 0.43}, {256, 28.0, 1.30, 24.0, 1.07},
+                                {256, 14.0, 1.00, 12.5, 0.65}};
+constexpr Rates kApplyRates[3] = {{512, 3.3, 0.43, 4.2, 0.20}, {512, 13.5, 0.95, 9.0, 0.68}, {256, 25.0, 1.60, 17.0, 1.18}};
+double launch_cost(const Rates& r, int64_t tiles, int64_t steps) {
+  const int64_t whole = tiles / r.slots, rest = tiles % r.slots;
+  const double full = r.start + r.step * steps, alone = r.start_alone + r.step_alone * steps;
+  return whole * full + (rest == 0 ? 0.0 : rest <= r.slots / 2 ? alone : full);
+}
+
 int64_t triangle(int64_t t) { return t * (t + 1) / 2; }
 
 struct NewtonPlan {
@@ -364,11 +384,12 @@ NewtonPlan newton_plan(int64_t B, int R, int K, moe_dtype o_t) {
   const int passes = p.terms == 2 ? 3 : 1;
   for (int i = 0; i < 2; ++i) {
     double least = 0;
-    for (int shape = 0; shape < 3; ++shape) {
+    for (int shape = 0; shape < (i == 0 ? 4 : 3); ++shape) {
       const int64_t tiles = B * newton_tiles(p, i == 0, kSides[shape]);
-      // A's and P's products share a choice: their reductions added
-      const int64_t steps = i == 0 ? (int64_t)passes * (p.n + p.m) / kBK : (int64_t)passes * p.m / kBK;
-      const double c = tile_cost(shape, tiles, steps);
+      // A's and P's products share a choice
+      const double c = i == 0 ? launch_cost(kSymRates[shape], tiles, (int64_t)passes * p.n / kBK) +
+                                    launch_cost(kSymRates[shape], tiles, (int64_t)passes * p.m / kBK)
+                              : launch_cost(kApplyRates[shape], tiles, (int64_t)passes * p.m / kBK);
       if (least == 0 || c < least) {
         least = c;
         p.shape[i] = shape;

@@ -25,7 +25,7 @@ namespace {
 
 typedef double f64x4_t __attribute__((ext_vector_type(4)));
 constexpr int kSide = 64, kTiles = 10;  // 16 x 16 tiles on and above the diagonal of a 64 x 64 matrix
-constexpr int kMaxParts = 16;           // workgroups that share a matrix's Gram matrix
+constexpr int kMaxParts = 32;           // workgroups that share a matrix's Gram matrix
 constexpr int kMaxSteps = 16;
 
 template <typename F>
@@ -73,14 +73,15 @@ __global__ __launch_bounds__(256) void small_gram_kernel(Update u, int parts, in
   f64x4_t acc[3] = {};
   float v[4][4];
   const int first = part * subs, last = min(first + subs, (n + kSide - 1) / kSide);
+  load_tile<true>(u, base, turned ? first * kSide : 0, turned ? 0 : first * kSide, v);
   for (int c = first; c < last; ++c) {
-    load_tile<true>(u, base, turned ? c * kSide : 0, turned ? 0 : c * kSide, v);
     if (c > first) __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<float4*>(xs + (16 * i + (threadIdx.x >> 4)) * stride + (threadIdx.x & 15) * 4) =
           make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
     __syncthreads();
+    if (c + 1 < last) load_tile<true>(u, base, turned ? (c + 1) * kSide : 0, turned ? 0 : (c + 1) * kSide, v);
 #pragma unroll
     for (int s = 0; s < 3; ++s) {
       const int t = wave + 4 * s;
@@ -106,9 +107,9 @@ struct Coefs {
 
 // All steps of one matrix: wave t has tile t of the upper triangle of every matrix, and stores it on both sides.  Leaves
 // Q [64][64] (of which the tiles in use are written) and 1 / (norm + eps).
-template <typename F>
-__global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* __restrict__ parts, int count, int tiles,
-                                                                  int steps, Coefs coef, double eps, F* __restrict__ q_out,
+template <typename F, int TILES>
+__global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* __restrict__ parts, int count, int steps,
+                                                                  Coefs coef, double eps, F* __restrict__ q_out,
                                                                   double* __restrict__ inv_out) {
   typedef Mat<F> M;
   typedef typename M::Acc Acc;
@@ -116,13 +117,13 @@ __global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* 
   __shared__ F as[kSide * kS], ss[kSide * kS], ts[kSide * kS], qs[kSide * kS];
   __shared__ double red[kTiles];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
-  const bool in = wave < tiles * (tiles + 1) / 2;
+  const bool in = wave < TILES * (TILES + 1) / 2;
   int ti, tj;
   tile_at(wave, ti, tj);
   f64x4_t g = {};
   if (in) {
     const double* p = parts + (((int64_t)blockIdx.x * count * kTiles + wave) * 64 + lane) * 4;
-#pragma unroll 4
+#pragma unroll 16
     for (int i = 0; i < count; ++i) g += *reinterpret_cast<const f64x4_t*>(p + (int64_t)i * kTiles * 256);
   }
   double trace = 0.0;
@@ -148,10 +149,8 @@ __global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* 
     const F* a = x + (16 * ti + r) * kS + q;
     const F* b = y + (16 * tj + r) * kS + q;
     Acc acc = {};
-    for (int k = 0; k < 4 * tiles; k += 4) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc = M::mma(a[4 * (k + e)], b[4 * (k + e)], acc);
-    }
+    for (int k = 0; k < 4 * TILES; ++k) acc = M::mma(a[4 * k], b[4 * k], acc);
     return acc;
   };
   if (in) {  // (the sums are laid out as 64-bit results)
@@ -230,12 +229,16 @@ __global__ __launch_bounds__(256) void small_apply_kernel(Update u, int chunks, 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
   float v[4][4];
   load_tile<false>(u, base, turned ? chunk * kSide : 0, turned ? 0 : chunk * kSide, v);
-  const F* from = q_in + (int64_t)matrix * kSide * kSide;
-  for (int i = threadIdx.x; i < 16 * tiles * kSide; i += 256) {
-    const int row = i >> 6, col = i & 63;
-    if (col < 16 * tiles) qs[row * kS + col] = from[i];
-  }
+  typedef F F4 __attribute__((ext_vector_type(4)));
+  const F4* from = reinterpret_cast<const F4*>(q_in + (int64_t)matrix * kSide * kSide);
+  F4 part[4];  // (rows and columns past the tiles in use hold what they held before; nothing reads them)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) part[i] = from[256 * i + threadIdx.x];
   const double inv = inv_in[matrix];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) qs[(16 * i + (threadIdx.x >> 4)) * kS + (threadIdx.x & 15) * 4 + e] = part[i][e];
   const int stride = turned ? kS : kL;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -248,10 +251,13 @@ __global__ __launch_bounds__(256) void small_apply_kernel(Update u, int chunks, 
   typename M::Acc acc[4] = {};
   const F* a = qs + (16 * wave + r) * kS + q;
   const F* b = xs + q * along_m + r * along_n;
-  for (int k = 0; k < 4 * tiles; ++k) {
-    const F x = a[4 * k];
+  for (int t = 0; t < tiles; ++t) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = M::mma(x, b[4 * k * along_m + 16 * j * along_n], acc[j]);
+    for (int k = 4 * t; k < 4 * t + 4; ++k) {
+      const F x = a[4 * k];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] = M::mma(x, b[4 * k * along_m + 16 * j * along_n], acc[j]);
+    }
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -316,8 +322,13 @@ moe_status launch_newton_small(const Update& u, int B, int steps, const float* c
   auto go = [&](auto zero) {
     using F = decltype(zero);
     F* q = reinterpret_cast<F*>(base + p.q);
-    launch_k(MOE_KERNEL_ORTHOGONALIZE, small_steps_kernel<F>, dim3((unsigned)B), dim3(64 * kTiles), 0, s, gram, p.parts, tiles, steps,
-             c, eps, q, inv);
+    auto run = [&](auto kernel) {
+      launch_k(MOE_KERNEL_ORTHOGONALIZE, kernel, dim3((unsigned)B), dim3(64 * kTiles), 0, s, gram, p.parts, steps, c, eps, q, inv);
+    };
+    if (tiles == 1) run(small_steps_kernel<F, 1>);
+    else if (tiles == 2) run(small_steps_kernel<F, 2>);
+    else if (tiles == 3) run(small_steps_kernel<F, 3>);
+    else run(small_steps_kernel<F, 4>);
     small_apply_kernel<F><<<all, 256, 0, s>>>(u, p.chunks, q, inv, o, o_t == MOE_BF16);
   };
   if (o_t == MOE_BF16 && growth(steps, coef) <= kGrowth32) go(0.0f);

@@ -291,14 +291,6 @@ Plan plan_products(const Shape* s, int count) {
   return best;
 }
 
-int shape_side(int shape) { return kRates[shape].side; }
-
-double tile_cost(int shape, int64_t tiles, int64_t steps) {
-  const Rates& r = kRates[shape];
-  const double d = tiles <= r.slots / 2 ? r.start_alone + r.step_alone * steps : r.start + r.step * steps;
-  return 2.0 + d * ceil_div(tiles, r.slots);
-}
-
 int tile_side(const Plan& plan) { return plan.shape == kDirect ? Direct::TM : kRates[plan.shape].side; }
 
 moe_status launch_products(int kid, const Plan& plan, Prob* p, int count, bool grad, bool first_is_dw, const DbSum& db,

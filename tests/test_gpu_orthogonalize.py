@@ -80,11 +80,12 @@ def test_low_rank_gradients_stay_clean(moe):
 
 
 # (B, R, K, o): tiles of A and P, tiles of P X
-FORMS = [(1, 64, 128, BF16, 0, 0), (7, 500, 33, F32, 0, 0), (2, 70, 5000, BF16, 64, 64), (2, 190, 130, F32, 64, 64), (24, 515, 130, BF16, 64, 128), (24, 130, 515, F32, 64, 128),
-         (2, 4097, 1025, BF16, 64, 256), (2, 1025, 4097, F32, 64, 256), (24, 515, 513, BF16, 128, 64), (24, 513, 515, F32, 128, 64),
-         (3, 1100, 1100, BF16, 128, 128), (3, 1101, 1100, F32, 128, 128), (8, 1100, 1100, BF16, 128, 256),
-         (24, 700, 512, F32, 128, 256), (8, 1700, 1500, BF16, 256, 128), (8, 1500, 1700, F32, 256, 128),
-         (24, 1500, 1700, BF16, 256, 256), (24, 1700, 1500, F32, 256, 256)]
+FORMS = [(1, 64, 128, BF16, 0, 0), (7, 500, 33, F32, 0, 0), (2, 70, 5000, BF16, 64, 64), (2, 190, 130, F32, 64, 64),
+         (24, 5000, 70, BF16, 64, 128), (24, 70, 5000, F32, 64, 128), (3, 4097, 1025, BF16, 64, 256), (3, 1025, 4097, F32, 64, 256),
+         (24, 512, 700, BF16, 128, 64), (3, 1100, 1100, BF16, 128, 128), (3, 1101, 1100, F32, 128, 128), (8, 700, 2050, BF16, 128, 256),
+         (8, 2050, 700, F32, 128, 256), (24, 515, 513, BF16, 192, 64), (24, 513, 515, F32, 192, 64), (8, 1100, 1100, BF16, 192, 128),
+         (48, 515, 513, F32, 192, 128), (48, 1030, 700, BF16, 192, 256), (24, 1030, 700, F32, 192, 256), (3, 2500, 2500, BF16, 256, 128),
+         (3, 2500, 2500, F32, 256, 128), (8, 1500, 1700, BF16, 256, 256), (8, 1500, 1700, F32, 256, 256)]
 
 
 def _spread(B, R, K, seed):
