@@ -782,9 +782,9 @@ def orthogonalize_workspace_bytes(B: int, R: int, K: int, o_dtype=torch.bfloat16
 
 def orthogonalize_form(B: int, R: int, K: int, o_dtype=torch.bfloat16) -> dict:
     """How orthogonalize cuts its work at these sizes, for tests and measurements (moe_orthogonalize_form)."""
-    form = (ctypes.c_int32 * 2)()
+    form = (ctypes.c_int32 * 4)()
     _check(lib.moe_orthogonalize_form(B, R, K, *_size_codes("none", o_dtype)[1], form))
-    return dict(zip(("gram", "apply"), form))
+    return dict(zip(("gram", "apply", "gram_paired", "apply_paired"), form))
 
 
 # ---- the dense parts in 8 bits ----------------------------------------------------------

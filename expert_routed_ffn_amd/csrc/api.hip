@@ -608,7 +608,7 @@ moe_status moe_orthogonalize(const void* g, moe_dtype g_t, float* momentum, doub
   return launch_orthogonalize(g, g_t, momentum, beta, nesterov, B, R, K, steps, every, eps, o, o_t, ws, stream);
 }
 
-moe_status moe_orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[2]) {
+moe_status moe_orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[4]) {
   if (moe_status st = check_newton("moe_orthogonalize_form", B, R, K)) return st;
   if (B == 0 || !form) return fail(MOE_EINVAL, "moe_orthogonalize_form: no matrices, or a null pointer");
   if (!is_dtype(o_t)) return fail(MOE_EINVAL, "moe_orthogonalize_form: dtype");

@@ -176,7 +176,7 @@ moe_status launch_linear_backward(const void* dy, moe_dtype dy_t, const void* pr
                                   moe_dtype dw_t, float* db, void* ws, hipStream_t s);
 
 size_t orthogonalize_ws_bytes(int B, int R, int K, moe_dtype o_t);
-void orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[2]);
+void orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[4]);
 moe_status launch_orthogonalize(const void* g, moe_dtype g_t, float* momentum, double beta, int nesterov, int B, int R, int K,
                                 int steps, const float* coef, double eps, void* o, moe_dtype o_t, void* ws, hipStream_t s);
 

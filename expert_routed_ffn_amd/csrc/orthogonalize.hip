@@ -25,6 +25,23 @@ namespace {
 // A tile shape besides those of product_dev.hpp: 192 x 192 (12 waves, 64 x 48 each), for symmetric products whose 256 x 256
 // tiles leave half of the CUs without one.
 using Mid = Tile<192, 192, 3, 4>;
+// Small tiles for launches of few of them, whose time is latency: an epilogue of few values per thread and short ways to
+// it, 76 -> 57 us for all of a 128 x 128 matrix, 104 -> 79 for 512 x 512.  A K-step brings two pieces of each operand: of
+// one term 128 k, of two terms both planes of 64 k, which the three products of the terms then share (1,001 x 777 in two
+// terms: 232 -> 160 us).  Rings of three buffers measured better than longer ones, which leave fewer workgroups to a CU.
+template <typename T, int RING>
+struct Paired : T {
+  static constexpr int kRing = RING, kPair = 2 * T::kStage;  // words of a buffer: A's two pieces, then B's
+  static constexpr int kBuffers = kRing * kPair * 2, kLds = std::max(kBuffers, T::TM * T::TN * 4);
+  static_assert(kBuffers <= 160 * 1024, "LDS of a CU");
+};
+template <typename T>
+struct IsPaired : std::false_type {};
+template <typename T, int RING>
+struct IsPaired<Paired<T, RING>> : std::true_type {};
+using Nano = Paired<Tile<32, 32, 2, 2>, 3>;  // symmetric products
+using Flat = Paired<Tile<32, 64, 2, 2>, 3>;  // P X
+using Wide = Paired<Tile<64, 64, 2, 2, 3, 2>, 3>;
 
 constexpr float kXScale = 8192.0f, kGScale = 4096.0f;  // of X; of A and P
 
@@ -146,6 +163,81 @@ __global__ __launch_bounds__(256) void newton_start_kernel(Update u, int blocks,
   }
 }
 
+// The products of a tile by a Paired shape (see product_loop for the ring): K is a multiple of 64.
+template <typename T, bool BK, int TERMS, typename RowA, typename RowB>
+__device__ __forceinline__ void paired_loop(const Mats& p, int m0, int n0, RowA row_a, RowB row_b, uint8_t* lds,
+                                            f32x4_t (&acc)[T::kFM][T::kFN]) {
+  constexpr int kFM = T::kFM, kFN = T::kFN, WM = T::WM, WN = T::WN, kPieceA = T::kStageA, kPieceB = T::kStage - T::kStageA;
+  const int wave = uniform(threadIdx.x >> 6), kg = wave / (WM * WN), wm = wave / WN % WM, wn = wave % WN;
+  Operand<T::TM, T::kThreads, false> A;
+  Operand<T::TN, T::kThreads, BK> B;
+  A.init(p.lda, p.lda - m0, row_a);
+  B.init(p.ldb, p.ldb - n0, row_b);
+  const int steps = p.K / kBK, phases = TERMS == 2 ? steps : (steps + 1) / 2;
+  uint16_t* const base = reinterpret_cast<uint16_t*>(lds);
+  const int64_t step_a = kBK, step_b = BK ? (int64_t)kBK * p.ldb : kBK;
+  const uint16_t *src_a = A.at(p.A, m0, 0, p.lda), *src_b = B.at(p.B, n0, 0, p.ldb);
+  int next = 0;  // the phase that is loaded next
+  auto load = [&](int buf) {
+    uint16_t* la = base + buf * T::kPair;
+    uint16_t* lb = la + 2 * kPieceA;
+    A.load(src_a, p.lda, la, 64 * wave);
+    B.load(src_b, p.ldb, lb, 64 * wave);
+    // (one term and an odd number of steps: the last has no second piece, and its first one again is not multiplied)
+    const bool pair = TERMS == 2 || 2 * next + 1 < steps;
+    A.load(src_a + (TERMS == 2 ? p.a_plane : pair ? step_a : 0), p.lda, la + kPieceA, 64 * wave);
+    B.load(src_b + (TERMS == 2 ? p.b_plane : pair ? step_b : 0), p.ldb, lb + kPieceB, 64 * wave);
+    if (next + 1 < phases) {  // (past the end the last phase is loaded again, into a buffer that nobody reads)
+      ++next;
+      src_a += (TERMS == 2 ? 1 : 2) * step_a;
+      src_b += (TERMS == 2 ? 1 : 2) * step_b;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kFM; ++i)
+#pragma unroll
+    for (int j = 0; j < kFN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  constexpr int kPer = 2 * (decltype(A)::kLoads + decltype(B)::kLoads), kLeft = (T::kRing - 2) * kPer;
+  static_assert(kLeft < 64, "vmcnt's bits");
+#pragma unroll
+  for (int i = 0; i < T::kRing - 1; ++i) load(i);
+  int now = 0, free = T::kRing - 1;
+  for (int s = 0; s < phases; ++s) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | (kLeft & 15) | (kLeft >> 4) << 14);  // vmcnt(kLeft) lgkmcnt(0): this phase's loads have landed
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    load(free);
+    const uint16_t* la = base + now * T::kPair;
+    const uint16_t* lb = la + 2 * kPieceA;
+#pragma unroll
+    for (int half = 0; half < 2 / T::KG; ++half) {
+      const int kk = T::KG == 2 ? kg : half;
+      bf16x8_t af[2][kFM], bf[2][kFN];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        B.template read<kFN>(lb + w * kPieceB, (T::TN / WN) * wn, kk, bf[w]);
+        A.template read<kFM>(la + w * kPieceA, (T::TM / WM) * wm, kk, af[w]);
+      }
+      auto mma = [&](int x, int y) {
+#pragma unroll
+        for (int i = 0; i < kFM; ++i)
+#pragma unroll
+          for (int j = 0; j < kFN; ++j) acc[i][j] = KindF16::mma(bf[y][j], af[x][i], acc[i][j]);
+      };
+      mma(0, 0);
+      if constexpr (TERMS == 2) {
+        mma(0, 1);
+        mma(1, 0);
+      } else {
+        if (2 * s + 1 < steps) mma(1, 1);
+      }
+    }
+    now = now + 1 == T::kRing ? 0 : now + 1;
+    free = free + 1 == T::kRing ? 0 : free + 1;
+  }
+}
+
 // ---- the steps' products ------------------------------------------------------------------
 
 enum Stage { kGram, kPoly, kApply, kLast };
@@ -188,13 +280,14 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
   }
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int kg = wave / (WM * WN), wm = T::KG == 1 ? wave / WN : wave / WN % WM, wn = wave % WN;
-  // Through LDS, so that loads and stores run along rows: 16-byte pieces, piece c of row m at c ^ (m % 16).
+  // Through LDS, so that loads and stores run along rows: 16-byte pieces, piece c of row m at c ^ (m % 16)
+  // (of 32 columns, m % 8).
   float* tile_c = reinterpret_cast<float*>(lds);
-  constexpr int kPieces = TN / 4, kPassRows = TM / T::kPasses, kStep = kThreads / kPieces;
+  constexpr int kPieces = TN / 4, kTurn = std::min(16, kPieces) - 1, kPassRows = TM / T::kPasses, kStep = kThreads / kPieces;
   // What the epilogue reads is loaded before the products where the registers hold it, else four rows ahead.
   constexpr bool kEarly = STAGE != kGram && TM <= 128;
   constexpr int kAhead = kEarly ? kPassRows / kStep : std::min(4, kPassRows / kStep);
-  static_assert(kThreads % kPieces == 0 && kPassRows % 64 == 0 && 64 % (std::min(4, kAhead) * kStep) == 0, "rows come by 64");
+  static_assert(kThreads % kPieces == 0 && kPassRows % 32 == 0 && kPassRows % (std::min(4, kAhead) * kStep) == 0, "rows come by 64");
   const int r16 = lane & 15, q = lane >> 4;
   const int ld = p.R;
   const uint16_t* in = st.in.p + matrix * st.in.step;
@@ -219,9 +312,10 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
   const int steps = p.K / kBK * p.nseg;
   f32x4_t acc[kFM][kFN];
   // rows past the end read the last one and are not stored
-  product_loop<T, false, !SYM, 0, KindF16>(
-      p, m0, n0, 0, steps, [&](int r) { return min(m0 + r, p.M - 1) - m0; },
-      [&](int r) { return min(n0 + r, p.R - 1) - n0; }, lds, acc);
+  const auto row_a = [&](int r) { return min(m0 + r, p.M - 1) - m0; };
+  const auto row_b = [&](int r) { return min(n0 + r, p.R - 1) - n0; };
+  if constexpr (IsPaired<T>::value) paired_loop<T, !SYM, TERMS>(p, m0, n0, row_a, row_b, lds, acc);
+  else product_loop<T, false, !SYM, 0, KindF16>(p, m0, n0, 0, steps, row_a, row_b, lds, acc);
 
 #pragma unroll
   for (int pass = 0; pass < T::kPasses; ++pass) {
@@ -232,7 +326,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
 #pragma unroll
         for (int j = 0; j < kFN; ++j) {
           const int m = (T::kPasses == 1 ? (TM / WM) * wm : 0) + 16 * i + r16, c = (TN / WN / 4) * wn + 4 * j + q;
-          f32x4_t* at = reinterpret_cast<f32x4_t*>(tile_c + (m * kPieces + (c ^ (m & 15))) * 4);
+          f32x4_t* at = reinterpret_cast<f32x4_t*>(tile_c + (m * kPieces + (c ^ (m & kTurn))) * 4);
           *at = decltype(add)::value ? acc[i][j] + *at : acc[i][j];
         }
     };
@@ -254,7 +348,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
       for (int k = 0; k < kAhead; ++k) {
         const int r = d + k * kStep, m = mp + r;
         if (kEarly && r >= rows) break;
-        float4* at = reinterpret_cast<float4*>(tile_c + (r * kPieces + (o ^ (r & 15))) * 4);
+        float4* at = reinterpret_cast<float4*>(tile_c + (r * kPieces + (o ^ (r & kTurn))) * 4);
         const float4 s = *at;
         const float z[4] = {s.x, s.y, s.z, s.w};
         float h[4], l[4], v[4];
@@ -312,7 +406,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
           float v[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            v[e] = tile_c[((rq + e) * kPieces + ((c >> 2) ^ ((rq + e) & 15))) * 4 + (c & 3)];
+            v[e] = tile_c[((rq + e) * kPieces + ((c >> 2) ^ ((rq + e) & kTurn))) * 4 + (c & 3)];
           if constexpr (STAGE == kLast) {
             if (n0 + c < st.rows) {
               const size_t i = ((size_t)matrix * st.rows + n0 + c) * st.cols + m;
@@ -342,21 +436,30 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 int up64(int v) { return (v + 63) / 64 * 64; }
 
-constexpr int kSides[4] = {64, 128, 256, 192};
+// Shapes; the last two are Mid and Nano in symmetric products, Flat (twice) in P X.
+enum { kTiny, kSmall, kLarge, kWide, kMid, kNano, kShapes };
 
-// Time of a launch in microseconds, from traces of 1 to 4,096 tiles of 4 to 64 K-steps: a workgroup costs a start and an
+// Time of a launch in microseconds, from traces of 1 to 4,096 tiles of 2 to 64 K-steps: a workgroup costs a start and an
 // epilogue (most of a short reduction's time) and its K-steps, less of each while it has a CU to itself.
 //   P X, 8 K-steps (48 matrices of 512 x 2,048): 128 x 128 tiles 124 us, 256 x 256 114; of 8 matrices 21 and 26, 64 x 64 27
 //   A, 64 K-steps of 4,096 x 4,096: 64 x 64 168 us, 128 x 128 110, 192 x 192 77, 256 x 256 108
-//   A, 32 K-steps of 512 x 2,048: 11.4, 25.8, 33, 58
+//   A, 32 K-steps of 512 x 2,048: Nano 7.6 us, 64 x 64 10.5, 128 x 128 25.8
 struct Rates {
-  int slots;                       // workgroups at once
+  int rows, cols, slots;           // of a tile; workgroups at once
   double start, step;              // with the slots taken
   double start_alone, step_alone;  // up to half of them
 };
-constexpr Rates kSymRates[4] = {{512, 5.0, 0.42, 4.5, 0.19}, {512, 18.0, 1.12, 12.0, 0.43}, {256, 28.0, 1.30, 24.0, 1.07},
-                                {256, 14.0, 1.00, 12.5, 0.65}};
-constexpr Rates kApplyRates[3] = {{512, 3.3, 0.43, 4.2, 0.20}, {512, 13.5, 0.95, 9.0, 0.68}, {256, 25.0, 1.60, 17.0, 1.18}};
+// A paired shape's step is 64 k of all terms, by one term and by two; the others take each pass of the terms by itself.
+constexpr Rates kSymRates[2][kShapes] = {
+    {{64, 64, 512, 5.0, 0.42, 4.5, 0.19}, {128, 128, 512, 18.0, 1.12, 12.0, 0.43}, {256, 256, 256, 28.0, 1.30, 24.0, 1.07},
+     {64, 64, 256, 5.4, 0.18, 5.4, 0.18}, {192, 192, 256, 14.0, 1.00, 12.5, 0.65}, {32, 32, 768, 4.5, 0.25, 3.3, 0.13}},
+    {{64, 64, 512, 5.0, 0.42, 4.5, 0.19}, {128, 128, 512, 18.0, 1.12, 12.0, 0.43}, {256, 256, 256, 28.0, 1.30, 24.0, 1.07},
+     {64, 64, 256, 5.4, 0.36, 5.4, 0.36}, {192, 192, 256, 14.0, 1.00, 12.5, 0.65}, {32, 32, 768, 5.5, 0.38, 3.6, 0.20}}};
+constexpr Rates kApplyRates[2][kShapes - 1] = {
+    {{64, 64, 512, 3.3, 0.43, 4.2, 0.20}, {128, 128, 512, 13.5, 0.95, 9.0, 0.68}, {256, 256, 256, 25.0, 1.60, 17.0, 1.18},
+     {64, 64, 256, 3.5, 0.28, 4.0, 0.20}, {32, 64, 512, 3.4, 0.40, 3.4, 0.20}},
+    {{64, 64, 512, 3.3, 0.43, 4.2, 0.20}, {128, 128, 512, 13.5, 0.95, 9.0, 0.68}, {256, 256, 256, 25.0, 1.60, 17.0, 1.18},
+     {64, 64, 256, 4.2, 0.45, 4.2, 0.40}, {32, 64, 512, 3.8, 0.68, 3.8, 0.30}}};
 double launch_cost(const Rates& r, int64_t tiles, int64_t steps) {
   const int64_t whole = tiles / r.slots, rest = tiles % r.slots;
   const double full = r.start + r.step * steps, alone = r.start_alone + r.step_alone * steps;
@@ -371,9 +474,13 @@ struct NewtonPlan {
   int shape[2];       // tile shapes of the symmetric products (A and P alike) and of P X
   size_t xa, xb, gram, poly, diag, parts, bytes;
 };
-int64_t newton_tiles(const NewtonPlan& p, bool sym, int side) {
-  const int64_t tm = ceil_div(p.m, side);
-  return sym ? triangle(tm) : tm * ceil_div(p.n, side);
+const Rates& rates_of(const NewtonPlan& p, bool sym, int shape) {
+  return sym ? kSymRates[p.terms - 1][shape] : kApplyRates[p.terms - 1][std::min(shape, kShapes - 2)];
+}
+int64_t newton_tiles(const NewtonPlan& p, bool sym, int shape) {
+  const Rates& r = rates_of(p, sym, shape);
+  const int64_t tm = ceil_div(p.m, r.rows);
+  return sym ? triangle(tm) : tm * ceil_div(p.n, r.cols);
 }
 NewtonPlan newton_plan(int64_t B, int R, int K, moe_dtype o_t) {
   NewtonPlan p{};
@@ -381,18 +488,17 @@ NewtonPlan newton_plan(int64_t B, int R, int K, moe_dtype o_t) {
   p.n = up64(std::max(R, K));
   p.terms = o_t == MOE_F32 ? 2 : 1;
   p.blocks = (int)std::min<int64_t>(512, ceil_div((int64_t)R * K, 8192));
-  const int passes = p.terms == 2 ? 3 : 1;
-  for (int i = 0; i < 2; ++i) {
+  for (int sym = 0; sym < 2; ++sym) {
     double least = 0;
-    for (int shape = 0; shape < (i == 0 ? 4 : 3); ++shape) {
-      const int64_t tiles = B * newton_tiles(p, i == 0, kSides[shape]);
-      // A's and P's products share a choice
-      const double c = i == 0 ? launch_cost(kSymRates[shape], tiles, (int64_t)passes * p.n / kBK) +
-                                    launch_cost(kSymRates[shape], tiles, (int64_t)passes * p.m / kBK)
-                              : launch_cost(kApplyRates[shape], tiles, (int64_t)passes * p.m / kBK);
+    for (int shape = 0; shape < kShapes - !sym; ++shape) {
+      const Rates& r = rates_of(p, sym, shape);
+      const int64_t tiles = B * newton_tiles(p, sym, shape);
+      const int64_t passes = p.terms == 2 && !(shape == kWide || shape == kNano || (!sym && shape > kWide)) ? 3 : 1;
+      double c = launch_cost(r, tiles, passes * p.m / kBK);
+      if (sym) c += launch_cost(r, tiles, passes * p.n / kBK);  // A's and P's products share a choice
       if (least == 0 || c < least) {
         least = c;
-        p.shape[i] = shape;
+        p.shape[sym ? 0 : 1] = shape;
       }
     }
   }
@@ -411,7 +517,7 @@ NewtonPlan newton_plan(int64_t B, int R, int K, moe_dtype o_t) {
 template <int STAGE>
 moe_status launch_stage(const NewtonPlan& pl, int64_t B, Step st, hipStream_t s) {
   const int shape = pl.shape[STAGE == kGram || STAGE == kPoly ? 0 : 1];
-  st.tiles = (int)newton_tiles(pl, STAGE == kGram || STAGE == kPoly, kSides[shape]);
+  st.tiles = (int)newton_tiles(pl, STAGE == kGram || STAGE == kPoly, shape);
   const dim3 grid((unsigned)(B * st.tiles));
   auto go = [&](auto tile) {
     using T = decltype(tile);
@@ -419,10 +525,12 @@ moe_status launch_stage(const NewtonPlan& pl, int64_t B, Step st, hipStream_t s)
     if (pl.terms == 2) launch_k(MOE_KERNEL_ORTHOGONALIZE, newton_product_kernel<T, STAGE, 2>, grid, threads, 0, s, st);
     else launch_k(MOE_KERNEL_ORTHOGONALIZE, newton_product_kernel<T, STAGE, 1>, grid, threads, 0, s, st);
   };
-  if (shape == 0) go(Tiny{});
-  else if (shape == 1) go(Small{});
-  else if (shape == 2) go(Large{});
-  else if constexpr (STAGE == kGram || STAGE == kPoly) go(Mid{});
+  if (shape == kTiny) go(Tiny{});
+  else if (shape == kSmall) go(Small{});
+  else if (shape == kLarge) go(Large{});
+  else if (shape == kWide) go(Wide{});
+  else if constexpr (STAGE == kGram || STAGE == kPoly) shape == kMid ? go(Mid{}) : go(Nano{});
+  else go(Flat{});
   return check_launch("orthogonalize");
 }
 
@@ -433,14 +541,16 @@ size_t orthogonalize_ws_bytes(int B, int R, int K, moe_dtype o_t) {
   return std::max(newton_plan(B, R, K, o_t).bytes, newton_small_ws_bytes(B, R, K));
 }
 
-void orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[2]) {
+void orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[4]) {
   if (newton_is_small(B, R, K, 5, nullptr)) {
-    form[0] = form[1] = 0;
+    form[0] = form[1] = form[2] = form[3] = 0;
     return;
   }
   const NewtonPlan p = newton_plan(B, R, K, o_t);
-  form[0] = kSides[p.shape[0]];
-  form[1] = kSides[p.shape[1]];
+  form[0] = rates_of(p, true, p.shape[0]).rows;
+  form[1] = rates_of(p, false, p.shape[1]).rows;
+  form[2] = p.shape[0] == kWide || p.shape[0] == kNano;
+  form[3] = p.shape[1] >= kWide;
 }
 
 moe_status launch_orthogonalize(const void* g, moe_dtype g_t, float* momentum, double beta, int nesterov, int B, int R, int K,

@@ -545,9 +545,10 @@ moe_status moe_orthogonalize(const void* g, moe_dtype g_t, float* momentum, doub
                              int steps, const float* coef, double eps, void* o, moe_dtype o_t, void* ws, size_t ws_bytes,
                              hipStream_t stream);
 
-/* How moe_orthogonalize cuts its work, as moe_linear_form: sides of the square tiles of A and A A, and of the product
- * with X (0: the steps run on the shorter side, one workgroup a matrix); with the coefficients of coef == NULL and 5 steps. */
-moe_status moe_orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[2]);
+/* How moe_orthogonalize cuts its work, as moe_linear_form: rows of the tiles of A and A A (form[0]) and of the product
+ * with X (form[1]), 0 where the steps run on the shorter side, one workgroup a matrix; form[2], form[3]: whether a K-step of
+ * theirs brings two pieces of each operand.  With the coefficients of coef == NULL and 5 steps. */
+moe_status moe_orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[4]);
 
 /*
  * Serving the dense parts in 8 bits.

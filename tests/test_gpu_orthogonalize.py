@@ -79,13 +79,16 @@ def test_low_rank_gradients_stay_clean(moe):
     assert _near(moe.orthogonalize(u.cuda(), o_dtype=F32), u, F32) < 2e-4
 
 
-# (B, R, K, o): tiles of A and P, tiles of P X
-FORMS = [(1, 64, 128, BF16, 0, 0), (7, 500, 33, F32, 0, 0), (2, 70, 5000, BF16, 64, 64), (2, 190, 130, F32, 64, 64),
-         (24, 5000, 70, BF16, 64, 128), (24, 70, 5000, F32, 64, 128), (3, 4097, 1025, BF16, 64, 256), (3, 1025, 4097, F32, 64, 256),
-         (24, 512, 700, BF16, 128, 64), (3, 1100, 1100, BF16, 128, 128), (3, 1101, 1100, F32, 128, 128), (8, 700, 2050, BF16, 128, 256),
-         (8, 2050, 700, F32, 128, 256), (24, 515, 513, BF16, 192, 64), (24, 513, 515, F32, 192, 64), (8, 1100, 1100, BF16, 192, 128),
-         (48, 515, 513, F32, 192, 128), (48, 1030, 700, BF16, 192, 256), (24, 1030, 700, F32, 192, 256), (3, 2500, 2500, BF16, 256, 128),
-         (3, 2500, 2500, F32, 256, 128), (8, 1500, 1700, BF16, 256, 256), (8, 1500, 1700, F32, 256, 256)]
+# (B, R, K, o): rows of the tiles of A and P, of P X, and whether their K-steps bring two pieces
+FORMS = [(1, 64, 128, BF16, 0, 0, 0, 0), (7, 500, 33, F32, 0, 0, 0, 0), (1, 190, 130, BF16, 32, 32, 1, 1),
+         (2, 130, 190, F32, 32, 32, 1, 1), (2, 5000, 70, BF16, 32, 64, 1, 0), (2, 70, 5000, F32, 32, 64, 1, 0),
+         (1, 70, 5000, BF16, 32, 64, 1, 1), (1, 5000, 70, F32, 32, 64, 1, 1), (24, 70, 5000, BF16, 32, 128, 1, 0),
+         (24, 5000, 70, F32, 32, 128, 1, 0), (48, 190, 130, BF16, 64, 64, 0, 0), (48, 130, 190, F32, 64, 64, 0, 0),
+         (1, 1000, 12000, BF16, 64, 128, 1, 0), (3, 513, 515, F32, 64, 64, 1, 1), (3, 4097, 1025, BF16, 64, 256, 0, 0), (8, 2050, 700, F32, 64, 256, 1, 0),
+         (24, 700, 512, BF16, 128, 64, 0, 0), (3, 1100, 1100, BF16, 128, 128, 0, 0), (3, 1101, 1100, F32, 128, 128, 0, 0),
+         (8, 700, 2050, BF16, 128, 256, 0, 0), (24, 515, 513, BF16, 192, 64, 0, 0), (24, 513, 515, F32, 192, 64, 0, 0),
+         (8, 1100, 1100, BF16, 192, 128, 0, 0), (48, 1030, 700, BF16, 192, 256, 0, 0), (24, 700, 1030, F32, 192, 256, 0, 0),
+         (4, 2050, 2100, BF16, 256, 128, 0, 0), (8, 1500, 1700, BF16, 256, 256, 0, 0), (8, 1700, 1500, F32, 256, 256, 0, 0)]
 
 
 def _spread(B, R, K, seed):
@@ -120,15 +123,15 @@ def test_places(moe, B, R, K, o_dtype):
     _check_spread(moe, B, R, K, o_dtype, seed=B + R + K)
 
 
-@pytest.mark.parametrize("B,R,K,o_dtype,gram,apply", FORMS)
-def test_places_in_every_form(moe, B, R, K, o_dtype, gram, apply):
+@pytest.mark.parametrize("B,R,K,o_dtype,gram,apply,gram_paired,apply_paired", FORMS)
+def test_places_in_every_form(moe, B, R, K, o_dtype, gram, apply, gram_paired, apply_paired):
     form = moe.orthogonalize_form(B, R, K, o_dtype)
-    assert form["gram"] == gram and form["apply"] == apply, form
+    assert tuple(form.values()) == (gram, apply, gram_paired, apply_paired), form
     _check_spread(moe, B, R, K, o_dtype, seed=R)
 
 
-@pytest.mark.parametrize("B,R,K,o_dtype,gram,apply", FORMS)
-def test_dense_in_every_form(moe, B, R, K, o_dtype, gram, apply):
+@pytest.mark.parametrize("B,R,K,o_dtype", [f[:4] for f in FORMS])
+def test_dense_in_every_form(moe, B, R, K, o_dtype):
     """The last matrix of the batch, against 64-bit products on the GPU."""
     g = torch.Generator(device="cuda").manual_seed(R + K)
     u = torch.randn((B, R, K), generator=g, device="cuda")

@@ -61,11 +61,11 @@ def test_forms():
     for a in [(0, 64, 64), (-1, 64, 64), (1, 0, 64), (1, 64, 16385)]:
         with pytest.raises(m.MoeError):
             m.orthogonalize_form(*a)
-    form = (ctypes.c_int32 * 2)()
+    form = (ctypes.c_int32 * 4)()
     assert int(L.moe_orthogonalize_form(1, 64, 64, I8, form)) == EINVAL
     assert int(L.moe_orthogonalize_form(1, 64, 64, BF16, None)) == EINVAL
-    assert m.orthogonalize_form(1, 60, 544) == {"gram": 0, "apply": 0}
-    assert m.orthogonalize_form(1, 544, 65) == {"gram": 64, "apply": 64}
+    assert m.orthogonalize_form(1, 60, 544) == {"gram": 0, "apply": 0, "gram_paired": 0, "apply_paired": 0}
+    assert m.orthogonalize_form(1, 544, 65) == {"gram": 32, "apply": 32, "gram_paired": 1, "apply_paired": 1}
 
 
 def _t(*shape, dtype=torch.float32):
