@@ -56,7 +56,7 @@ __device__ __forceinline__ void load_update(const Update& u, int64_t base, int r
 }
 
 // Matrices whose shorter side is at most 64: see orthogonalize_small.hip.
-bool newton_is_small(int B, int R, int K, int steps, const float* coef);
+bool newton_is_small(int R, int K, int steps, const float* coef);
 size_t newton_small_ws_bytes(int B, int R, int K);
 moe_status launch_newton_small(const Update& u, int B, int steps, const float* coef, double eps, void* o, moe_dtype o_t,
                                void* ws, hipStream_t s);

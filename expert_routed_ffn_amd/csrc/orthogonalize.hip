@@ -542,7 +542,7 @@ size_t orthogonalize_ws_bytes(int B, int R, int K, moe_dtype o_t) {
 }
 
 void orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[4]) {
-  if (newton_is_small(B, R, K, 5, nullptr)) {
+  if (newton_is_small(R, K, 5, nullptr)) {
     form[0] = form[1] = form[2] = form[3] = 0;
     return;
   }
@@ -556,7 +556,7 @@ void orthogonalize_form(int B, int R, int K, moe_dtype o_t, int32_t form[4]) {
 moe_status launch_orthogonalize(const void* g, moe_dtype g_t, float* momentum, double beta, int nesterov, int B, int R, int K,
                                 int steps, const float* coef, double eps, void* o, moe_dtype o_t, void* ws, hipStream_t s) {
   const Update u{g, momentum, g_t == MOE_BF16, nesterov, (float)beta, (float)(1.0 - beta), R, K};
-  if (newton_is_small(B, R, K, steps, coef)) return launch_newton_small(u, B, steps, coef, eps, o, o_t, ws, s);
+  if (newton_is_small(R, K, steps, coef)) return launch_newton_small(u, B, steps, coef, eps, o, o_t, ws, s);
   const NewtonPlan pl = newton_plan(B, R, K, o_t);
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
   const int64_t xs = (int64_t)pl.m * pl.n, gs = (int64_t)pl.m * pl.m;

@@ -59,8 +59,8 @@ __device__ __forceinline__ void load_tile(const Update& u, int64_t base, int r0,
 }
 
 // Parts of the Gram matrices: a workgroup takes `subs` stretches of 64 along the longer side, brings the moment up to
-// date there, and leaves the ten tiles of its sum as its lanes hold them.
-__global__ __launch_bounds__(256) void small_gram_kernel(Update u, int parts, int subs, double* __restrict__ out) {
+// date there, and leaves the ten tiles of its sum as the lanes of the next kernel hold them.
+__global__ __launch_bounds__(256) void small_gram_kernel(Update u, int parts, int subs, int as_f32, double* __restrict__ out) {
   __shared__ float xs[kSide * 80];
   const int matrix = blockIdx.x / parts, part = blockIdx.x - matrix * parts;
   const int64_t base = (int64_t)matrix * u.R * u.K;
@@ -97,12 +97,56 @@ __global__ __launch_bounds__(256) void small_gram_kernel(Update u, int parts, in
 #pragma unroll
   for (int s = 0; s < 3; ++s) {
     const int t = wave + 4 * s;
-    if (t < count) *reinterpret_cast<f64x4_t*>(out + (((int64_t)blockIdx.x * kTiles + t) * 64 + lane) * 4) = acc[s];
+    if (t >= count) break;
+    double* to = out + ((int64_t)blockIdx.x * kTiles + t) * 256;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[as_f32 ? (16 * i + r) * 4 + q : lane * 4 + i] = acc[s][i];  // row 4 i + q
   }
 }
 
 struct Coefs {
   float v[3 * kMaxSteps];
+};
+
+// A symmetric 64 x 64 matrix in LDS that several waves write tile by tile and multiply.  (fp32 values as three bf16 terms on
+// v_mfma_f32_16x16x32_bf16 need a third of the matrix units' time, but cutting them into terms took as long again.)
+template <typename F>
+struct Held {
+  typedef Mat<F> M;
+  typedef typename M::Acc Acc;
+  static constexpr int kS = M::kStride;
+  F v[kSide * kS] __attribute__((aligned(16)));
+  __device__ __forceinline__ void store(int ti, int tj, const Acc& t) {
+    const int r = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
+    const int col = 16 * tj + r;
+    if constexpr (sizeof(F) == 4) {  // four neighbouring rows
+      *reinterpret_cast<Acc*>(v + col * kS + 16 * ti + 4 * q) = t;
+      if (ti == tj) return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * ti + M::row(i, q);
+      v[row * kS + col] = t[i];
+      if constexpr (sizeof(F) == 8) v[col * kS + row] = t[i];
+    }
+  }
+  // The tile of x y, and with TWO that of x z: x's values are read once, and independent sums follow each other on the
+  // matrix unit.
+  template <int TILES, bool TWO>
+  static __device__ __forceinline__ void products(const Held& x, const Held& y, const Held& z, int ti, int tj, Acc& xy,
+                                                  Acc& xz) {
+    const int r = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
+    const int at = (16 * ti + r) * kS + q, bt = (16 * tj + r) * kS + q;
+    Acc u = {}, w = {};
+#pragma unroll
+    for (int k = 0; k < 4 * TILES; ++k) {
+      const F p = x.v[at + 4 * k];
+      u = M::mma(p, y.v[bt + 4 * k], u);
+      if constexpr (TWO) w = M::mma(p, z.v[bt + 4 * k], w);
+    }
+    xy = u;
+    if constexpr (TWO) xz = w;
+  }
 };
 
 // All steps of one matrix: wave t has tile t of the upper triangle of every matrix, and stores it on both sides.  Leaves
@@ -113,8 +157,7 @@ __global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* 
                                                                   double* __restrict__ inv_out) {
   typedef Mat<F> M;
   typedef typename M::Acc Acc;
-  constexpr int kS = M::kStride;
-  __shared__ F as[kSide * kS], ss[kSide * kS], ts[kSide * kS], qs[kSide * kS];
+  __shared__ Held<F> as, ss, ts, qs;
   __shared__ double red[kTiles];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
   const bool in = wave < TILES * (TILES + 1) / 2;
@@ -123,13 +166,19 @@ __global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* 
   f64x4_t g = {};
   if (in) {
     const double* p = parts + (((int64_t)blockIdx.x * count * kTiles + wave) * 64 + lane) * 4;
-#pragma unroll 16
-    for (int i = 0; i < count; ++i) g += *reinterpret_cast<const f64x4_t*>(p + (int64_t)i * kTiles * 256);
+    for (int first = 0; first < count; first += 8) {
+      f64x4_t v[8];  // (loads past the last part bring it again and are left out)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = *reinterpret_cast<const f64x4_t*>(p + (int64_t)min(first + e, count - 1) * kTiles * 256);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (first + e < count) g += v[e];
+    }
   }
   double trace = 0.0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (ti == tj && 4 * i + q == r) trace += g[i];
+    if (ti == tj && M::row(i, q) == r) trace += g[i];
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) trace += __shfl_xor(trace, d);
   if (lane == 0) red[wave] = trace;
@@ -137,70 +186,48 @@ __global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* 
   const double inv = inverse_norm((red[0] + red[2]) + (red[5] + red[9]), eps);  // (the tiles on the diagonal)
   if (threadIdx.x == 0) inv_out[blockIdx.x] = inv;
 
-  auto store = [&](F* to, const Acc& v) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 16 * ti + M::row(i, q), col = 16 * tj + r;
-      to[row * kS + col] = v[i];
-      to[col * kS + row] = v[i];
-    }
-  };
-  auto product = [&](const F* x, const F* y) {  // the tile of x y, both symmetric
-    const F* a = x + (16 * ti + r) * kS + q;
-    const F* b = y + (16 * tj + r) * kS + q;
-    Acc acc = {};
-#pragma unroll
-    for (int k = 0; k < 4 * TILES; ++k) acc = M::mma(a[4 * k], b[4 * k], acc);
-    return acc;
-  };
-  if (in) {  // (the sums are laid out as 64-bit results)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 16 * ti + 4 * i + q, col = 16 * tj + r;
-      const F v = (F)(g[i] * inv * inv);
-      as[row * kS + col] = v;
-      as[col * kS + row] = v;
-    }
-  }
-  __syncthreads();
   Acc A = {}, Q = {};
   if (in) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) A[i] = as[(16 * ti + M::row(i, q)) * kS + 16 * tj + r];
+    for (int i = 0; i < 4; ++i) A[i] = (F)(g[i] * inv * inv);
+    as.store(ti, tj, A);
   }
+  __syncthreads();
   for (int k = 0; k < steps; ++k) {
     const F a = coef.v[3 * k], b = coef.v[3 * k + 1], c = coef.v[3 * k + 2];
-    Acc S = {}, T = {};
+    Acc S = {}, T = {}, z = {};
     if (in) {
-      S = product(as, as);
+      Held<F>::template products<TILES, false>(as, as, as, ti, tj, S, z);
 #pragma unroll
       for (int i = 0; i < 4; ++i) S[i] = b * A[i] + c * S[i];
-      store(ss, S);
+      ss.store(ti, tj, S);
     }
     __syncthreads();
+    const bool last = k + 1 == steps;
     if (in) {
       if (k == 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) Q[i] = ti == tj && M::row(i, q) == r ? S[i] + a : S[i];
+        if (!last) Held<F>::template products<TILES, false>(ss, as, as, ti, tj, T, z);
       } else {
-        const Acc z = product(ss, qs);
+        if (last) Held<F>::template products<TILES, false>(ss, qs, qs, ti, tj, z, T);
+        else Held<F>::template products<TILES, true>(ss, qs, as, ti, tj, z, T);
 #pragma unroll
         for (int i = 0; i < 4; ++i) Q[i] = a * Q[i] + z[i];
       }
     }
-    if (k + 1 == steps) break;
-    if (in) T = product(ss, as);
+    if (last) break;
     __syncthreads();  // Q's old values have been read
     if (in) {
-      store(qs, Q);
-      store(ts, T);
+      qs.store(ti, tj, Q);
+      ts.store(ti, tj, T);
     }
     __syncthreads();
     if (in) {
-      const Acc z = product(ss, ts);
+      Held<F>::template products<TILES, false>(ss, ts, ts, ti, tj, z, S);
 #pragma unroll
       for (int i = 0; i < 4; ++i) A[i] = a * (a * A[i] + (F)2 * T[i]) + z[i];
-      store(as, A);
+      as.store(ti, tj, A);
     }
     __syncthreads();
   }
@@ -295,16 +322,15 @@ double growth(int steps, const float* coef) {
   return g;
 }
 constexpr double kGrowth32 = 32768.0, kGrowth64 = 268435456.0;  // times 2^-24 and 2^-53: 2e-3 and 3e-8
-constexpr int kSmallMost = 1024;  // matrices, one workgroup each
 
 }  // namespace
 
-bool newton_is_small(int B, int R, int K, int steps, const float* coef) {
-  return std::min(R, K) <= kSide && B <= kSmallMost && (!coef || growth(steps, coef) <= kGrowth64);
+bool newton_is_small(int R, int K, int steps, const float* coef) {
+  return std::min(R, K) <= kSide && (!coef || growth(steps, coef) <= kGrowth64);
 }
 
 size_t newton_small_ws_bytes(int B, int R, int K) {
-  return std::min(R, K) <= kSide && B <= kSmallMost ? small_plan(B, R, K).bytes : 0;
+  return std::min(R, K) <= kSide ? small_plan(B, R, K).bytes : 0;
 }
 
 moe_status launch_newton_small(const Update& u, int B, int steps, const float* coef, double eps, void* o, moe_dtype o_t,
@@ -316,7 +342,8 @@ moe_status launch_newton_small(const Update& u, int B, int steps, const float* c
   const int tiles = (std::min(u.R, u.K) + 15) / 16;
   Coefs c{};
   std::copy(coef, coef + 3 * steps, c.v);
-  small_gram_kernel<<<dim3((unsigned)(B * p.parts)), 256, 0, s>>>(u, p.parts, p.subs, gram);
+  const bool f32 = o_t == MOE_BF16 && growth(steps, coef) <= kGrowth32;
+  small_gram_kernel<<<dim3((unsigned)(B * p.parts)), 256, 0, s>>>(u, p.parts, p.subs, f32, gram);
   if (moe_status st = check_launch("orthogonalize")) return st;
   const dim3 all((unsigned)((int64_t)B * p.chunks));
   auto go = [&](auto zero) {
@@ -331,7 +358,7 @@ moe_status launch_newton_small(const Update& u, int B, int steps, const float* c
     else run(small_steps_kernel<F, 4>);
     small_apply_kernel<F><<<all, 256, 0, s>>>(u, p.chunks, q, inv, o, o_t == MOE_BF16);
   };
-  if (o_t == MOE_BF16 && growth(steps, coef) <= kGrowth32) go(0.0f);
+  if (f32) go(0.0f);
   else go(0.0);
   return check_launch("orthogonalize");
 }
