@@ -121,7 +121,7 @@ def _c(t):
 # T around the switch from few tokens to tiles, from 16 to 32 to 64 tokens, and from coding in the product's launch to
 # one before it; K below, off and on the step of 64 values, and of 128; N below, off and over 8, 16 and the tile
 SHAPES = [(1, 32, 1), (1, 2048, 40), (2, 96, 7), (3, 512, 130), (16, 544, 33), (16, 1024, 9), (5, 4096, 24), (17, 64, 16),
-          (33, 160, 19), (64, 320, 200), (65, 32, 1), (65, 1024, 72), (127, 96, 129), (129, 64, 3), (200, 224, 257),
+          (33, 160, 19), (32, 512, 11), (33, 512, 18), (64, 256, 10), (64, 320, 200), (65, 32, 1), (65, 1024, 72), (127, 96, 129), (129, 64, 3), (200, 224, 257),
           (384, 128, 260)]
 
 

@@ -107,7 +107,8 @@ def test_forms():
     assert int(L.moe_linear_q8_form(100, 64, 64, 0, 3, form)) == EINVAL
     assert int(L.moe_linear_q8_form(100, 64, 64, 0, BF16, None)) == EINVAL
     assert m.linear_q8_form(1, 2048, 512, "swiglu") == {"tile": 0, "parts": 1, "coded_before": 0}
-    assert m.linear_q8_form(64, 64, 64) == {"tile": 0, "parts": 1, "coded_before": 1}
+    assert m.linear_q8_form(64, 256, 64) == {"tile": 0, "parts": 1, "coded_before": 0}
+    assert m.linear_q8_form(64, 288, 64) == {"tile": 0, "parts": 1, "coded_before": 1}
     assert m.linear_q8_form(64, 64, 64, x_dtype=torch.int8)["coded_before"] == 0
     assert m.linear_q8_form(100, 64, 64)["tile"] == 64
 
