@@ -591,6 +591,11 @@ moe_status moe_orthogonalize(const void* g, moe_dtype g_t, float* momentum, doub
   if (!(beta >= 0.0 && beta < 1.0)) return fail(MOE_EINVAL, "moe_orthogonalize: beta outside [0, 1)");
   if (!(eps >= 0.0 && eps < __builtin_huge_val())) return fail(MOE_EINVAL, "moe_orthogonalize: eps");
   if (steps < 1 || steps > kNewtonMaxSteps) return fail(MOE_EUNSUPPORTED, fmt("moe_orthogonalize: steps=%lld outside [1, 16]", steps));
+  float every[3 * kNewtonMaxSteps];
+  for (int i = 0; i < 3 * steps; ++i) {
+    every[i] = coef ? coef[i] : kNewtonCoef[i % 3];
+    if (!__builtin_isfinite(every[i])) return fail(MOE_EINVAL, "moe_orthogonalize: a coefficient is not finite");
+  }
   if (B == 0) return MOE_OK;
   if (!g || !o) return fail(MOE_EINVAL, "moe_orthogonalize: null pointer");
   if (!aligned(g, elem(g_t)) || !aligned(o, elem(o_t)) || !aligned(momentum, 4) || !aligned(ws, 256))
@@ -603,8 +608,6 @@ moe_status moe_orthogonalize(const void* g, moe_dtype g_t, float* momentum, doub
   const Span out[] = {{momentum, n * 4}, {o, n * elem(o_t)}, {ws, need}};
   const Span in[] = {{g, n * elem(g_t)}};
   if (any_overlap(out, in)) return fail(MOE_EINVAL, "moe_orthogonalize: an output or ws overlaps another buffer");
-  float every[3 * kNewtonMaxSteps];
-  for (int i = 0; i < 3 * steps; ++i) every[i] = coef ? coef[i] : kNewtonCoef[i % 3];
   return launch_orthogonalize(g, g_t, momentum, beta, nesterov, B, R, K, steps, every, eps, o, o_t, ws, stream);
 }
 

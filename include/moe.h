@@ -528,7 +528,7 @@ moe_status moe_linear_backward_form(int T, int K, int N, moe_act act, moe_dtype 
  * Each step takes a singular value s to a s + b s^3 + c s^5 and leaves the singular vectors as they are.
  *   g         [B x R x K], dtype g_t; 1 <= R, K <= 16384.
  *   momentum  NULL or [B x R x K] fp32, in and out.     0 <= beta < 1; eps >= 0, finite.
- *   steps     1 ... 16.   coef  host: [steps x 3], NULL: (3.4445, -4.7750, 2.0315) in every step; read before the
+ *   steps     1 ... 16.   coef  host: [steps x 3], finite; NULL: (3.4445, -4.7750, 2.0315) in every step; read before the
  *             call returns.  Singular values may not pass 8 on the way (values past that become infinite or NaN).
  *   o         [B x R x K] out, dtype o_t.
  *   ws        moe_orthogonalize_workspace_bytes(B, R, K, o_t) bytes, 256-byte aligned (0 for sizes and types that the call

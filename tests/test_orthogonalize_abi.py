@@ -32,7 +32,8 @@ def _call(g=_at(1), g_t=F32, mom=None, beta=0.95, nesterov=1, B=2, R=40, K=60, s
     (dict(eps=NAN), EINVAL), (dict(g=None), EINVAL), (dict(o=None), EINVAL), (dict(g=ODD), EINVAL), (dict(o=ODD), EINVAL),
     (dict(mom=ODD), EINVAL), (dict(ws=ODD), EINVAL), (dict(ws=None), EWS), (dict(nb=1024), EWS),
     (dict(o=_at(1)), EINVAL), (dict(mom=_at(1)), EINVAL), (dict(mom=_at(2)), EINVAL), (dict(ws=_at(1)), EINVAL),
-    (dict(ws=_at(2)), EINVAL), (dict(mom=_at(64)), EINVAL)])
+    (dict(ws=_at(2)), EINVAL), (dict(mom=_at(64)), EINVAL),
+    (dict(coef=(ctypes.c_float * 15)(*([1.0] * 14), NAN)), EINVAL), (dict(coef=(ctypes.c_float * 15)(INF, *([1.0] * 14))), EINVAL)])
 def test_refusals(kw, want):
     assert _call(**kw) == want
     assert b"moe_orthogonalize" in L.moe_last_error()
