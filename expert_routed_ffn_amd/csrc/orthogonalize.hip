@@ -442,6 +442,7 @@ enum { kTiny, kSmall, kLarge, kWide, kMid, kNano, kShapes };
 // Time of a launch in microseconds, from traces of 1 to 4,096 tiles of 2 to 64 K-steps: a workgroup costs a start and an
 // epilogue (most of a short reduction's time) and its K-steps, less of each while it has a CU to itself.
 //   P X, 8 K-steps (48 matrices of 512 x 2,048): 128 x 128 tiles 124 us, 256 x 256 114; of 8 matrices 21 and 26, 64 x 64 27
+//   P X, 5 K-steps (24 matrices of 300 x 700): 64 x 64 18 us, 128 x 128 16 (64 x 128 14, not built)
 //   A, 64 K-steps of 4,096 x 4,096: 64 x 64 168 us, 128 x 128 110, 192 x 192 77, 256 x 256 108
 //   A, 32 K-steps of 512 x 2,048: Nano 7.6 us, 64 x 64 10.5, 128 x 128 25.8
 struct Rates {
@@ -456,9 +457,9 @@ constexpr Rates kSymRates[2][kShapes] = {
     {{64, 64, 512, 5.0, 0.42, 4.5, 0.19}, {128, 128, 512, 18.0, 1.12, 12.0, 0.43}, {256, 256, 256, 28.0, 1.30, 24.0, 1.07},
      {64, 64, 256, 5.4, 0.36, 5.4, 0.36}, {192, 192, 256, 14.0, 1.00, 12.5, 0.65}, {32, 32, 768, 5.5, 0.38, 3.6, 0.20}}};
 constexpr Rates kApplyRates[2][kShapes - 1] = {
-    {{64, 64, 512, 3.3, 0.43, 4.2, 0.20}, {128, 128, 512, 13.5, 0.95, 9.0, 0.68}, {256, 256, 256, 25.0, 1.60, 17.0, 1.18},
+    {{64, 64, 512, 4.3, 0.40, 4.2, 0.20}, {128, 128, 512, 12.5, 0.97, 9.0, 0.68}, {256, 256, 256, 25.0, 1.60, 17.0, 1.18},
      {64, 64, 256, 3.5, 0.28, 4.0, 0.20}, {32, 64, 512, 3.4, 0.40, 3.4, 0.20}},
-    {{64, 64, 512, 3.3, 0.43, 4.2, 0.20}, {128, 128, 512, 13.5, 0.95, 9.0, 0.68}, {256, 256, 256, 25.0, 1.60, 17.0, 1.18},
+    {{64, 64, 512, 4.3, 0.40, 4.2, 0.20}, {128, 128, 512, 12.5, 0.97, 9.0, 0.68}, {256, 256, 256, 25.0, 1.60, 17.0, 1.18},
      {64, 64, 256, 4.2, 0.45, 4.2, 0.40}, {32, 64, 512, 3.8, 0.68, 3.8, 0.30}}};
 double launch_cost(const Rates& r, int64_t tiles, int64_t steps) {
   const int64_t whole = tiles / r.slots, rest = tiles % r.slots;

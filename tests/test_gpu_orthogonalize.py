@@ -85,10 +85,10 @@ FORMS = [(1, 64, 128, BF16, 0, 0, 0, 0), (7, 500, 33, F32, 0, 0, 0, 0), (1, 190,
          (1, 70, 5000, BF16, 32, 64, 1, 1), (1, 5000, 70, F32, 32, 64, 1, 1), (24, 70, 5000, BF16, 32, 128, 1, 0),
          (24, 5000, 70, F32, 32, 128, 1, 0), (48, 190, 130, BF16, 64, 64, 0, 0), (48, 130, 190, F32, 64, 64, 0, 0),
          (1, 1000, 12000, BF16, 64, 128, 1, 0), (3, 513, 515, F32, 64, 64, 1, 1), (3, 4097, 1025, BF16, 64, 256, 0, 0), (8, 2050, 700, F32, 64, 256, 1, 0),
-         (24, 700, 512, BF16, 128, 64, 0, 0), (3, 1100, 1100, BF16, 128, 128, 0, 0), (3, 1101, 1100, F32, 128, 128, 0, 0),
+         (24, 700, 512, BF16, 128, 128, 0, 0), (3, 1100, 1100, BF16, 128, 128, 0, 0), (3, 1101, 1100, F32, 128, 128, 0, 0),
          (8, 700, 2050, BF16, 128, 256, 0, 0), (24, 515, 513, BF16, 192, 64, 0, 0), (24, 513, 515, F32, 192, 64, 0, 0),
-         (8, 1100, 1100, BF16, 192, 128, 0, 0), (48, 1030, 700, BF16, 192, 256, 0, 0), (24, 700, 1030, F32, 192, 256, 0, 0),
-         (4, 2050, 2100, BF16, 256, 128, 0, 0), (8, 1500, 1700, BF16, 256, 256, 0, 0), (8, 1700, 1500, F32, 256, 256, 0, 0)]
+         (8, 1100, 1100, BF16, 192, 128, 0, 0), (48, 1030, 700, BF16, 192, 256, 0, 0), (48, 700, 1030, F32, 192, 256, 0, 0),
+         (4, 2050, 2100, BF16, 256, 128, 0, 0), (24, 1500, 1700, BF16, 256, 256, 0, 0), (8, 1700, 1500, F32, 256, 256, 0, 0)]
 
 
 def _spread(B, R, K, seed):
