@@ -64,6 +64,21 @@ __device__ __forceinline__ void unpack4(uint2 q, float (&v)[4]) {
   v[2] = f16_to_f32(q.y & 0xFFFF); v[3] = f16_to_f32(q.y >> 16);
 }
 
+// P X reads X's first term twice, the second time while the L2 may still hold it, and its second term once, whose loads
+// are therefore marked as not to be kept (16 matrices of 1,024 x 2,048: 1,239 -> 1,202 us; not in launches of few tiles: one of
+// 512 x 2,048 111 -> 113).  What it writes is read by the next launches, from the 256 MB cache where X's terms, old and
+// new, fit there; else its stores are marked, too (48 of 512 x 2,048: 1,164 -> 1,119 us, 100 of 256 x 2,048: 991 -> 964; 24 of
+// 512 x 2,048, which fit: 631 -> 661).
+constexpr size_t kKept = 256u << 20;
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint2 load_once(const uint16_t* p) {
+  const u32x2_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(p));
+  return make_uint2(v.x, v.y);
+}
+__device__ __forceinline__ void store_past(uint16_t* p, uint2 v) {
+  __builtin_nontemporal_store(u32x2_t{v.x, v.y}, reinterpret_cast<u32x2_t*>(p));
+}
+
 // ---- the update and its norm -----------------------------------------------------------
 
 // The moment m = beta m + (1 - beta) g, and per workgroup the sum of u^2.  In 64 bits: squares of fp32 values neither
@@ -240,7 +255,7 @@ __device__ __forceinline__ void paired_loop(const Mats& p, int m0, int n0, RowA 
 
 // ---- the steps' products ------------------------------------------------------------------
 
-enum Stage { kGram, kPoly, kApply, kLast };
+enum Stage { kGram, kPoly, kApply, kApplyPast, kLast };  // kApplyPast: X goes past the caches
 
 struct Step {
   Mats mats;                // of the first matrix
@@ -303,9 +318,9 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
       const int m = first + k * kStep;
       const uint16_t* at = in + (int64_t)(m < p.M ? m : m0) * ld + (cols_in ? n : 0);
       if constexpr (STAGE != kGram) hi[k] = *reinterpret_cast<const uint2*>(at);
-      if constexpr (STAGE == kApply || STAGE == kLast || (STAGE == kPoly && TERMS == 2))
-        lo[k] = *reinterpret_cast<const uint2*>(at + st.in.plane);
-      if constexpr (STAGE == kApply || STAGE == kLast) dg[k] = diag[m < p.M ? m : m0];
+      if constexpr (!SYM || (STAGE == kPoly && TERMS == 2))
+        lo[k] = IsPaired<T>::value ? *reinterpret_cast<const uint2*>(at + st.in.plane) : load_once(at + st.in.plane);
+      if constexpr (!SYM) dg[k] = diag[m < p.M ? m : m0];
     }
   };
   if constexpr (kEarly) ahead(m0 + r0);
@@ -353,7 +368,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
         const float z[4] = {s.x, s.y, s.z, s.w};
         float h[4], l[4], v[4];
         if constexpr (STAGE != kGram) unpack4(hi[k], h);
-        if constexpr (STAGE == kApply || STAGE == kLast || (STAGE == kPoly && TERMS == 2)) unpack4(lo[k], l);
+        if constexpr (!SYM || (STAGE == kPoly && TERMS == 2)) unpack4(lo[k], l);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if constexpr (STAGE == kGram) {
@@ -390,12 +405,17 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
           uint2 a, b;
           terms4(v, a, b);
           uint16_t* to = out + (int64_t)m * ld + n;
-          *reinterpret_cast<uint2*>(to) = a;
-          if constexpr (STAGE == kApply || TERMS == 2) *reinterpret_cast<uint2*>(to + st.out.plane) = b;
+          if constexpr (STAGE == kApplyPast) {
+            store_past(to, a);
+            store_past(to + st.out.plane, b);
+          } else {
+            *reinterpret_cast<uint2*>(to) = a;
+            if constexpr (STAGE == kApply || TERMS == 2) *reinterpret_cast<uint2*>(to + st.out.plane) = b;
+          }
         }
       }
     }
-    if constexpr (STAGE != kApply) {
+    if constexpr (SYM || STAGE == kLast) {
       if (mirrored) {  // the tile's transpose: a thread takes four rows of a column
         hand_over();
         constexpr int kRowPieces = kPassRows / 4;
@@ -595,6 +615,7 @@ moe_status launch_orthogonalize(const void* g, moe_dtype g_t, float* momentum, d
     st.a_step = a.step;
     st.b_step = b.step;
   };
+  const bool past = (size_t)B * xs * 8 > kKept;
   for (int i = 0; i < steps; ++i) {
     st.a = coef[3 * i];
     st.b = coef[3 * i + 1];
@@ -610,7 +631,10 @@ moe_status launch_orthogonalize(const void* g, moe_dtype g_t, float* momentum, d
     operands(poly, pl.m, x, pl.n, pl.n, pl.m);
     st.in = x;
     st.out = next;
-    if (moe_status e = i + 1 < steps ? launch_stage<kApply>(pl, B, st, s) : launch_stage<kLast>(pl, B, st, s)) return e;
+    if (moe_status e = i + 1 == steps ? launch_stage<kLast>(pl, B, st, s)
+                       : past         ? launch_stage<kApplyPast>(pl, B, st, s)
+                                      : launch_stage<kApply>(pl, B, st, s))
+      return e;
     std::swap(x, next);
   }
   return MOE_OK;
