@@ -13,10 +13,10 @@
 namespace moe {
 namespace {
 
-// A sum times both scales, the smaller first: the sum's magnitude is at least 1 (or it is 0) and no scale is below 2^-126,
-// so nothing is lost below the range, and nothing passes its top that the result would not.  A NaN scale is taken last.
+// A sum times both scales, the one of smaller magnitude first: the sum's magnitude is at least 1 (or it is 0), so nothing is
+// lost below a normal scale's range, and nothing passes its top that the result would not.
 __device__ __forceinline__ float scaled(int sum, float a, float b) {
-  const bool first = a < b;
+  const bool first = fabsf(a) < fabsf(b);
   return (float)sum * (first ? a : b) * (first ? b : a);
 }
 

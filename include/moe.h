@@ -529,13 +529,16 @@ moe_status moe_linear_backward_form(int T, int K, int N, moe_act act, moe_dtype 
  *   g         [B x R x K], dtype g_t; 1 <= R, K <= 16384.
  *   momentum  NULL or [B x R x K] fp32, in and out.     0 <= beta < 1; eps >= 0, finite.
  *   steps     1 ... 16.   coef  host: [steps x 3], finite; NULL: (3.4445, -4.7750, 2.0315) in every step; read before the
- *             call returns.  Singular values may not pass 8 on the way (values past that become infinite or NaN).
+ *             call returns.  On the way no singular value s of X may reach 4, and no b s^2 + c s^4 reach 16 in
+ *             magnitude (infinities or NaN may come of that).
  *   o         [B x R x K] out, dtype o_t.
  *   ws        moe_orthogonalize_workspace_bytes(B, R, K, o_t) bytes, 256-byte aligned (0 for sizes and types that the call
  *             refuses, and for B == 0).
  * momentum, o and ws may not overlap g or each other.  With R and K rounded up to multiples of 64, B * R * K <= 2^33.
- * The norm's sum is 64-bit, all others are fp32.  A bf16 o comes from products of fp16 terms with 11 bits, X held
- * with 22 (result to 2e-3 of its norm before its rounding, with the usual coefficients); an fp32 o from products of 22-bit terms, as near as fp32 arithmetic.
+ * The norm's sum is 64-bit, all others are fp32 or more.  A bf16 o comes from products of fp16 terms with 11 bits, X held
+ * with 22 (to 2e-3 of its norm before its rounding, with the usual coefficients); an fp32 o from products of 22-bit terms, as
+ * near as fp32 arithmetic.  X is held to multiples of 2^-37, so of a u far smaller than eps (|u| < 1e-4 eps), whose o is as
+ * small, fewer digits are right.
  * A matrix of zeros gives zeros when eps == 0, too; one whose u has an infinity or a NaN gives NaN throughout; neither touches the
  * batch's other matrices.  The same bits for the same inputs every time.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE.
@@ -586,7 +589,7 @@ moe_status moe_quantize_rows(const void* x, moe_dtype x_t, int T, int K, int8_t*
  *             (the query answers 0 for sizes and types that the call refuses); it may
  *             not overlap any other buffer.
  * The integer sums are exact; scales, bias, activation and residual are fp32.  A row of x with an
- * infinity or a NaN, and a NaN scale, give NaN (before the residual).  T <= 2^20.  Scales below 2^-126 may be taken as 0.
+ * infinity or a NaN, and a NaN scale, give NaN (before the residual).  T <= 2^20.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE.
  */
 size_t moe_linear_q8_workspace_bytes(int T, int K, int N, moe_act act, moe_dtype x_t);

@@ -208,6 +208,21 @@ def test_scales_far_apart(moe, T):
             within(y, ref, 4 * 2.0 ** -24 * ref.abs() + 2.0 ** -149, f"{a} {b}")
 
 
+@pytest.mark.parametrize("T", [3, 40, 100])
+def test_scales_of_either_sign_and_below_the_normal_range(moe, T):
+    """Scales that a caller made: negative ones, the large ones among them, whose product with a sum passes fp32's range while the
+    result does not; and one below 2^-126, of which fp32 holds multiples of 2^-149, exact beside sums this small."""
+    K, N = 64, 40
+    x, w, sw, _, _ = _inputs(T, K, N, "none", seed=T)
+    qx, sx = codes64(x)
+    for a, b in [(-1e36, 1e-30), (1e36, -1e-30), (-1e36, -1e-30), (-2.0, 0.5), (2.0 ** -140, 2.0 ** 100), (-2.0 ** -140, 2.0 ** 100)]:
+        s, t = torch.full((T,), a), torch.full((N,), b)
+        for p, q in ((s, t), (t.new_full((T,), b), s.new_full((N,), a))):
+            y = moe.linear_q8(qx.cuda(), w.cuda(), q.cuda(), x_scale=p.cuda(), y_dtype=F32)
+            ref, _ = q8_64(qx, p, w, q, None, "none", None)
+            within(y, ref, 4 * 2.0 ** -24 * ref.abs(), f"{a} {b}")
+
+
 @pytest.mark.parametrize("T", [6, 48, 150])
 @pytest.mark.parametrize("xt", [F32, BF16])
 def test_a_nonfinite_row_stays_in_its_row(moe, T, xt):
