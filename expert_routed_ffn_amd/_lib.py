@@ -745,6 +745,18 @@ def linear_backward_form(T: int, K: int, N: int, act: str = "none", dy_dtype=tor
     return dict(zip(("tile", "dw_parts", "dx_parts", "terms"), form))
 
 
+def _newton_coefs(coef, steps: int) -> list:
+    """The coefficients of all steps in a row."""
+    rows = coef.tolist() if hasattr(coef, "tolist") else list(coef)
+    if rows and not hasattr(rows[0], "__len__"):
+        rows = [rows] * max(0, min(steps, 16))  # (the call refuses more steps)
+    elif len(rows) != steps:
+        rows = [()]
+    if any(not hasattr(c, "__len__") or len(c) != 3 for c in rows):
+        raise ValueError(f"coef holds one (a, b, c), or one for each of {steps} steps")
+    return [float(v) for c in rows for v in c]
+
+
 def orthogonalize(g: torch.Tensor, momentum: torch.Tensor | None = None, beta: float = 0.95, nesterov: bool = True,
                   steps: int = 5, coef=None, eps: float = 1e-7, o: torch.Tensor | None = None, o_dtype=None,
                   ws: torch.Tensor | None = None, stream=None):
@@ -763,9 +775,7 @@ def orthogonalize(g: torch.Tensor, momentum: torch.Tensor | None = None, beta: f
     a_m = None if momentum is None else _arg(momentum, "momentum", shape, (_F32,), at)
     a_coef = None
     if coef is not None:
-        flat = [float(v) for c in coef for v in c] if hasattr(coef[0], "__len__") else [float(v) for v in coef] * steps
-        if len(flat) != 3 * steps:
-            raise ValueError(f"coef holds one (a, b, c), or one for each of {steps} steps")
+        flat = _newton_coefs(coef, steps)
         a_coef = (ctypes.c_float * len(flat))(*flat)
     if o is None:
         o = _new(g, shape, o_dtype or _BF16, stream)

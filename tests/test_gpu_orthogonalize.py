@@ -199,6 +199,25 @@ def test_coefficients_and_steps(moe):
     assert (o @ o.t() - torch.eye(48, dtype=torch.float64)).abs().max() < 1e-3
 
 
+@pytest.mark.parametrize("o_dtype", [BF16, F32])
+def test_singular_values_up_to_the_documented_range(moe, o_dtype):
+    """X's singular values to just below 4 and b s^2 + c s^4 to just below 16 on the way, on matrices of one value in each row and
+    column, where A and P hold the squares themselves: they stay finite and as exact as others."""
+    d = torch.tensor([1.0, 0.9, 0.5, 0.1])
+    u = torch.zeros((70, 90))
+    u[[3, 68, 41, 17], [89, 2, 40, 64]] = d
+    n = float(d.double().norm())
+    top = 3.99 * n  # takes the largest value, 1 / n, to 3.99
+    for coef in ([(top, 0.0, 0.0), (0.1, -0.005, 0.0)], [(top, 0.0, 0.0), (-15.0, 1.004, 0.0)],
+                 [(top, 0.0, 0.0), (1.0, -1.004, 0.0)], [(top, 0.0, 0.0), (-15.0, 0.0, 0.063)]):
+        o = moe.orthogonalize(u.cuda(), steps=len(coef), coef=coef, eps=0.0, o_dtype=o_dtype)
+        got = o.cpu()[[3, 68, 41, 17], [89, 2, 40, 64]].double()
+        ref, e = scalar_bound(d, n, o_dtype, steps=len(coef), coef=coef)
+        h = HALF[o_dtype]
+        assert ((got - ref).abs() <= e * (1 + h) + h * ref.abs()).all(), (got, ref)
+        assert int((o != 0).sum()) == 4
+
+
 @pytest.mark.parametrize("R,K", [(40, 70), (70, 90)])
 def test_zero_and_nonfinite_matrices_stay_alone(moe, R, K):
     u = torch.stack([_dense(R, K, "strong", s) for s in range(6)])

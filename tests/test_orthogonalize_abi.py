@@ -85,3 +85,15 @@ def _t(*shape, dtype=torch.float32):
 def test_binding_refusals(call, error, word):
     with pytest.raises(error, match=word):
         call()
+
+
+def test_coefficients_of_the_binding():
+    one, many = (3.0, -2.0, 0.5), [(1.5, -0.5, 0.0), (2.0, -1.5, 0.5)]
+    assert _lib._newton_coefs(one, 3) == [3.0, -2.0, 0.5] * 3
+    assert _lib._newton_coefs(many, 2) == [1.5, -0.5, 0.0, 2.0, -1.5, 0.5]
+    assert _lib._newton_coefs(torch.tensor(many), 2) == _lib._newton_coefs(many, 2)
+    assert _lib._newton_coefs(torch.tensor(one, dtype=torch.float64), 1) == list(one)
+    assert len(_lib._newton_coefs(one, 1 << 30)) == 3 * 16  # the call refuses that many steps before it reads any
+    for coef, steps in [((), 5), ((1.0, 2.0), 5), (many, 3), (many, 1), ([(1.0, 2.0)], 1), ([one, 1.0], 2)]:
+        with pytest.raises(ValueError, match="coef"):
+            _lib._newton_coefs(coef, steps)
