@@ -36,6 +36,9 @@ constexpr int kOwnValues = kFewThreads * kOwnGroups * 8;  // 16,384 of all token
 // LDS.  XT: the activations are codes (0), bf16 (1) or fp32 (2); in the last two every workgroup codes all of them into LDS
 // while its first weights are on their way (each value by one thread, rows' maxima by LDS atomics, whose order does not
 // matter).  Rows of W past R and tokens past T read the last valid one and are not stored.
+//
+// One token of 2,048 -> 512 SwiGLU: 4.0 us, three of 512 -> 2,048 3.8, where the weights' 2.1 and 1.0 MB are 0.4 and 0.2 us
+// of memory: what counts is the launch, one round trip to memory, the codes' two barriers and the join of the waves.
 template <int XT, int TF>
 __global__ __launch_bounds__(kFewThreads) void q8_few_kernel(const void* __restrict__ x, const int8_t* __restrict__ w,
                                                              Scales sc, int T, int K, Epi e) {
@@ -181,6 +184,9 @@ struct ColumnScales {
   }
 };
 
+// 8,192 x 4,096 x 4,096 without an epilogue takes 123 us (2.23 POP/s; a library product of 8,192^3 has 2.0), with SiLU,
+// residual and a bf16 result 144: the epilogue of one workgroup per CU is overlapped by nothing.  8,192 x 2,048 -> 512 SwiGLU on
+// 128 x 128 tiles 23.4 us (1.47 POP/s; two workgroups a CU, one round of them).
 template <typename T, bool PAIR>
 __global__ __launch_bounds__(T::kThreads, 2) void q8_product_kernel(Prob p, Scales sc) {
   constexpr int TM = T::TM, TN = T::TN, WM = T::WM, WN = T::WN, kFM = T::kFM, kFN = T::kFN, kThreads = T::kThreads;

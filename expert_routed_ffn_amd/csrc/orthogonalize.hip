@@ -82,7 +82,7 @@ __device__ __forceinline__ void store_past(uint16_t* p, uint2 v) {
 // ---- the update and its norm -----------------------------------------------------------
 
 // The moment m = beta m + (1 - beta) g, and per workgroup the sum of u^2.  In 64 bits: squares of fp32 values neither
-// overflow nor vanish there.
+// overflow nor vanish there.  48 matrices of 512 x 2,048, bf16 with momentum: 503 MB in 100 us, a copy's rate.
 __global__ __launch_bounds__(256) void newton_moment_kernel(Update u, int blocks, double* __restrict__ parts) {
   __shared__ double red[4];
   const int matrix = blockIdx.x / blocks, block = blockIdx.x - matrix * blocks;
@@ -128,7 +128,8 @@ struct Planes {  // of fp16 terms, `plane` words apart, matrices `step` words ap
   int64_t plane, step;
 };
 
-// X in two terms, padded with zeros, transposed where R > K: a workgroup brings 64 x 64 values of u through LDS.
+// X in two terms, padded with zeros, transposed where R > K: a workgroup brings 64 x 64 values of u through LDS.  The norm has
+// to be known before a value is rounded, so g and the moment are read again: 503 MB in 99 us for the 48 matrices above.
 __global__ __launch_bounds__(256) void newton_start_kernel(Update u, int blocks, const double* __restrict__ parts, double eps,
                                                            int tr, int tk, Planes x, int ld) {
   __shared__ float tile[64][65];
@@ -269,6 +270,11 @@ struct Step {
 };
 
 // One tile of one matrix.  SYM stages compute the tiles on and above the diagonal.
+//
+// What bounds it, per launch: for one 4,096 x 4,096 matrix the matrix units (A 73 us and P 75 on 192 x 192 tiles, 22 x 23 / 2
+// of them in one round, 1.05 PFLOP/s; P X 122 us, 1.13 PFLOP/s) and the epilogue behind them; for 48 of 512 x 2,048 memory in
+// P X (X's terms in and out, 409 MB or more in 105 us) and the tiles' loads out of the L2 in A (45 us, 480 tiles of which each
+// brings 32 KB per K-step); for one of 512 x 2,048 latency (A 6.5 us, P 3.5, P X 5.5, of 17 launches in a row).
 template <typename T, int STAGE, int TERMS>
 __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st) {
   constexpr bool SYM = STAGE == kGram || STAGE == kPoly;

@@ -13,6 +13,9 @@
 // 1.66e-3) and by 1e-12 before an fp32 result's rounding.  Coefficients that grow more than that take 64 bits, or the way
 // of orthogonalize.hip.
 //
+// One 60 x 544 matrix: 4.7 us for its Gram matrix, 19.7 for the steps (34 in 64 bits; one workgroup, whose products, barriers and
+// trips through LDS follow one another) and 4.6 for Q X; by the launches of orthogonalize.hip 74 in all.
+//
 // v_mfma_f32_16x16x4_f32 and v_mfma_f64_16x16x4_f64: lane l holds row l % 16 and k = l / 16 of an operand; of the result
 // column l % 16, rows 4 (l / 16) + i in fp32 and 4 i + l / 16 in 64 bits.
 #include <algorithm>
