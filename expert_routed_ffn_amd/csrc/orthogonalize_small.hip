@@ -7,14 +7,16 @@
 // and o = Q X in the end.  X (m x n) is read twice whatever the number of steps, and one workgroup holds A, S, S A and Q of
 // a matrix in LDS through all of them.
 //
-// What is near 0 in A grows by a^2 a step, 19,800 over the four that matter of five, where X's own steps have 3.44 each, so
-// fp16 terms would not do: A is summed in 64 bits, and the steps run in fp32 for a bf16 result and in 64 bits for an
-// fp32 one.  Random, low-rank and steeply falling matrices are then off by 1e-6 to 7e-4 of their norm (bf16; its rounding is
-// 1.66e-3) and by 1e-12 before an fp32 result's rounding.  Coefficients that grow more than that take 64 bits, or the way
-// of orthogonalize.hip.
+// What is near 0 in A, and the noise beside it, grows by a^2 a step, 19,800 over the four that matter of five, where X's own
+// steps have 3.44 each.  A is therefore summed in 64 bits, and steps run in 64 bits until what they leave grows by no more
+// than 16 in those that follow: two of five for a bf16 result, all for an fp32 one.  On matrices of one or a few strong
+// directions over noise of 0.01 to 1 of them, sides 8 to 64, a bf16 result was then off by 7e-4 of its norm at most before its
+// rounding (1.66e-3); with the first step alone in 64 bits by 6e-3, with none by 6e-2; with three by 1.1e-4, 3 us slower.
+// (Tiles are stored on both sides of the diagonal, so products that should commute leave their noise on A.)  Coefficients
+// whose growth 64 bits do not hold go the way of orthogonalize.hip.
 //
-// One 60 x 544 matrix: 4.7 us for its Gram matrix, 19.7 for the steps (34 in 64 bits; one workgroup, whose products, barriers and
-// trips through LDS follow one another) and 4.6 for Q X; by the launches of orthogonalize.hip 74 in all.
+// One 60 x 544 matrix: 4.8 us for its Gram matrix, 26.6 for the steps (34 in 64 bits throughout; one workgroup, whose products,
+// barriers and trips through LDS follow one another) and 4.6 for Q X; by the launches of orthogonalize.hip 74 in all.
 //
 // v_mfma_f32_16x16x4_f32 and v_mfma_f64_16x16x4_f64: lane l holds row l % 16 and k = l / 16 of an operand; of the result
 // column l % 16, rows 4 (l / 16) + i in fp32 and 4 i + l / 16 in 64 bits.
@@ -63,7 +65,7 @@ __device__ __forceinline__ void load_tile(const Update& u, int64_t base, int r0,
 
 // Parts of the Gram matrices: a workgroup takes `subs` stretches of 64 along the longer side, brings the moment up to
 // date there, and leaves the ten tiles of its sum as the lanes of the next kernel hold them.
-__global__ __launch_bounds__(256) void small_gram_kernel(Update u, int parts, int subs, int as_f32, double* __restrict__ out) {
+__global__ __launch_bounds__(256) void small_gram_kernel(Update u, int parts, int subs, double* __restrict__ out) {
   __shared__ float xs[kSide * 80];
   const int matrix = blockIdx.x / parts, part = blockIdx.x - matrix * parts;
   const int64_t base = (int64_t)matrix * u.R * u.K;
@@ -103,7 +105,7 @@ __global__ __launch_bounds__(256) void small_gram_kernel(Update u, int parts, in
     if (t >= count) break;
     double* to = out + ((int64_t)blockIdx.x * kTiles + t) * 256;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) to[as_f32 ? (16 * i + r) * 4 + q : lane * 4 + i] = acc[s][i];  // row 4 i + q
+    for (int i = 0; i < 4; ++i) to[lane * 4 + i] = acc[s][i];
   }
 }
 
@@ -152,15 +154,66 @@ struct Held {
   }
 };
 
-// All steps of one matrix: wave t has tile t of the upper triangle of every matrix, and stores it on both sides.  Leaves
-// Q [64][64] (of which the tiles in use are written) and 1 / (norm + eps).
+template <typename F>
+struct Work {  // of the steps, in LDS
+  Held<F> as, ss, ts, qs;
+};
+
+// Steps from ... to - 1 of `steps`: wave t has tile t of the upper triangle of every matrix, and stores it on both sides.  A is
+// in w.as, too, and from the second step on Q in w.qs.
 template <typename F, int TILES>
-__global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* __restrict__ parts, int count, int steps,
-                                                                  Coefs coef, double eps, F* __restrict__ q_out,
-                                                                  double* __restrict__ inv_out) {
+__device__ __forceinline__ void run_steps(Work<F>& w, const Coefs& coef, int from, int to, int steps, bool in, int ti, int tj,
+                                          typename Mat<F>::Acc& A, typename Mat<F>::Acc& Q) {
   typedef Mat<F> M;
   typedef typename M::Acc Acc;
-  __shared__ Held<F> as, ss, ts, qs;
+  const int r = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
+  for (int k = from; k < to; ++k) {
+    const F a = coef.v[3 * k], b = coef.v[3 * k + 1], c = coef.v[3 * k + 2];
+    Acc S = {}, T = {}, z = {};
+    if (in) {
+      Held<F>::template products<TILES, false>(w.as, w.as, w.as, ti, tj, S, z);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[i] = b * A[i] + c * S[i];
+      w.ss.store(ti, tj, S);
+    }
+    __syncthreads();
+    const bool last = k + 1 == steps;
+    if (in) {
+      if (k == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Q[i] = ti == tj && M::row(i, q) == r ? S[i] + a : S[i];
+        if (!last) Held<F>::template products<TILES, false>(w.ss, w.as, w.as, ti, tj, T, z);
+      } else {
+        if (last) Held<F>::template products<TILES, false>(w.ss, w.qs, w.qs, ti, tj, z, T);
+        else Held<F>::template products<TILES, true>(w.ss, w.qs, w.as, ti, tj, z, T);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Q[i] = a * Q[i] + z[i];
+      }
+    }
+    if (last) break;
+    __syncthreads();  // Q's old values have been read
+    if (in) {
+      w.qs.store(ti, tj, Q);
+      w.ts.store(ti, tj, T);
+    }
+    __syncthreads();
+    if (in) {
+      Held<F>::template products<TILES, false>(w.ss, w.ts, w.ts, ti, tj, z, S);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) A[i] = a * (a * A[i] + (F)2 * T[i]) + z[i];
+      w.as.store(ti, tj, A);
+    }
+    __syncthreads();
+  }
+}
+
+// All steps of one matrix, the first `wide` of them in 64 bits.  Leaves Q [64][64] (of which the tiles in use are written) and
+// 1 / (norm + eps).
+template <typename F, int TILES>
+__global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* __restrict__ parts, int count, int steps, int wide,
+                                                                  Coefs coef, double eps, F* __restrict__ q_out,
+                                                                  double* __restrict__ inv_out) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[sizeof(Work<double>)];
   __shared__ double red[kTiles];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
   const bool in = wave < TILES * (TILES + 1) / 2;
@@ -181,7 +234,7 @@ __global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* 
   double trace = 0.0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (ti == tj && M::row(i, q) == r) trace += g[i];
+    if (ti == tj && Mat<double>::row(i, q) == r) trace += g[i];
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) trace += __shfl_xor(trace, d);
   if (lane == 0) red[wave] = trace;
@@ -189,59 +242,44 @@ __global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* 
   const double inv = inverse_norm((red[0] + red[2]) + (red[5] + red[9]), eps);  // (the tiles on the diagonal)
   if (threadIdx.x == 0) inv_out[blockIdx.x] = inv;
 
-  Acc A = {}, Q = {};
+  Work<double>& w = *reinterpret_cast<Work<double>*>(lds);
+  f64x4_t A = {}, Q = {};
   if (in) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) A[i] = (F)(g[i] * inv * inv);
-    as.store(ti, tj, A);
+    A = g * inv * inv;
+    w.as.store(ti, tj, A);
   }
   __syncthreads();
-  for (int k = 0; k < steps; ++k) {
-    const F a = coef.v[3 * k], b = coef.v[3 * k + 1], c = coef.v[3 * k + 2];
-    Acc S = {}, T = {}, z = {};
-    if (in) {
-      Held<F>::template products<TILES, false>(as, as, as, ti, tj, S, z);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) S[i] = b * A[i] + c * S[i];
-      ss.store(ti, tj, S);
-    }
-    __syncthreads();
-    const bool last = k + 1 == steps;
-    if (in) {
-      if (k == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) Q[i] = ti == tj && M::row(i, q) == r ? S[i] + a : S[i];
-        if (!last) Held<F>::template products<TILES, false>(ss, as, as, ti, tj, T, z);
-      } else {
-        if (last) Held<F>::template products<TILES, false>(ss, qs, qs, ti, tj, z, T);
-        else Held<F>::template products<TILES, true>(ss, qs, as, ti, tj, z, T);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) Q[i] = a * Q[i] + z[i];
-      }
-    }
-    if (last) break;
-    __syncthreads();  // Q's old values have been read
-    if (in) {
-      qs.store(ti, tj, Q);
-      ts.store(ti, tj, T);
-    }
-    __syncthreads();
-    if (in) {
-      Held<F>::template products<TILES, false>(ss, ts, ts, ti, tj, z, S);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) A[i] = a * (a * A[i] + (F)2 * T[i]) + z[i];
-      as.store(ti, tj, A);
-    }
-    __syncthreads();
-  }
-  if (in) {
+  run_steps<double, TILES>(w, coef, 0, wide, steps, in, ti, tj, A, Q);
+  auto leave = [&](const auto& tile, auto of) {
     F* to = q_out + (int64_t)blockIdx.x * kSide * kSide;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = 16 * ti + M::row(i, q), col = 16 * tj + r;
-      to[row * kSide + col] = Q[i];
-      if (ti != tj) to[col * kSide + row] = Q[i];
+      const int row = 16 * ti + decltype(of)::row(i, q), col = 16 * tj + r;
+      to[row * kSide + col] = (F)tile[i];
+      if (ti != tj) to[col * kSide + row] = (F)tile[i];
     }
+  };
+  if (sizeof(F) == 8 || wide == steps) {
+    if (in) leave(Q, Mat<double>{});
+  } else if constexpr (sizeof(F) == 4) {  // the lanes hold other rows of an fp32 tile: A and Q come back out of LDS
+    Work<float>& n = *reinterpret_cast<Work<float>*>(lds);
+    f32x4_t an = {}, qn = {};
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = (16 * ti + Mat<float>::row(i, q)) * Held<double>::kS + 16 * tj + r;
+        an[i] = (float)w.as.v[at];
+        qn[i] = wide ? (float)w.qs.v[at] : 0.0f;
+      }
+    }
+    __syncthreads();
+    if (in) {
+      n.as.store(ti, tj, an);
+      n.qs.store(ti, tj, qn);
+    }
+    __syncthreads();
+    run_steps<float, TILES>(n, coef, wide, steps, steps, in, ti, tj, an, qn);
+    if (in) leave(qn, Mat<float>{});
   }
 }
 
@@ -318,18 +356,18 @@ SmallPlan small_plan(int64_t B, int R, int K) {
   return p;
 }
 
-// What the smallest eigenvalues of A may grow by before the last step uses them.
-double growth(int steps, const float* coef) {
+// What A's smallest eigenvalues, and the noise beside them, grow by in steps first ... steps - 2, before the last step uses them.
+double growth(int first, int steps, const float* coef) {
   double g = 1.0;
-  for (int i = 0; i + 1 < steps; ++i) g *= std::max(1.0, (double)coef[3 * i] * coef[3 * i]);
+  for (int i = first; i + 1 < steps; ++i) g *= std::max(1.0, (double)coef[3 * i] * coef[3 * i]);
   return g;
 }
-constexpr double kGrowth32 = 32768.0, kGrowth64 = 268435456.0;  // times 2^-24 and 2^-53: 2e-3 and 3e-8
+constexpr double kGrowth32 = 16.0, kGrowth64 = 268435456.0;
 
 }  // namespace
 
 bool newton_is_small(int R, int K, int steps, const float* coef) {
-  return std::min(R, K) <= kSide && (!coef || growth(steps, coef) <= kGrowth64);
+  return std::min(R, K) <= kSide && (!coef || growth(0, steps, coef) <= kGrowth64);
 }
 
 size_t newton_small_ws_bytes(int B, int R, int K) {
@@ -345,15 +383,17 @@ moe_status launch_newton_small(const Update& u, int B, int steps, const float* c
   const int tiles = (std::min(u.R, u.K) + 15) / 16;
   Coefs c{};
   std::copy(coef, coef + 3 * steps, c.v);
-  const bool f32 = o_t == MOE_BF16 && growth(steps, coef) <= kGrowth32;
-  small_gram_kernel<<<dim3((unsigned)(B * p.parts)), 256, 0, s>>>(u, p.parts, p.subs, f32, gram);
+  int wide = steps;  // steps in 64 bits: all that leave an A whose noise would grow
+  if (o_t == MOE_BF16)
+    while (wide > 0 && growth(wide, steps, coef) <= kGrowth32) --wide;
+  small_gram_kernel<<<dim3((unsigned)(B * p.parts)), 256, 0, s>>>(u, p.parts, p.subs, gram);
   if (moe_status st = check_launch("orthogonalize")) return st;
   const dim3 all((unsigned)((int64_t)B * p.chunks));
   auto go = [&](auto zero) {
     using F = decltype(zero);
     F* q = reinterpret_cast<F*>(base + p.q);
     auto run = [&](auto kernel) {
-      launch_k(MOE_KERNEL_ORTHOGONALIZE, kernel, dim3((unsigned)B), dim3(64 * kTiles), 0, s, gram, p.parts, steps, c, eps, q, inv);
+      launch_k(MOE_KERNEL_ORTHOGONALIZE, kernel, dim3((unsigned)B), dim3(64 * kTiles), 0, s, gram, p.parts, steps, wide, c, eps, q, inv);
     };
     if (tiles == 1) run(small_steps_kernel<F, 1>);
     else if (tiles == 2) run(small_steps_kernel<F, 2>);
@@ -361,7 +401,7 @@ moe_status launch_newton_small(const Update& u, int B, int steps, const float* c
     else run(small_steps_kernel<F, 4>);
     small_apply_kernel<F><<<all, 256, 0, s>>>(u, p.chunks, q, inv, o, o_t == MOE_BF16);
   };
-  if (f32) go(0.0f);
+  if (o_t == MOE_BF16) go(0.0f);
   else go(0.0);
   return check_launch("orthogonalize");
 }

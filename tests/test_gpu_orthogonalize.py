@@ -79,6 +79,23 @@ def test_low_rank_gradients_stay_clean(moe):
     assert _near(moe.orthogonalize(u.cuda(), o_dtype=F32), u, F32) < 2e-4
 
 
+@pytest.mark.parametrize("R,K", [(8, 8), (16, 40), (17, 17), (24, 24), (33, 36), (64, 64), (200, 24), (64, 700), (65, 65), (128, 200)])
+@pytest.mark.parametrize("strong,noise", [(1, 1.0), (1, 0.3), (1, 0.1), (1, 0.03), (1, 0.01), (3, 0.1), (3, 0.01)])
+def test_strong_directions_over_noise(moe, R, K, strong, noise):
+    """What is weak grows most on the way, and noise of the strong directions' size with it.  bf16: with o' the result before its
+    rounding and |o' - ref| <= 2e-3 |ref| as documented; the way from a value to the nearest bf16 changes by no more than the
+    value does, so the rounding adds at most |bf16(ref) - ref| + |o' - ref|.  fp32: newton_bound."""
+    g = _gen(R + K + strong)
+    u = torch.randn((16, R, strong), generator=g) @ torch.randn((16, strong, K), generator=g) / strong ** 0.5
+    u = u + noise * torch.randn((16, R, K), generator=g)
+    o, f = moe.orthogonalize(u.cuda()).double().cpu(), moe.orthogonalize(u.cuda(), o_dtype=F32)
+    for b in range(16):
+        ref = newton64(u[b])
+        most = 2 * 2e-3 * ref.norm() + (ref.to(BF16).double() - ref).norm()
+        assert (o[b] - ref).norm() <= most, (b, float((o[b] - ref).norm() / ref.norm()))
+        _near(f[b], u[b], F32)
+
+
 # (B, R, K, o): rows of the tiles of A and P, of P X, and whether their K-steps bring two pieces
 FORMS = [(1, 64, 128, BF16, 0, 0, 0, 0), (7, 500, 33, F32, 0, 0, 0, 0), (1, 190, 130, BF16, 32, 32, 1, 1),
          (2, 130, 190, F32, 32, 32, 1, 1), (2, 5000, 70, BF16, 32, 64, 1, 0), (2, 70, 5000, F32, 32, 64, 1, 0),
