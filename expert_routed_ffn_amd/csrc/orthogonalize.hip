@@ -81,6 +81,11 @@ __device__ __forceinline__ void store_past(uint16_t* p, uint2 v) {
 
 // ---- the update and its norm -----------------------------------------------------------
 
+// Values that a workgroup of the next kernel has under way at once; up to 2,048 workgroups a matrix.  (With one load of four
+// values a thread at a time and 8,192 values a workgroup 512 x 2,048 took 113 us in all instead of 110, 48 of them 1,128 instead
+// of 1,110, 4,096 x 4,096 1,487 instead of 1,480.)
+constexpr int kNormValues = 2048, kNormBlocks = 2048;
+
 // The moment m = beta m + (1 - beta) g, and per workgroup the sum of u^2.  In 64 bits: squares of fp32 values neither
 // overflow nor vanish there.  48 matrices of 512 x 2,048, bf16 with momentum: 503 MB in 100 us, a copy's rate.
 __global__ __launch_bounds__(256) void newton_moment_kernel(Update u, int blocks, double* __restrict__ parts) {
@@ -88,28 +93,36 @@ __global__ __launch_bounds__(256) void newton_moment_kernel(Update u, int blocks
   const int matrix = blockIdx.x / blocks, block = blockIdx.x - matrix * blocks;
   const int64_t n = (int64_t)u.R * u.K, base = matrix * n;
   double sum = 0.0;
-  for (int64_t i = ((int64_t)block * 256 + threadIdx.x) * 4; i < n; i += (int64_t)blocks * 1024) {
-    float g[4], m[4] = {0.f, 0.f, 0.f, 0.f};
-    if (i + 4 <= n) {
-      load4(u.g, u.g_bf16, base + i, g);
+  for (int64_t first = (int64_t)block * kNormValues; first < n; first += (int64_t)blocks * kNormValues) {
+    if (first + kNormValues <= n) {
+      float g[kNormValues / 1024][4], m[kNormValues / 1024][4] = {};
+      const int64_t at = base + first + threadIdx.x * 4;
+#pragma unroll
+      for (int e = 0; e < kNormValues / 1024; ++e) load4(u.g, u.g_bf16, at + e * 1024, g[e]);
       if (u.moment) {
-        load4(u.moment, 0, base + i, m);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) m[r] = __builtin_fmaf(u.beta, m[r], u.rest * g[r]);
-        store4(u.moment, 0, base + i, m);
+        for (int e = 0; e < kNormValues / 1024; ++e) load4(u.moment, 0, at + e * 1024, m[e]);
+#pragma unroll
+        for (int e = 0; e < kNormValues / 1024; ++e) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) m[e][r] = __builtin_fmaf(u.beta, m[e][r], u.rest * g[e][r]);
+          store4(u.moment, 0, at + e * 1024, m[e]);
+        }
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const double v = update_of(u, g[r], m[r]);
-        sum += v * v;
-      }
+      for (int e = 0; e < kNormValues / 1024; ++e)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const double v = update_of(u, g[e][r], m[e][r]);
+          sum += v * v;
+        }
     } else {
-      for (int r = 0; r < (int)(n - i); ++r) {
-        const float gv = load_any(u.g, u.g_bf16, base + i + r);
+      for (int64_t i = first + threadIdx.x; i < n; i += 256) {
+        const float gv = load_any(u.g, u.g_bf16, base + i);
         float mv = 0.0f;
         if (u.moment) {
-          mv = __builtin_fmaf(u.beta, u.moment[base + i + r], u.rest * gv);
-          u.moment[base + i + r] = mv;
+          mv = __builtin_fmaf(u.beta, u.moment[base + i], u.rest * gv);
+          u.moment[base + i] = mv;
         }
         const double v = update_of(u, gv, mv);
         sum += v * v;
@@ -514,7 +527,7 @@ NewtonPlan newton_plan(int64_t B, int R, int K, moe_dtype o_t) {
   p.m = up64(std::min(R, K));
   p.n = up64(std::max(R, K));
   p.terms = o_t == MOE_F32 ? 2 : 1;
-  p.blocks = (int)std::min<int64_t>(512, ceil_div((int64_t)R * K, 8192));
+  p.blocks = (int)std::min<int64_t>(kNormBlocks, ceil_div((int64_t)R * K, kNormValues));
   for (int sym = 0; sym < 2; ++sym) {
     double least = 0;
     for (int shape = 0; shape < kShapes - !sym; ++shape) {
