@@ -68,7 +68,8 @@ __device__ __forceinline__ void unpack4(uint2 q, float (&v)[4]) {
 // are therefore marked as not to be kept (16 matrices of 1,024 x 2,048: 1,239 -> 1,202 us; not in launches of few tiles: one of
 // 512 x 2,048 111 -> 113).  What it writes is read by the next launches, from the 256 MB cache where X's terms, old and
 // new, fit there; else its stores are marked, too (48 of 512 x 2,048: 1,164 -> 1,119 us, 100 of 256 x 2,048: 991 -> 964; 24 of
-// 512 x 2,048, which fit: 631 -> 661).
+// 512 x 2,048, which fit: 631 -> 661), and it goes through the batch from the back, as A before it has just read the last X (100
+// of 512 x 2,048: 2,306 -> 2,272; where X fits this costs more than it gives, 8 of 512 x 2,048: 255 -> 271).
 constexpr size_t kKept = 256u << 20;
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint2 load_once(const uint16_t* p) {
@@ -87,7 +88,8 @@ __device__ __forceinline__ void store_past(uint16_t* p, uint2 v) {
 constexpr int kNormValues = 2048, kNormBlocks = 2048;
 
 // The moment m = beta m + (1 - beta) g, and per workgroup the sum of u^2.  In 64 bits: squares of fp32 values neither
-// overflow nor vanish there.  48 matrices of 512 x 2,048, bf16 with momentum: 503 MB in 100 us, a copy's rate.
+// overflow nor vanish there.  48 matrices of 512 x 2,048, bf16 with momentum: 503 MB in 74 us (98 at a copy's rate; part of what
+// is written stays in the 256 MB cache).
 __global__ __launch_bounds__(256) void newton_moment_kernel(Update u, int blocks, double* __restrict__ parts) {
   __shared__ double red[4];
   const int matrix = blockIdx.x / blocks, block = blockIdx.x - matrix * blocks;
@@ -142,12 +144,13 @@ struct Planes {  // of fp16 terms, `plane` words apart, matrices `step` words ap
 };
 
 // X in two terms, padded with zeros, transposed where R > K: a workgroup brings 64 x 64 values of u through LDS.  The norm has
-// to be known before a value is rounded, so g and the moment are read again: 503 MB in 99 us for the 48 matrices above.
+// to be known before a value is rounded, so g and the moment are read again: 503 MB in 99 us for the 48 matrices above.  They
+// come from the back, as the caches still hold the last of what the kernel before has read (11 us of 1,106).
 __global__ __launch_bounds__(256) void newton_start_kernel(Update u, int blocks, const double* __restrict__ parts, double eps,
                                                            int tr, int tk, Planes x, int ld) {
   __shared__ float tile[64][65];
   __shared__ double red[4];
-  const int per = tr * tk, matrix = blockIdx.x / per, t = blockIdx.x - matrix * per;
+  const int item = gridDim.x - 1 - blockIdx.x, per = tr * tk, matrix = item / per, t = item - matrix * per;
   const int r0 = t / tk * 64, k0 = t % tk * 64;
   const int64_t base = (int64_t)matrix * u.R * u.K;
   double sum = 0.0;
@@ -293,7 +296,8 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
   constexpr bool SYM = STAGE == kGram || STAGE == kPoly;
   constexpr int TM = T::TM, TN = T::TN, WM = T::WM, WN = T::WN, kFM = T::kFM, kFN = T::kFN, kThreads = T::kThreads;
   __shared__ __attribute__((aligned(16))) uint8_t lds[T::kLds];
-  const int item = die_item(blockIdx.x, gridDim.x);
+  const int forward = die_item(blockIdx.x, gridDim.x);
+  const int item = STAGE == kApplyPast ? (int)gridDim.x - 1 - forward : forward;
   const int matrix = uniform(item / st.tiles), t = uniform(item - matrix * st.tiles);
   Mats p = st.mats;
   p.A += matrix * st.a_step;
