@@ -82,10 +82,10 @@ __device__ __forceinline__ void store_past(uint16_t* p, uint2 v) {
 
 // ---- the update and its norm -----------------------------------------------------------
 
-// Values that a workgroup of the next kernel has under way at once; up to 2,048 workgroups a matrix.  (With one load of four
+// Values that a workgroup of the next kernel has under way at once; up to 1,024 workgroups a matrix.  (With one load of four
 // values a thread at a time and 8,192 values a workgroup 512 x 2,048 took 113 us in all instead of 110, 48 of them 1,128 instead
 // of 1,110, 4,096 x 4,096 1,487 instead of 1,480.)
-constexpr int kNormValues = 2048, kNormBlocks = 2048;
+constexpr int kNormValues = 2048, kNormBlocks = 1024;
 
 // The moment m = beta m + (1 - beta) g, and per workgroup the sum of u^2.  In 64 bits: squares of fp32 values neither
 // overflow nor vanish there.  48 matrices of 512 x 2,048, bf16 with momentum: 503 MB in 74 us (98 at a copy's rate; part of what
