@@ -144,7 +144,7 @@ struct Planes {  // of fp16 terms, `plane` words apart, matrices `step` words ap
 };
 
 // X in two terms, padded with zeros, transposed where R > K: a workgroup brings 64 x 64 values of u through LDS.  The norm has
-// to be known before a value is rounded, so g and the moment are read again: 503 MB in 99 us for the 48 matrices above.  They
+// to be known before a value is rounded, so g and the moment are read again: 503 MB in 94 us for the 48 matrices above.  They
 // come from the back, as the caches still hold the last of what the kernel before has read (11 us of 1,106).
 __global__ __launch_bounds__(256) void newton_start_kernel(Update u, int blocks, const double* __restrict__ parts, double eps,
                                                            int tr, int tk, Planes x, int ld) {
