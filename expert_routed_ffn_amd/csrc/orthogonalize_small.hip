@@ -113,14 +113,14 @@ struct Coefs {
   float v[3 * kMaxSteps];
 };
 
-// A symmetric 64 x 64 matrix in LDS that several waves write tile by tile and multiply.  (fp32 values as three bf16 terms on
+// A symmetric matrix of TILES x TILES tiles in LDS that several waves write tile by tile and multiply.  (fp32 values as three bf16 terms on
 // v_mfma_f32_16x16x32_bf16 need a third of the matrix units' time, but cutting them into terms took as long again.)
-template <typename F>
+template <typename F, int TILES>
 struct Held {
   typedef Mat<F> M;
   typedef typename M::Acc Acc;
   static constexpr int kS = M::kStride;
-  F v[kSide * kS] __attribute__((aligned(16)));
+  F v[16 * TILES * kS] __attribute__((aligned(16)));
   __device__ __forceinline__ void store(int ti, int tj, const Acc& t) {
     const int r = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
     const int col = 16 * tj + r;
@@ -137,7 +137,7 @@ struct Held {
   }
   // The tile of x y, and with TWO that of x z: x's values are read once, and independent sums follow each other on the
   // matrix unit.
-  template <int TILES, bool TWO>
+  template <bool TWO>
   static __device__ __forceinline__ void products(const Held& x, const Held& y, const Held& z, int ti, int tj, Acc& xy,
                                                   Acc& xz) {
     const int r = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
@@ -154,24 +154,25 @@ struct Held {
   }
 };
 
-template <typename F>
+template <typename F, int TILES>
 struct Work {  // of the steps, in LDS
-  Held<F> as, ss, ts, qs;
+  Held<F, TILES> as, ss, ts, qs;
 };
 
 // Steps from ... to - 1 of `steps`: wave t has tile t of the upper triangle of every matrix, and stores it on both sides.  A is
 // in w.as, too, and from the second step on Q in w.qs.
 template <typename F, int TILES>
-__device__ __forceinline__ void run_steps(Work<F>& w, const Coefs& coef, int from, int to, int steps, bool in, int ti, int tj,
+__device__ __forceinline__ void run_steps(Work<F, TILES>& w, const Coefs& coef, int from, int to, int steps, bool in, int ti, int tj,
                                           typename Mat<F>::Acc& A, typename Mat<F>::Acc& Q) {
   typedef Mat<F> M;
   typedef typename M::Acc Acc;
+  typedef Held<F, TILES> H;
   const int r = threadIdx.x & 15, q = (threadIdx.x >> 4) & 3;
   for (int k = from; k < to; ++k) {
     const F a = coef.v[3 * k], b = coef.v[3 * k + 1], c = coef.v[3 * k + 2];
     Acc S = {}, T = {}, z = {};
     if (in) {
-      Held<F>::template products<TILES, false>(w.as, w.as, w.as, ti, tj, S, z);
+      H::template products<false>(w.as, w.as, w.as, ti, tj, S, z);
 #pragma unroll
       for (int i = 0; i < 4; ++i) S[i] = b * A[i] + c * S[i];
       w.ss.store(ti, tj, S);
@@ -182,10 +183,10 @@ __device__ __forceinline__ void run_steps(Work<F>& w, const Coefs& coef, int fro
       if (k == 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) Q[i] = ti == tj && M::row(i, q) == r ? S[i] + a : S[i];
-        if (!last) Held<F>::template products<TILES, false>(w.ss, w.as, w.as, ti, tj, T, z);
+        if (!last) H::template products<false>(w.ss, w.as, w.as, ti, tj, T, z);
       } else {
-        if (last) Held<F>::template products<TILES, false>(w.ss, w.qs, w.qs, ti, tj, z, T);
-        else Held<F>::template products<TILES, true>(w.ss, w.qs, w.as, ti, tj, z, T);
+        if (last) H::template products<false>(w.ss, w.qs, w.qs, ti, tj, z, T);
+        else H::template products<true>(w.ss, w.qs, w.as, ti, tj, z, T);
 #pragma unroll
         for (int i = 0; i < 4; ++i) Q[i] = a * Q[i] + z[i];
       }
@@ -198,7 +199,7 @@ __device__ __forceinline__ void run_steps(Work<F>& w, const Coefs& coef, int fro
     }
     __syncthreads();
     if (in) {
-      Held<F>::template products<TILES, false>(w.ss, w.ts, w.ts, ti, tj, z, S);
+      H::template products<false>(w.ss, w.ts, w.ts, ti, tj, z, S);
 #pragma unroll
       for (int i = 0; i < 4; ++i) A[i] = a * (a * A[i] + (F)2 * T[i]) + z[i];
       w.as.store(ti, tj, A);
@@ -213,7 +214,7 @@ template <typename F, int TILES>
 __global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* __restrict__ parts, int count, int steps, int wide,
                                                                   Coefs coef, double eps, F* __restrict__ q_out,
                                                                   double* __restrict__ inv_out) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[sizeof(Work<double>)];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[sizeof(Work<double, TILES>)];
   __shared__ double red[kTiles];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
   const bool in = wave < TILES * (TILES + 1) / 2;
@@ -242,7 +243,7 @@ __global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* 
   const double inv = inverse_norm((red[0] + red[2]) + (red[5] + red[9]), eps);  // (the tiles on the diagonal)
   if (threadIdx.x == 0) inv_out[blockIdx.x] = inv;
 
-  Work<double>& w = *reinterpret_cast<Work<double>*>(lds);
+  Work<double, TILES>& w = *reinterpret_cast<Work<double, TILES>*>(lds);
   f64x4_t A = {}, Q = {};
   if (in) {
     A = g * inv * inv;
@@ -262,12 +263,12 @@ __global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* 
   if (sizeof(F) == 8 || wide == steps) {
     if (in) leave(Q, Mat<double>{});
   } else if constexpr (sizeof(F) == 4) {  // the lanes hold other rows of an fp32 tile: A and Q come back out of LDS
-    Work<float>& n = *reinterpret_cast<Work<float>*>(lds);
+    Work<float, TILES>& n = *reinterpret_cast<Work<float, TILES>*>(lds);
     f32x4_t an = {}, qn = {};
     if (in) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int at = (16 * ti + Mat<float>::row(i, q)) * Held<double>::kS + 16 * tj + r;
+        const int at = (16 * ti + Mat<float>::row(i, q)) * Held<double, TILES>::kS + 16 * tj + r;
         an[i] = (float)w.as.v[at];
         qn[i] = wide ? (float)w.qs.v[at] : 0.0f;
       }
