@@ -162,7 +162,7 @@ struct Work {  // of the steps, in LDS
 // Steps from ... to - 1 of `steps`: wave t has tile t of the upper triangle of every matrix, and stores it on both sides.  A is
 // in w.as, too, and from the second step on Q in w.qs.
 template <typename F, int TILES>
-__device__ __forceinline__ void run_steps(Work<F, TILES>& w, const Coefs& coef, int from, int to, int steps, bool in, int ti, int tj,
+__device__ __forceinline__ void run_steps(Work<F, TILES>& w, const Coefs& coef, int from, int to, int steps, int ti, int tj,
                                           typename Mat<F>::Acc& A, typename Mat<F>::Acc& Q) {
   typedef Mat<F> M;
   typedef typename M::Acc Acc;
@@ -171,39 +171,31 @@ __device__ __forceinline__ void run_steps(Work<F, TILES>& w, const Coefs& coef, 
   for (int k = from; k < to; ++k) {
     const F a = coef.v[3 * k], b = coef.v[3 * k + 1], c = coef.v[3 * k + 2];
     Acc S = {}, T = {}, z = {};
-    if (in) {
-      H::template products<false>(w.as, w.as, w.as, ti, tj, S, z);
+    H::template products<false>(w.as, w.as, w.as, ti, tj, S, z);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) S[i] = b * A[i] + c * S[i];
-      w.ss.store(ti, tj, S);
-    }
+    for (int i = 0; i < 4; ++i) S[i] = b * A[i] + c * S[i];
+    w.ss.store(ti, tj, S);
     __syncthreads();
     const bool last = k + 1 == steps;
-    if (in) {
-      if (k == 0) {
+    if (k == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) Q[i] = ti == tj && M::row(i, q) == r ? S[i] + a : S[i];
-        if (!last) H::template products<false>(w.ss, w.as, w.as, ti, tj, T, z);
-      } else {
-        if (last) H::template products<false>(w.ss, w.qs, w.qs, ti, tj, z, T);
-        else H::template products<true>(w.ss, w.qs, w.as, ti, tj, z, T);
+      for (int i = 0; i < 4; ++i) Q[i] = ti == tj && M::row(i, q) == r ? S[i] + a : S[i];
+      if (!last) H::template products<false>(w.ss, w.as, w.as, ti, tj, T, z);
+    } else {
+      if (last) H::template products<false>(w.ss, w.qs, w.qs, ti, tj, z, T);
+      else H::template products<true>(w.ss, w.qs, w.as, ti, tj, z, T);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) Q[i] = a * Q[i] + z[i];
-      }
+      for (int i = 0; i < 4; ++i) Q[i] = a * Q[i] + z[i];
     }
     if (last) break;
     __syncthreads();  // Q's old values have been read
-    if (in) {
-      w.qs.store(ti, tj, Q);
-      w.ts.store(ti, tj, T);
-    }
+    w.qs.store(ti, tj, Q);
+    w.ts.store(ti, tj, T);
     __syncthreads();
-    if (in) {
-      H::template products<false>(w.ss, w.ts, w.ts, ti, tj, z, S);
+    H::template products<false>(w.ss, w.ts, w.ts, ti, tj, z, S);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) A[i] = a * (a * A[i] + (F)2 * T[i]) + z[i];
-      w.as.store(ti, tj, A);
-    }
+    for (int i = 0; i < 4; ++i) A[i] = a * (a * A[i] + (F)2 * T[i]) + z[i];
+    w.as.store(ti, tj, A);
     __syncthreads();
   }
 }
@@ -211,26 +203,25 @@ __device__ __forceinline__ void run_steps(Work<F, TILES>& w, const Coefs& coef, 
 // All steps of one matrix, the first `wide` of them in 64 bits.  Leaves Q [64][64] (of which the tiles in use are written) and
 // 1 / (norm + eps).
 template <typename F, int TILES>
-__global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* __restrict__ parts, int count, int steps, int wide,
-                                                                  Coefs coef, double eps, F* __restrict__ q_out,
-                                                                  double* __restrict__ inv_out) {
+__global__ __launch_bounds__(32 * TILES * (TILES + 1)) void small_steps_kernel(const double* __restrict__ parts, int count,
+                                                                                int steps, int wide, Coefs coef, double eps,
+                                                                                F* __restrict__ q_out,
+                                                                                double* __restrict__ inv_out) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[sizeof(Work<double, TILES>)];
-  __shared__ double red[kTiles];
+  constexpr int kWaves = TILES * (TILES + 1) / 2;
+  __shared__ double red[kWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
-  const bool in = wave < TILES * (TILES + 1) / 2;
   int ti, tj;
   tile_at(wave, ti, tj);
   f64x4_t g = {};
-  if (in) {
-    const double* p = parts + (((int64_t)blockIdx.x * count * kTiles + wave) * 64 + lane) * 4;
-    for (int first = 0; first < count; first += 8) {
-      f64x4_t v[8];  // (loads past the last part bring it again and are left out)
+  const double* p = parts + (((int64_t)blockIdx.x * count * kTiles + wave) * 64 + lane) * 4;
+  for (int first = 0; first < count; first += 8) {
+    f64x4_t v[8];  // (loads past the last part bring it again and are left out)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = *reinterpret_cast<const f64x4_t*>(p + (int64_t)min(first + e, count - 1) * kTiles * 256);
+    for (int e = 0; e < 8; ++e) v[e] = *reinterpret_cast<const f64x4_t*>(p + (int64_t)min(first + e, count - 1) * kTiles * 256);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (first + e < count) g += v[e];
-    }
+    for (int e = 0; e < 8; ++e)
+      if (first + e < count) g += v[e];
   }
   double trace = 0.0;
 #pragma unroll
@@ -240,17 +231,18 @@ __global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* 
   for (int d = 32; d > 0; d >>= 1) trace += __shfl_xor(trace, d);
   if (lane == 0) red[wave] = trace;
   __syncthreads();
-  const double inv = inverse_norm((red[0] + red[2]) + (red[5] + red[9]), eps);  // (the tiles on the diagonal)
+  double squares = 0.0;
+#pragma unroll
+  for (int i = 0; i < TILES; ++i) squares += red[i * (i + 3) / 2];  // (the tiles on the diagonal)
+  const double inv = inverse_norm(squares, eps);
   if (threadIdx.x == 0) inv_out[blockIdx.x] = inv;
 
   Work<double, TILES>& w = *reinterpret_cast<Work<double, TILES>*>(lds);
   f64x4_t A = {}, Q = {};
-  if (in) {
-    A = g * inv * inv;
-    w.as.store(ti, tj, A);
-  }
+  A = g * inv * inv;
+  w.as.store(ti, tj, A);
   __syncthreads();
-  run_steps<double, TILES>(w, coef, 0, wide, steps, in, ti, tj, A, Q);
+  run_steps<double, TILES>(w, coef, 0, wide, steps, ti, tj, A, Q);
   auto leave = [&](const auto& tile, auto of) {
     F* to = q_out + (int64_t)blockIdx.x * kSide * kSide;
 #pragma unroll
@@ -261,26 +253,22 @@ __global__ __launch_bounds__(64 * kTiles) void small_steps_kernel(const double* 
     }
   };
   if (sizeof(F) == 8 || wide == steps) {
-    if (in) leave(Q, Mat<double>{});
+    leave(Q, Mat<double>{});
   } else if constexpr (sizeof(F) == 4) {  // the lanes hold other rows of an fp32 tile: A and Q come back out of LDS
     Work<float, TILES>& n = *reinterpret_cast<Work<float, TILES>*>(lds);
     f32x4_t an = {}, qn = {};
-    if (in) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = (16 * ti + Mat<float>::row(i, q)) * Held<double, TILES>::kS + 16 * tj + r;
-        an[i] = (float)w.as.v[at];
-        qn[i] = wide ? (float)w.qs.v[at] : 0.0f;
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int at = (16 * ti + Mat<float>::row(i, q)) * Held<double, TILES>::kS + 16 * tj + r;
+      an[i] = (float)w.as.v[at];
+      qn[i] = wide ? (float)w.qs.v[at] : 0.0f;
     }
     __syncthreads();
-    if (in) {
-      n.as.store(ti, tj, an);
-      n.qs.store(ti, tj, qn);
-    }
+    n.as.store(ti, tj, an);
+    n.qs.store(ti, tj, qn);
     __syncthreads();
-    run_steps<float, TILES>(n, coef, wide, steps, steps, in, ti, tj, an, qn);
-    if (in) leave(qn, Mat<float>{});
+    run_steps<float, TILES>(n, coef, wide, steps, steps, ti, tj, an, qn);
+    leave(qn, Mat<float>{});
   }
 }
 
@@ -394,7 +382,7 @@ moe_status launch_newton_small(const Update& u, int B, int steps, const float* c
     using F = decltype(zero);
     F* q = reinterpret_cast<F*>(base + p.q);
     auto run = [&](auto kernel) {
-      launch_k(MOE_KERNEL_ORTHOGONALIZE, kernel, dim3((unsigned)B), dim3(64 * kTiles), 0, s, gram, p.parts, steps, wide, c, eps, q, inv);
+      launch_k(MOE_KERNEL_ORTHOGONALIZE, kernel, dim3((unsigned)B), dim3((unsigned)(32 * tiles * (tiles + 1))), 0, s, gram, p.parts, steps, wide, c, eps, q, inv);
     };
     if (tiles == 1) run(small_steps_kernel<F, 1>);
     else if (tiles == 2) run(small_steps_kernel<F, 2>);
