@@ -8,12 +8,13 @@
 // a matrix in LDS through all of them.
 //
 // What is near 0 in A, and the noise beside it, grows by a^2 a step, 19,800 over the four that matter of five, where X's own
-// steps have 3.44 each.  A is therefore summed in 64 bits, and steps run in 64 bits until what they leave grows by no more
-// than 16 in those that follow: two of five for a bf16 result, all for an fp32 one.  On matrices of one or a few strong
-// directions over noise of 0.01 to 1 of them, sides 8 to 64, a bf16 result was then off by 7e-4 of its norm at most before its
-// rounding (1.66e-3); with the first step alone in 64 bits by 6e-3, with none by 6e-2; with three by 1.1e-4, 3 us slower.
-// (Tiles are stored on both sides of the diagonal, so products that should commute leave their noise on A.)  Coefficients
-// whose growth 64 bits do not hold go the way of orthogonalize.hip.
+// steps have 3.44 each.  A is therefore summed in 64 bits, and steps run in 64 bits until A's rounding to fp32 grows by no
+// more than 144 in the steps that are left, and what the first fp32 step adds by no more than 16 in those behind it: two of five for
+// a bf16 result, all for an fp32 one.  On matrices of one or a few strong directions over noise of 0.01 to 1 of them, sides 8
+// to 64, a bf16 result was then off by 7e-4 of its norm at most before its rounding (1.66e-3); with the first step alone in 64 bits
+// by 6e-3, with none by 6e-2; with three by 1.1e-4, 3 us slower.  (The bound of 16 alone lets the fp32 steps begin with one of
+// any a: with a = 15 there results were 5e-3 to 2.6e-2 off.  Tiles are stored on both sides of the diagonal, so products that should
+// commute leave their noise on A.)  Coefficients whose growth 64 bits do not hold go the way of orthogonalize.hip.
 //
 // One 60 x 544 matrix: 4.8 us for its Gram matrix, 26.6 for the steps (34 in 64 bits throughout; one workgroup, whose products,
 // barriers and trips through LDS follow one another) and 4.6 for Q X; by the launches of orthogonalize.hip 74 in all.
@@ -351,7 +352,7 @@ double growth(int first, int steps, const float* coef) {
   for (int i = first; i + 1 < steps; ++i) g *= std::max(1.0, (double)coef[3 * i] * coef[3 * i]);
   return g;
 }
-constexpr double kGrowth32 = 16.0, kGrowth64 = 268435456.0;
+constexpr double kGrowthA = 144.0, kGrowthStep = 16.0, kGrowth64 = 268435456.0;
 
 }  // namespace
 
@@ -374,7 +375,7 @@ moe_status launch_newton_small(const Update& u, int B, int steps, const float* c
   std::copy(coef, coef + 3 * steps, c.v);
   int wide = steps;  // steps in 64 bits: all that leave an A whose noise would grow
   if (o_t == MOE_BF16)
-    while (wide > 0 && growth(wide, steps, coef) <= kGrowth32) --wide;
+    while (wide > 0 && growth(wide, steps, coef) <= kGrowthStep && growth(wide - 1, steps, coef) <= kGrowthA) --wide;
   small_gram_kernel<<<dim3((unsigned)(B * p.parts)), 256, 0, s>>>(u, p.parts, p.subs, gram);
   if (moe_status st = check_launch("orthogonalize")) return st;
   const dim3 all((unsigned)((int64_t)B * p.chunks));
