@@ -9,11 +9,14 @@
 // What the roundings do: a step multiplies a small singular value by a = 3.44, five of them by 485, and noise beside
 // it as much, so X rounded to 11 bits before each step leaves results of low-rank gradients 1 to 7% off, and bf16 20%
 // or more.  X is therefore kept as two fp16 terms (22 bits): the sum a X takes both, and only the product P X, whose P is
-// nearly 0 on the weak directions, takes the first alone.  P's diagonal, the largest of its values on matrices of
-// even spectrum, stays in fp32 beside it and enters as diag P X.  On matrices of 65 to 1,024 rows, from even
-// spectra to one strong direction over noise, the result is 0.1 to 1.8e-3 of its norm off, and a bf16 result's own rounding
-// 1.66e-3.  An fp32 result takes two
-// terms of X, A and P in every product (three passes of the matrix units), and is as near as an fp32 computation.
+// nearly 0 on the weak directions, takes the first alone.  The diagonals of A and P, the largest of their values where the spectrum
+// is even or few rows are not 0, stay in fp32 beside them: A^2 = E^2 + D E + E D + D^2, E off the diagonal D, and
+// diag P X.  (With A's diagonal in 11 bits, too, gradients of a few rows were up to 6e-3 off; in fp32 it costs 0.5 to 2%.)
+// The result is 0.1 to 1.2e-3 of its norm off on matrices of 128 to 4,096 rows from Gaussian ones to one strong direction
+// over noise, 1.2 to 1.9e-3 where few rows are not 0, 0.9 to 2.5e-3 where all singular values are equal; a bf16
+// result's own rounding is 1.66e-3.  Matrices of one value in each row and column, whose roundings do not average out, come to
+// 7e-3 where the values are equal and to 1.8e-2 with two or three of the worst sizes.  An fp32 result takes two terms of X,
+// A and P in every product (three passes of the matrix units), and is as near as an fp32 computation.
 //
 // A and P are symmetric: only tiles on and above the diagonal are computed, and stored twice.  All matrices of a
 // call share each launch.  m and n are padded to multiples of 64 with zeros, which stay zeros.
@@ -280,7 +283,8 @@ struct Step {
   int64_t a_step, b_step;   // words from one matrix to the next
   int tiles;                // per matrix
   Planes in, out;           // kPoly: A -> P;  kApply: X -> X;  kGram: -> A;  kLast: X
-  float* diag;              // [matrix][M] P's diagonal: written by kPoly, read by kApply and kLast
+  float* gram_diag;         // [matrix][M] A's diagonal (0 in its planes): written by kGram, read by kPoly
+  float* diag;              // [matrix][M] P's diagonal (0 in its planes): written by kPoly, read by kApply and kLast
   float a, b, c;
   void* o;                  // kLast: [matrix][rows][cols], where X is [cols][rows] if `turned`
   int o_bf16, turned, rows, cols;
@@ -331,11 +335,14 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
   const int ld = p.R;
   const uint16_t* in = st.in.p + matrix * st.in.step;
   uint16_t* out = st.out.p + matrix * st.out.step;
+  float* gram_diag = st.gram_diag + (int64_t)matrix * p.M;
   float* diag = st.diag + (int64_t)matrix * p.M;
   const int o = tid % kPieces, n = n0 + 4 * o, r0 = tid / kPieces;
   const bool cols_in = n < p.R;
   uint2 hi[kAhead], lo[kAhead];
   float dg[kAhead];
+  float4 dc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if constexpr (STAGE == kPoly) dc = *reinterpret_cast<const float4*>(gram_diag + (cols_in ? n : 0));
   auto ahead = [&](int first) {  // of rows first + k kStep; those past the end read the first row, columns the first ones
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
@@ -344,7 +351,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
       if constexpr (STAGE != kGram) hi[k] = *reinterpret_cast<const uint2*>(at);
       if constexpr (!SYM || (STAGE == kPoly && TERMS == 2))
         lo[k] = IsPaired<T>::value ? *reinterpret_cast<const uint2*>(at + st.in.plane) : load_once(at + st.in.plane);
-      if constexpr (!SYM) dg[k] = diag[m < p.M ? m : m0];
+      if constexpr (STAGE != kGram) dg[k] = (STAGE == kPoly ? gram_diag : diag)[m < p.M ? m : m0];
     }
   };
   if constexpr (kEarly) ahead(m0 + r0);
@@ -397,9 +404,19 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
         for (int e = 0; e < 4; ++e) {
           if constexpr (STAGE == kGram) {
             v[e] = z[e] * (kGScale / (kXScale * kXScale));
+            if (m == n + e) {
+              gram_diag[m] = v[e] * (1.0f / kGScale);
+              v[e] = 0.0f;
+            }
           } else if constexpr (STAGE == kPoly) {
-            const float g = TERMS == 2 ? h[e] + l[e] : h[e];
-            v[e] = __builtin_fmaf(st.b, g, st.c * (z[e] * (1.0f / kGScale)));
+            // A = E + D with E off the diagonal: A^2 = E^2 + D E + E D + D^2
+            float g = TERMS == 2 ? h[e] + l[e] : h[e];
+            float sq = __builtin_fmaf(g, dg[k] + (e == 0 ? dc.x : e == 1 ? dc.y : e == 2 ? dc.z : dc.w), z[e] * (1.0f / kGScale));
+            if (m == n + e) {
+              g = kGScale * dg[k];
+              sq = __builtin_fmaf(g, dg[k], sq);
+            }
+            v[e] = __builtin_fmaf(st.b, g, st.c * sq);
             if (m == n + e) {
               diag[m] = v[e] * (1.0f / kGScale);
               v[e] = 0.0f;
@@ -517,7 +534,7 @@ struct NewtonPlan {
   int m, n;           // padded
   int terms, blocks;  // fp16 terms of products; workgroups of the norm per matrix
   int shape[2];       // tile shapes of the symmetric products (A and P alike) and of P X
-  size_t xa, xb, gram, poly, diag, parts, bytes;
+  size_t xa, xb, gram, poly, gram_diag, diag, parts, bytes;
 };
 const Rates& rates_of(const NewtonPlan& p, bool sym, int shape) {
   return sym ? kSymRates[p.terms - 1][shape] : kApplyRates[p.terms - 1][std::min(shape, kShapes - 2)];
@@ -553,6 +570,7 @@ NewtonPlan newton_plan(int64_t B, int R, int K, moe_dtype o_t) {
   p.xb = o; o = up256(o + 2 * x);
   p.gram = o; o = up256(o + p.terms * s);
   p.poly = o; o = up256(o + p.terms * s);
+  p.gram_diag = o; o = up256(o + (size_t)B * p.m * 4);
   p.diag = o; o = up256(o + (size_t)B * p.m * 4);
   p.parts = o; o = up256(o + (size_t)B * p.blocks * 8);
   p.bytes = o;
@@ -621,6 +639,7 @@ moe_status launch_orthogonalize(const void* g, moe_dtype g_t, float* momentum, d
   st.mats.sa = 1u << 4;
   st.mats.sb = 1u << 2;
   st.mats.M = pl.m;
+  st.gram_diag = reinterpret_cast<float*>(base + pl.gram_diag);
   st.diag = reinterpret_cast<float*>(base + pl.diag);
   st.o = o;
   st.o_bf16 = o_t == MOE_BF16;
