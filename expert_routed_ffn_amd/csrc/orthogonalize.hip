@@ -3,8 +3,10 @@
 // which takes each singular value s of X to a s + b s^3 + c s^5 and leaves the singular vectors as they are.
 //
 // Products run on v_mfma_f32_16x16x32_f16.  fp16 holds 11 bits where bf16 holds 8, and its range is enough: X, A and P of a
-// normalised matrix stay within a few units, and are stored times 2^13, 2^12 and 2^12, so that what lies below fp16's
-// normal range is below 2^-26 of the largest value.
+// normalised matrix stay within a few units, and are stored times 2^13, 2^12 and 2^11, so that what lies below fp16's
+// normal range is below 2^-25 of the largest value.  X's singular values below 4 and P's eigenvalues below 16, as the call asks for,
+// leave X's values below 4, P's below 16, and A's off its diagonal at no more than 8 (A has no negative eigenvalue), all
+// at about half of fp16's largest value.
 //
 // What the roundings do: a step multiplies a small singular value by a = 3.44, five of them by 485, and noise beside
 // it as much, so X rounded to 11 bits before each step leaves results of low-rank gradients 1 to 7% off, and bf16 20%
@@ -47,7 +49,7 @@ using Nano = Paired<Tile<32, 32, 2, 2>, 3>;  // symmetric products
 using Flat = Paired<Tile<32, 64, 2, 2>, 3>;  // P X
 using Wide = Paired<Tile<64, 64, 2, 2, 3, 2>, 3>;
 
-constexpr float kXScale = 8192.0f, kGScale = 4096.0f;  // of X; of A and P
+constexpr float kXScale = 8192.0f, kGScale = 4096.0f, kPScale = 2048.0f;  // of X, A and P
 
 __device__ __forceinline__ uint16_t f32_to_f16(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
 __device__ __forceinline__ float f16_to_f32(uint32_t h) { return (float)__builtin_bit_cast(_Float16, (uint16_t)h); }
@@ -285,7 +287,7 @@ struct Step {
   Planes in, out;           // kPoly: A -> P;  kApply: X -> X;  kGram: -> A;  kLast: X
   float* gram_diag;         // [matrix][M] A's diagonal (0 in its planes): written by kGram, read by kPoly
   float* diag;              // [matrix][M] P's diagonal (0 in its planes): written by kPoly, read by kApply and kLast
-  float a, b, c;
+  float a, b, c;            // b and c take A's scale to P's
   void* o;                  // kLast: [matrix][rows][cols], where X is [cols][rows] if `turned`
   int o_bf16, turned, rows, cols;
 };
@@ -418,12 +420,12 @@ __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st)
             }
             v[e] = __builtin_fmaf(st.b, g, st.c * sq);
             if (m == n + e) {
-              diag[m] = v[e] * (1.0f / kGScale);
+              diag[m] = v[e] * (1.0f / kPScale);
               v[e] = 0.0f;
             }
           } else {
             const float x = h[e] + l[e], by = TERMS == 2 ? x : h[e];
-            v[e] = __builtin_fmaf(st.a, x, __builtin_fmaf(dg[k], by, z[e] * (1.0f / kGScale)));
+            v[e] = __builtin_fmaf(st.a, x, __builtin_fmaf(dg[k], by, z[e] * (1.0f / kPScale)));
           }
         }
         if constexpr (STAGE == kLast) {
@@ -661,8 +663,8 @@ moe_status launch_orthogonalize(const void* g, moe_dtype g_t, float* momentum, d
   const bool past = (size_t)B * xs * 8 > kKept;
   for (int i = 0; i < steps; ++i) {
     st.a = coef[3 * i];
-    st.b = coef[3 * i + 1];
-    st.c = coef[3 * i + 2];
+    st.b = coef[3 * i + 1] * (kPScale / kGScale);
+    st.c = coef[3 * i + 2] * (kPScale / kGScale);
     operands(x, pl.n, x, pl.n, pl.m, pl.n);
     st.in = gram;  // (not read)
     st.out = gram;

@@ -7,7 +7,8 @@ d |ref| + |half steps|; and the way from a value to the nearest bf16 changes by 
 import pytest
 import torch
 
-from tests._newton_ref import coefs, newton64
+from tests._newton_ref import coefs, newton64, newton_bound
+from tests._train_ref import HALF
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
@@ -101,3 +102,41 @@ def test_single_values(moe, i, x, j, y):
     o = moe.orthogonalize(u.cuda(), eps=0.0).cpu()
     _rounded(o, newton64(u, eps=0.0), 2e-2)
     assert not o[u == 0].any()
+
+
+# ---- the ends of the documented range --------------------------------------------------------
+
+@pytest.mark.parametrize("o_dtype", [BF16, F32])
+@pytest.mark.parametrize("top", [3.9994, 3.9999])
+def test_singular_values_just_below_4(moe, top, o_dtype):
+    """A holds their squares, to 15.9992, on its diagonal."""
+    d = torch.tensor([1.0, 0.9, 0.5, 0.1])
+    u = torch.zeros((70, 90))
+    u[[3, 68, 41, 17], [89, 2, 40, 64]] = d
+    n = float(d.double().norm())
+    coef = [(top * n, 0.0, 0.0), (0.1, -0.005, 0.0)]  # the largest value, 1 / n, becomes top
+    o = moe.orthogonalize(u.cuda(), steps=2, coef=coef, eps=0.0, o_dtype=o_dtype).cpu()
+    ref = newton64(u, steps=2, coef=coef, eps=0.0)
+    most = newton_bound(u, o_dtype, steps=2, coef=coef, eps=0.0) * (1 + HALF[o_dtype]) + HALF[o_dtype] * ref.norm()
+    assert (o.double() - ref).norm() <= most
+    assert int((o != 0).sum()) == 4
+
+
+@pytest.mark.parametrize("o_dtype", [BF16, F32])
+def test_a_polynomial_just_below_16_off_the_diagonal(moe, o_dtype):
+    """Singular values 0.12 and 0.06 along (1, 1) and (1, -1) of two rows, where b s^2 + c s^4 is 15.998 and -15.998: b A + c A^2 then
+    holds 15.998 off its diagonal alone."""
+    top = 15.998
+    s, t = 0.12, 0.06
+    c = (top + top * (s / t) ** 2) / (s ** 4 - s ** 2 * t ** 2)
+    b = (-top - c * t ** 4) / t ** 2
+    u = torch.zeros((70, 90), dtype=torch.float64)
+    u[[5, 66], 80] = s / 2 ** 0.5
+    u[5, 7], u[66, 7] = t / 2 ** 0.5, -t / 2 ** 0.5
+    coef, eps = [(17.0, b, c)], 1.0 - (s * s + t * t) ** 0.5  # |u| + eps is 1
+    u = u.float()
+    o = moe.orthogonalize(u.cuda(), steps=1, coef=coef, eps=eps, o_dtype=o_dtype).cpu()
+    ref = newton64(u, steps=1, coef=coef, eps=eps)
+    assert abs(ref.norm() - ((33 * s) ** 2 + t ** 2) ** 0.5) < 0.02
+    most = newton_bound(u, o_dtype, steps=1, coef=coef, eps=eps) * (1 + HALF[o_dtype]) + HALF[o_dtype] * ref.norm()
+    assert (o.double() - ref).norm() <= most
