@@ -18,11 +18,11 @@ __device__ __forceinline__ float update_of(const Update& u, float g, float m) {
   return !u.moment ? g : u.nesterov ? __builtin_fmaf(u.beta, m, u.rest * g) : m;
 }
 
-// 1 / (norm + eps) from the sum of squares: 0 for a zero matrix, which stays zero, and NaN for one with an infinity or a
-// NaN, which becomes NaN throughout.
+// 1 / (norm + eps) from the sum of squares (which are 0 in 64 bits for zeros alone): 0 for a zero matrix, which stays zero
+// however small eps is, and NaN for one with an infinity or a NaN, which becomes NaN throughout.
 __device__ __forceinline__ double inverse_norm(double squares, double eps) {
   const double total = sqrt(squares) + eps;
-  return total == 0.0 ? 0.0 : total < __builtin_huge_val() ? 1.0 / total : __builtin_nan("");
+  return squares == 0.0 ? 0.0 : total < __builtin_huge_val() ? 1.0 / total : __builtin_nan("");
 }
 
 // Four values of u from row r, column k on; zeros past the matrix.  MOMENT: the moment is brought up to date on the way.

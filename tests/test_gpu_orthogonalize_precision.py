@@ -140,3 +140,17 @@ def test_a_polynomial_just_below_16_off_the_diagonal(moe, o_dtype):
     assert abs(ref.norm() - ((33 * s) ** 2 + t ** 2) ** 0.5) < 0.02
     most = newton_bound(u, o_dtype, steps=1, coef=coef, eps=eps) * (1 + HALF[o_dtype]) + HALF[o_dtype] * ref.norm()
     assert (o.double() - ref).norm() <= most
+
+
+@pytest.mark.parametrize("R,K", [(40, 70), (70, 90)])
+@pytest.mark.parametrize("o_dtype", [BF16, F32])
+def test_zeros_with_the_smallest_eps(moe, R, K, o_dtype):
+    """1 / eps is past the range of 64 bits below 5.6e-309, and 2^13 / eps below 4.6e-305."""
+    u = torch.zeros((3, R, K))
+    u[1] = torch.randn((R, K), generator=_gen(R)) * 1e-40
+    want = moe.orthogonalize(u.cuda(), eps=0.0, o_dtype=o_dtype)
+    assert want[1].isfinite().all() and want[1].any()
+    for eps in (1e-300, 1e-306, 1e-310, 5e-324):
+        o = moe.orthogonalize(u.cuda(), eps=eps, o_dtype=o_dtype)
+        assert not o[0].any() and not o[2].any(), eps
+        assert torch.equal(o[1], want[1]), eps
