@@ -9,6 +9,7 @@ import torch
 
 from tests._newton_ref import coefs, newton64, newton_bound
 from tests._train_ref import HALF
+from tests.test_gpu_orthogonalize import FORMS
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
@@ -154,3 +155,39 @@ def test_zeros_with_the_smallest_eps(moe, R, K, o_dtype):
         o = moe.orthogonalize(u.cuda(), eps=eps, o_dtype=o_dtype)
         assert not o[0].any() and not o[2].any(), eps
         assert torch.equal(o[1], want[1]), eps
+
+
+# ---- every form ------------------------------------------------------------------------------
+
+def _newton64_gpu(u):
+    """newton64 of a batch, with the usual coefficients, by 64-bit products on the GPU."""
+    x = u.double()
+    x = x / (x.flatten(1).norm(dim=1)[:, None, None] + 1e-7)
+    tall = x.shape[1] > x.shape[2]
+    x = x.mT.contiguous() if tall else x
+    for a, b, c in coefs(None, 5):
+        gram = torch.bmm(x, x.mT.contiguous())
+        x = a * x + torch.bmm(b * gram + c * torch.bmm(gram, gram), x)
+    return x.mT.contiguous() if tall else x
+
+
+# What reaches every kernel of a bf16 result above a short side of 64: forms as in test_gpu_orthogonalize.py, and whether X
+# is past the caches (over 8 bytes a padded value and 256 MB).
+BF16_FORMS = [(B, R, K) for B, R, K, o_dtype, *form in FORMS if o_dtype == BF16 and form[0]] + [
+    (48, 512, 2048), (100, 256, 2048), (1000, 130, 130)]
+
+
+@pytest.mark.parametrize("B,R,K", BF16_FORMS)
+@pytest.mark.parametrize("kind", ["strong over noise", "low rank"])
+def test_strong_and_low_rank_in_every_form(moe, B, R, K, kind):
+    """What X's second term is for: rounded to 11 bits before each step these come out 3 to 7% off, as what is weak grows 485-fold
+    and the rounding's noise with it."""
+    g = torch.Generator(device="cuda").manual_seed(R + K)
+    r = 3 if kind == "strong over noise" else 2
+    left, right = (torch.randn(s, generator=g, device="cuda") for s in ((B, R, r), (B, r, K)))
+    u = torch.bmm(left, right)
+    if kind == "strong over noise":
+        u += 0.01 * torch.randn((B, R, K), generator=g, device="cuda")
+    o = moe.orthogonalize(u)
+    for b in {0, B // 2, B - 1}:
+        _rounded(o[b], _newton64_gpu(u[b:b + 1])[0], 2e-3, f"matrix {b}")
