@@ -45,7 +45,7 @@ def _dense(R, K, kind, seed):
 
 
 # the shorter side around 16, 32, 48 and 64 (sums on the shorter side up to there), the longer one around stretches of 64 and
-# the 16 workgroups that share them
+# the 32 workgroups that share them (a stretch each; more are in test_gpu_orthogonalize_moment.py)
 SIZES = [(15, 17), (17, 100), (33, 49), (48, 1025), (49, 64), (64, 1024), (2000, 60), (1, 1), (1, 50), (50, 1), (3, 5), (16, 16), (60, 137), (64, 64), (65, 63), (129, 40), (100, 300), (257, 200), (200, 321)]
 
 

@@ -73,3 +73,24 @@ def test_gradients_above_a_short_side_of_64(moe, R, K, gt):
     u = _gradients(1, R, K, 3)[0].to(gt)
     for o_dtype in (BF16, F32):
         _near(moe.orthogonalize(u.cuda(), o_dtype=o_dtype), u.float(), o_dtype)
+
+
+# A short side up to 64 and a long one whose stretches of 64 are more than the 32 workgroups that share a Gram matrix, so that
+# a workgroup brings several: 33 stretches (the last of one column) are 16 workgroups of two and one of one, 65 are 21 of three
+# and one of two, 66 are 22 of three, 256 are 32 of eight
+LONG = [(60, 2049), (2049, 60), (33, 4100), (4161, 17), (64, 16384), (16384, 1), (48, 6145)]
+
+
+@pytest.mark.parametrize("R,K", LONG)
+@pytest.mark.parametrize("o_dtype", [BF16, F32])
+def test_long_sides_beside_short_ones(moe, R, K, o_dtype):
+    u = _gradients(2, R, K, R + K)
+    o = moe.orthogonalize(u.cuda(), o_dtype=o_dtype)
+    for b in range(2):
+        _near(o[b], u[b], o_dtype)
+
+
+@pytest.mark.parametrize("R,K", LONG)
+@pytest.mark.parametrize("gt,o_dtype,nesterov", [(F32, BF16, True), (BF16, F32, False)])
+def test_momentum_of_long_sides_beside_short_ones(moe, R, K, gt, o_dtype, nesterov):
+    _check_momentum(moe, 3, R, K, gt, o_dtype, nesterov)
