@@ -83,7 +83,6 @@ struct Eight<false> {
   __device__ __forceinline__ void load(const void* x, size_t i) {
     q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(x) + i);
   }
-  __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -100,7 +99,6 @@ struct Eight<true> {
     a = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(x) + i);
     b = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(x) + i + 4);
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
