@@ -294,10 +294,10 @@ struct Step {
 
 // One tile of one matrix.  SYM stages compute the tiles on and above the diagonal.
 //
-// What bounds it, per launch: for one 4,096 x 4,096 matrix the matrix units (A 73 us and P 75 on 192 x 192 tiles, 22 x 23 / 2
-// of them in one round, 1.05 PFLOP/s; P X 122 us, 1.13 PFLOP/s) and the epilogue behind them; for 48 of 512 x 2,048 memory in
-// P X (X's terms in and out, 409 MB or more in 105 us) and the tiles' loads out of the L2 in A (45 us, 480 tiles of which each
-// brings 32 KB per K-step); for one of 512 x 2,048 latency (A 6.5 us, P 3.5, P X 5.5, of 17 launches in a row).
+// What bounds it, per launch: for one 4,096 x 4,096 matrix the matrix units (A 73 to 77 us and P 75 to 79 on 192 x 192 tiles,
+// 22 x 23 / 2 of them in one round, 0.95 to 1.05 PFLOP/s; P X 122 to 127 us, 1.13 PFLOP/s) and the epilogue behind them; for 48 of
+// 512 x 2,048 memory in P X (X's terms in and out, 409 MB or more in 106 us) and the tiles' loads out of the L2 in A (46 us,
+// 480 tiles of which each brings 32 KB per K-step); for one of 512 x 2,048 latency (A 6.6 us, P 3.6, P X 5.5, of 17 launches in a row).
 template <typename T, int STAGE, int TERMS>
 __global__ __launch_bounds__(T::kThreads, 2) void newton_product_kernel(Step st) {
   constexpr bool SYM = STAGE == kGram || STAGE == kPoly;
