@@ -9,7 +9,7 @@ import torch
 
 from tests._newton_ref import coefs, newton64, newton_bound
 from tests._train_ref import HALF
-from tests.test_gpu_orthogonalize import FORMS
+from tests.test_gpu_orthogonalize import FORMS, _check_spread
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
@@ -191,3 +191,10 @@ def test_strong_and_low_rank_in_every_form(moe, B, R, K, kind):
     o = moe.orthogonalize(u)
     for b in {0, B // 2, B - 1}:
         _rounded(o[b], _newton64_gpu(u[b:b + 1])[0], 2e-3, f"matrix {b}")
+
+
+@pytest.mark.parametrize("R,K", [(16384, 16384), (65, 16384), (16384, 65), (16384, 8000)])
+@pytest.mark.parametrize("o_dtype", [BF16, F32])
+def test_longest_sides(moe, R, K, o_dtype):
+    """Values at every place, one in each row and column of the shorter side (their bounds are in _newton_ref.scalar_bound)."""
+    _check_spread(moe, 1, R, K, o_dtype, seed=R + K)
