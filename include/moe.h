@@ -535,14 +535,15 @@ moe_status moe_linear_backward_form(int T, int K, int N, moe_act act, moe_dtype 
  *   ws        moe_orthogonalize_workspace_bytes(B, R, K, o_t) bytes, 256-byte aligned (0 for sizes and types that the call
  *             refuses, and for B == 0).
  * momentum, o and ws may not overlap g or each other.  With R and K rounded up to multiples of 64, B * R * K <= 2^33.
- * The norm's sum is 64-bit, all others are fp32 or more.  A bf16 o comes from products of fp16 terms with 11 bits, X held
- * with 22 and the diagonals of A and b A + c A A in fp32.  Before its rounding it is off, with the usual coefficients, by up to
- * 2e-3 of its norm where the singular vectors spread over many entries (3e-3 if all singular values are equal), and up to 2e-2 where
- * rows and columns hold one value each, whose roundings add up; with R or K up to 64 by up to 1e-3.  An fp32 o comes from products of
- * 22-bit terms, as near as fp32 arithmetic.  X is held to multiples of 2^-37, so of a u far smaller than eps (|u| < 1e-4 eps), whose o is as
- * small, fewer digits are right.
- * A matrix of zeros gives zeros when eps == 0, too; one whose u has an infinity or a NaN gives NaN throughout; neither touches the
- * batch's other matrices.  The same bits for the same inputs every time.
+ * The norm's sum is 64-bit, all others are fp32 or more.  A bf16 o comes from products of fp16 terms with 11 bits, X
+ * held with 22 and the diagonals of A and b A + c A A in fp32.  Before its rounding it is off, with the usual
+ * coefficients, by up to 2e-3 of its norm where the singular vectors spread over many entries (3e-3 if all singular
+ * values are equal), by up to 2e-2 where rows and columns hold one value each, whose roundings add up, and by up to 1e-3
+ * with R or K up to 64.  An fp32 o comes from products of 22-bit terms, as near as fp32 arithmetic.
+ * X is held to multiples of 2^-37, so of a u far smaller than eps (|u| < 1e-4 eps), whose o is as small, fewer digits
+ * are right.
+ * A matrix of zeros gives zeros whatever eps is; one whose u has an infinity or a NaN gives NaN throughout; neither
+ * touches the batch's other matrices.  The same bits for the same inputs every time.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE.
  */
 size_t moe_orthogonalize_workspace_bytes(int B, int R, int K, moe_dtype o_t);
