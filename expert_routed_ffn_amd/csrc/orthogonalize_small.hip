@@ -11,7 +11,7 @@
 // steps have 3.44 each.  A is therefore summed in 64 bits, and steps run in 64 bits until A's rounding to fp32 grows by no
 // more than 144 in the steps that are left, and what the first fp32 step adds by no more than 16 in those behind it: two of five for
 // a bf16 result, all for an fp32 one.  On matrices of one or a few strong directions over noise of 0.01 to 1 of them, sides 8
-// to 64, a bf16 result was then off by 7e-4 of its norm at most before its rounding (1.66e-3); with the first step alone in 64 bits
+// to 64, a bf16 result was then off by 8e-4 of its norm at most before its rounding (1.66e-3); with the first step alone in 64 bits
 // by 6e-3, with none by 6e-2; with three by 1.1e-4, 3 us slower.  (The bound of 16 alone lets the fp32 steps begin with one of
 // any a: with a = 15 there results were 5e-3 to 2.6e-2 off.  Tiles are stored on both sides of the diagonal, so products that should
 // commute leave their noise on A.)  Coefficients whose growth 64 bits do not hold go the way of orthogonalize.hip.
